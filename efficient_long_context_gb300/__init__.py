@@ -30,6 +30,12 @@ from ._binding import (  # noqa: F401
     orthros_prefill_workspace_size,
     orthros_profile_begin,
     orthros_qkv_project,
+    orthros_rotary_frequencies,
+    orthros_rotary_steps,
+    orthros_rotate,
+    orthros_rotate_append,
+    orthros_rotate_backward,
+    orthros_rotate_backward_workspace_size,
     orthros_selftest_wait_timeout,
     orthros_profile_end,
     orthros_status_string,

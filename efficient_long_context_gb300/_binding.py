@@ -26,7 +26,9 @@ EXPORTS = ("orthros_prefill_workspace_size", "orthros_prefill", "orthros_prefill
            "orthros_prefill_shard", "orthros_merge_partials", "orthros_prefill_backward_workspace_size",
            "orthros_prefill_backward", "orthros_extend_workspace_size", "orthros_extend", "orthros_qkv_project",
            "orthros_decode_workspace_size",
-           "orthros_decode", "orthros_decode_static", "orthros_check", "orthros_profile_begin", "orthros_profile_end",
+           "orthros_decode", "orthros_decode_static", "orthros_rotary_frequencies", "orthros_rotary_steps",
+           "orthros_rotate", "orthros_rotate_backward_workspace_size", "orthros_rotate_backward",
+           "orthros_rotate_append", "orthros_check", "orthros_profile_begin", "orthros_profile_end",
            "orthros_selftest_wait_timeout", "orthros_status_string", "orthros_last_error")
 
 
@@ -104,6 +106,23 @@ def load_library(path: str | None = None):
         lib.orthros_decode_static.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp,
                                               vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float, i32,
                                               vp, vp, vp, vp, vp]
+        ll, f32, f64, u64 = ctypes.c_longlong, ctypes.c_float, ctypes.c_double, ctypes.c_uint64
+        lib.orthros_rotary_frequencies.restype = i32
+        lib.orthros_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64),
+                                                   ctypes.POINTER(f32)]
+        lib.orthros_rotary_steps.restype = i32
+        lib.orthros_rotary_steps.argtypes = [ctypes.POINTER(f64), i32, ctypes.POINTER(u64)]
+        lib.orthros_rotate.restype = i32
+        lib.orthros_rotate.argtypes = [vp, ll, vp, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, vp, ll, vp]
+        lib.orthros_rotate_backward_workspace_size.restype = sz
+        lib.orthros_rotate_backward_workspace_size.argtypes = [i32] * 4
+        lib.orthros_rotate_backward.restype = i32
+        lib.orthros_rotate_backward.argtypes = [vp, ll, vp, ll, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, vp, ll,
+                                                vp, vp, vp, sz, vp]
+        lib.orthros_rotate_append.restype = i32
+        lib.orthros_rotate_append.argtypes = [vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, i32, i32, f32, vp, vp,
+                                              vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                              vp, sz, vp]
         lib.orthros_selftest_wait_timeout.restype = i32
         lib.orthros_selftest_wait_timeout.argtypes = [ctypes.c_longlong, vp, sz, vp]
         lib.orthros_check.restype = i32
@@ -530,6 +549,178 @@ def orthros_decode_static(q, k_new, v_new, k_cache, v_cache, block_table, cache_
         _ptr(o_base), _ptr(lse_base), _ptr(o_out), _ptr(lse_out), _stream(stream))
     _raise_if(rc, lib)
     return o_base, lse_base, o_out, lse_out
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "stretch": 2, "bands": 3, "bands_tempered": 4}
+
+
+def _rope_layout(layout) -> int:
+    if layout not in _ROPE_LAYOUTS:
+        raise OrthrosError(1, f"rotary layout {layout!r}: one of {sorted(_ROPE_LAYOUTS)}")
+    return _ROPE_LAYOUTS[layout]
+
+
+def _token_rows(name, t):
+    """Elements between the tokens of t [n, heads, d], whose tokens' heads must be contiguous."""
+    n, H, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+        raise OrthrosError(1, f"{name}: the heads of a token must be contiguous")
+    return int(t.stride(0)) if n > 1 else H * d
+
+
+def _index(name, t, n):
+    """A contiguous int32 index tensor of n entries."""
+    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
+        raise OrthrosError(1, f"{name} must be a contiguous int32 tensor of {n} entries")
+    return t
+
+
+def _affine(name, t, H, d):
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (H, d)):
+        raise OrthrosError(1, f"{name} must be a contiguous float32 [{H}, {d}] tensor")
+    return t
+
+
+def _same_type(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise OrthrosError(1, f"{name} is {t.dtype}, not {dtype}")
+
+
+def _steps(t):
+    if t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous():
+        raise OrthrosError(1, "steps must be a contiguous int64 vector (orthros_rotary_steps)")
+    return t
+
+
+def orthros_rotary_frequencies(rot_dim, base, scaling="plain", *, factor=1.0, original_length=0.0, low_turns=1.0,
+                               high_turns=4.0):
+    """orthros_rotary_frequencies of include/orthros_attn.h: (freq float64 [rot_dim/2] CPU tensor, amplitude)
+    of a scaling rule ("plain", "linear", "stretch", "bands", "bands_tempered")."""
+    lib = load_library()
+    if scaling not in _ROPE_SCALINGS:
+        raise OrthrosError(1, f"scaling {scaling!r}: one of {sorted(_ROPE_SCALINGS)}")
+    freq = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    amp = ctypes.c_float(0.0)
+    rc = lib.orthros_rotary_frequencies(int(rot_dim), float(base), _ROPE_SCALINGS[scaling], float(factor),
+                                        float(original_length), float(low_turns), float(high_turns),
+                                        freq.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), ctypes.byref(amp))
+    _raise_if(rc, lib)
+    return torch.from_numpy(freq), float(amp.value)
+
+
+def orthros_rotary_steps(freq):
+    """orthros_rotary_steps of include/orthros_attn.h: frequencies (radians per
+    position) -> int64 CPU tensor holding the 64-bit steps; move it to the GPU once."""
+    lib = load_library()
+    f = freq.detach().cpu().numpy() if isinstance(freq, torch.Tensor) else freq
+    f = np.ascontiguousarray(np.asarray(f, dtype=np.float64).ravel())
+    steps = np.zeros(f.size, dtype=np.uint64)
+    rc = lib.orthros_rotary_steps(f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), int(f.size),
+                                  steps.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)))
+    _raise_if(rc, lib)
+    return torch.from_numpy(steps.view(np.int64))
+
+
+def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=None, beta=None, out=None, stream=None):
+    """orthros_rotate of include/orthros_attn.h: y = amplitude R(t) (alpha (.) x + beta).
+
+    x [n, H, d] (any token stride), positions [n] int32, steps from
+    orthros_rotary_steps on the GPU. Returns y [n, H, d] (`out` may be x).
+    """
+    lib = load_library()
+    n, H, d = x.shape
+    if out is None:
+        out = torch.empty((n, H, d), dtype=x.dtype, device=x.device)
+    if tuple(out.shape) != (n, H, d):
+        raise OrthrosError(1, f"out has shape {tuple(out.shape)}, not {(n, H, d)}")
+    _same_type(x.dtype, out=out)
+    rc = lib.orthros_rotate(_ptr(x), _token_rows("x", x), _ptr(_index("positions", positions, n)),
+                            _ptr(_affine("alpha", alpha, H, d)), _ptr(_affine("beta", beta, H, d)), _ptr(_steps(steps)),
+                            2 * steps.numel(), _rope_layout(layout), float(amplitude), n, H, d, _dtype(x), _ptr(out),
+                            _token_rows("out", out), _stream(stream))
+    _raise_if(rc, lib)
+    return out
+
+
+def orthros_rotate_backward_workspace_size(n, H, d, dtype=torch.bfloat16) -> int:
+    return int(load_library().orthros_rotate_backward_workspace_size(n, H, d, _DTYPES[dtype]))
+
+
+def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude=1.0, alpha=None, affine_grads=True,
+                            out=None, workspace=None, stream=None):
+    """orthros_rotate_backward of include/orthros_attn.h.
+
+    dy, x [n, H, d] (any token strides; x may be None without affine_grads).
+    Returns (dx, d_alpha, d_beta), the last two float [H, d], or None without
+    affine_grads; `out` gives the three tensors.
+    """
+    lib = load_library()
+    n, H, d = dy.shape
+    if out is None:
+        out = (torch.empty((n, H, d), dtype=dy.dtype, device=dy.device),
+               torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None,
+               torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None)
+    dx, da, db = out
+    if tuple(dx.shape) != (n, H, d) or (x is not None and tuple(x.shape) != (n, H, d)):
+        raise OrthrosError(1, f"x and dx must have the shape of dy, {(n, H, d)}")
+    _same_type(dy.dtype, x=x, dx=dx)
+    if workspace is None and da is not None:
+        workspace = torch.empty(max(orthros_rotate_backward_workspace_size(n, H, d, dy.dtype), 256),
+                                dtype=torch.uint8, device=dy.device)
+    rc = lib.orthros_rotate_backward(
+        _ptr(dy), _token_rows("dy", dy), _ptr(x), _token_rows("x", x) if x is not None else 0,
+        _ptr(_index("positions", positions, n)), _ptr(_affine("alpha", alpha, H, d)), _ptr(_steps(steps)),
+        2 * steps.numel(), _rope_layout(layout), float(amplitude), n, H, d, _dtype(dy), _ptr(dx),
+        _token_rows("dx", dx), _ptr(_affine("d_alpha", da, H, d)), _ptr(_affine("d_beta", db, H, d)), _ptr(workspace),
+        workspace.numel() if workspace is not None else 0, _stream(stream))
+    _raise_if(rc, lib)
+    return dx, da, db
+
+
+def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_seq, token_pos, steps, *,
+                          layout="half", amplitude=1.0, q_out=None, out_positions=None, alpha_base=None,
+                          beta_base=None, alpha_out=None, beta_out=None, out=None, workspace=None, stream=None):
+    """orthros_rotate_append of include/orthros_attn.h.
+
+    k_new, v_new [n, Hkv, d] go to their page slots (keys rotated); q [n, Hq,
+    d] (or None) and q_out [n_out, Hq, d] are rotated. Returns (q_rot or None,
+    q_out_rot or None); k_cache / v_cache are updated in place.
+    """
+    lib = load_library()
+    n, Hkv, d = k_new.shape
+    n_out = q_out.shape[0] if q_out is not None else 0
+    Hq = q.shape[1] if q is not None else (q_out.shape[1] if q_out is not None else Hkv)
+    num_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    B, max_pages = block_table.shape
+    for name, t, rows, heads in (("q", q, n, Hq), ("q_out", q_out, n_out, Hq), ("v_new", v_new, n, Hkv)):
+        if t is not None and tuple(t.shape) != (rows, heads, d):
+            raise OrthrosError(1, f"{name} has shape {tuple(t.shape)}, not {(rows, heads, d)}")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if tuple(t.shape) != (num_pages, page_size, Hkv, d) or not t.is_contiguous():
+            raise OrthrosError(1, f"{name} must be a contiguous [{num_pages}, {page_size}, {Hkv}, {d}] tensor")
+    _same_type(k_new.dtype, q=q, q_out=q_out, v_new=v_new, k_cache=k_cache, v_cache=v_cache)
+    if out is None:
+        out = (torch.empty((n, Hq, d), dtype=q.dtype, device=q.device) if q is not None else None,
+               torch.empty((n_out, Hq, d), dtype=q_out.dtype, device=q_out.device) if q_out is not None else None)
+    q_rot, q_out_rot = out
+    for name, t in (("q_rot", q_rot), ("q_out_rot", q_out_rot)):
+        _contig(name, t)
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=k_new.device)
+    rc = lib.orthros_rotate_append(
+        _ptr(q), _token_rows("q", q) if q is not None else 0, _ptr(q_out),
+        _token_rows("q_out", q_out) if q_out is not None else 0, _ptr(k_new), _token_rows("k_new", k_new), _ptr(v_new),
+        _token_rows("v_new", v_new), _ptr(_affine("alpha_base", alpha_base, Hq, d)),
+        _ptr(_affine("beta_base", beta_base, Hq, d)), _ptr(_affine("alpha_out", alpha_out, Hq, d)),
+        _ptr(_affine("beta_out", beta_out, Hq, d)), _ptr(_steps(steps)), 2 * steps.numel(), _rope_layout(layout),
+        float(amplitude), _ptr(_index("token_seq", token_seq, n)), _ptr(_index("token_pos", token_pos, n)),
+        _ptr(_index("out_positions", out_positions, n_out)), n, n_out, Hq, Hkv, d, _dtype(k_new), _ptr(q_rot),
+        _ptr(q_out_rot), _ptr(k_cache), _ptr(v_cache), _ptr(_index("block_table", block_table, B * max_pages)), B,
+        max_pages, page_size, num_pages, _ptr(workspace), workspace.numel(), _stream(stream))
+    _raise_if(rc, lib)
+    return q_rot, q_out_rot
 
 
 def orthros_selftest_wait_timeout(limit_cycles, workspace, stream=None):

@@ -86,6 +86,10 @@ enum RowKind { kPrefillBase = 0, kPrefillOut = 1, kDecodePair = 2, kExtendBase =
 // orthros_api.cu: records the message returned by orthros_last_error() and
 // passes the status through.
 orthros_status report_error(orthros_status s, const char *fmt, ...);
+// orthros_api.cu: empties that message (every entry point begins with it).
+void clear_error();
+// orthros_api.cu: SMs of the current device.
+int device_sm_count();
 
 // profile.cu: brackets one kernel launch with CUDA events while profiling is on.
 class ProfScope {
@@ -273,6 +277,53 @@ struct ProjParams {
     uint32_t *status;
 };
 cudaError_t launch_project_tc(const ProjParams &p, cudaStream_t stream);
+
+// rotary.cu: rotary positions (orthros_rotate, _backward, _append).
+struct RotateParams {
+    const void *x;
+    void *y;
+    long long x_stride, y_stride;  // elements between tokens
+    const int32_t *positions;
+    const float *alpha, *beta;  // both null: none
+    const uint64_t *steps;      // [rot / 2]
+    long long n;
+    int H, rot, heads_per_block;  // heads_per_block: set by the launcher
+    bool interleaved;
+    float amplitude;
+};
+struct RotateBwdParams {
+    const void *dy, *x;
+    void *dx;
+    long long dy_stride, x_stride, dx_stride;
+    const int32_t *positions;
+    const float *alpha;
+    const uint64_t *steps;
+    long long n;
+    int H, rot, heads_per_block;
+    bool interleaved;
+    float amplitude;
+    float *partial;  // [n_part, 2, H d] sums of the affine's gradient per block of tokens
+    int n_part;
+    float *d_alpha, *d_beta;  // both null: not wanted
+};
+struct RotateAppendParams {
+    const void *q, *q_out, *k, *v;  // q, q_out may be null
+    long long q_stride, q_out_stride, k_stride, v_stride;
+    const float *alpha_base, *beta_base, *alpha_out, *beta_out;
+    const uint64_t *steps;
+    const int32_t *token_seq, *token_pos, *out_positions, *block_table;
+    int n_new, n_out, Hq, Hkv, rot, heads_per_block;
+    bool interleaved;
+    float amplitude;
+    void *q_rot, *q_out_rot, *k_cache, *v_cache;
+    int B, max_pages, page_size, num_pages;
+    uint32_t *status;
+};
+int rotate_grad_parts(long long n, int H, int d, int elem_bytes);
+cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
+cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
+cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t stream);
+cudaError_t launch_rotate_append(const RotateAppendParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 
 // merge.cu: exact merge of normalised partials over disjoint key sets.
 cudaError_t launch_merge_partials(const float *o_parts, const float *lse_parts, int n_parts, int n_rows, int Hq, int d,

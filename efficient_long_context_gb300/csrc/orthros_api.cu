@@ -847,6 +847,10 @@ orthros_status report_error(orthros_status s, const char *fmt, ...) {
     return s;
 }
 
+void clear_error() { g_last_error.clear(); }
+
+int device_sm_count() { return device_sms(); }
+
 }  // namespace orthros
 
 using namespace orthros;

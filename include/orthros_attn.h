@@ -432,6 +432,140 @@ ORTHROS_API orthros_status orthros_decode_static(
     orthros_stream_t stream);
 
 /*
+ * Rotary positions. The pages leave the positional encoding of the converted
+ * models aside (Alg. 1 projects, applies the stream's affine and attends);
+ * models with rotary positions turn each query and key between those two
+ * steps. Pair i of a head at position t turns by the angle t * freq[i]:
+ *   (y_a, y_b) = amplitude * (u_a cos - u_b sin, u_a sin + u_b cos),
+ * over the first rot_dim channels of the head, paired (i, i + rot_dim/2) in
+ * the half layout or (2i, 2i + 1) in the interleaved one; channels past
+ * rot_dim keep u. The attention calls then take identity affines.
+ */
+typedef enum { ORTHROS_ROPE_HALF = 0, ORTHROS_ROPE_INTERLEAVED = 1 } orthros_rope_layout;
+
+/*
+ * How orthros_rotary_frequencies scales the plain frequencies
+ * f_i = base^(-2i/rot_dim) for contexts `factor` times the original_length a
+ * model was trained on:
+ *   PLAIN    f_i
+ *   LINEAR   f_i / factor (position interpolation)
+ *   STRETCH  base * factor^(rot_dim/(rot_dim-2)) in place of base (the
+ *            "NTK-aware" rule: the highest frequency kept, the lowest divided
+ *            by factor)
+ *   BANDS    by the turns r = original_length * f_i / 2 pi that a frequency
+ *            makes over the original length: f_i / factor below low_turns, f_i
+ *            above high_turns, ((1-s) / factor + s) f_i between, with
+ *            s = (r - low_turns) / (high_turns - low_turns)
+ *   BANDS_TEMPERED  BANDS with amplitude 0.1 ln(factor) + 1 on cos and sin
+ *            (YaRN; the other rules have amplitude 1)
+ */
+typedef enum {
+    ORTHROS_ROPE_PLAIN = 0,
+    ORTHROS_ROPE_LINEAR = 1,
+    ORTHROS_ROPE_STRETCH = 2,
+    ORTHROS_ROPE_BANDS = 3,
+    ORTHROS_ROPE_BANDS_TEMPERED = 4
+} orthros_rope_scaling;
+
+/*
+ * freq HOST [rot_dim/2] double (radians per position) and *amplitude HOST of
+ * a scaling rule. rot_dim even and >= 2 (>= 4 for STRETCH), base > 1, factor
+ * >= 1 (1 for PLAIN is customary; it is not read there); original_length > 0
+ * and 0 <= low_turns < high_turns for the two BANDS rules (not read by the
+ * others).
+ */
+ORTHROS_API orthros_status orthros_rotary_frequencies(int rot_dim, double base, orthros_rope_scaling rule, double factor,
+                                                      double original_length, double low_turns, double high_turns,
+                                                      double *freq, float *amplitude);
+
+/*
+ * freq HOST [n] (radians per position, finite) -> steps HOST [n]: the fraction
+ * of a turn per position in units of 2^-64. The calls below take a device copy
+ * of steps: position times step, modulo 2^64, is the phase at any 32-bit
+ * position without loss, where a float product has lost its fraction.
+ */
+ORTHROS_API orthros_status orthros_rotary_steps(const double *freq, int n, uint64_t *steps);
+
+/*
+ * Rotates n tokens: y = amplitude R(t) u with u = alpha (.) x + beta.
+ *
+ * x, y         [n, H, d]: token i starts x_stride (y_stride) elements after
+ *              token i - 1; the heads of a token are contiguous. Strides are
+ *              multiples of 16 bytes; y_stride >= H d. So slices of a packed
+ *              projection need no copy. y may be x (same stride); the
+ *              elements of x and y must not overlap otherwise.
+ * positions    [n] int32, any value
+ * alpha, beta  [H, d] float (16-byte aligned), or both NULL (u = x)
+ * steps        [rot_dim/2] device copy of orthros_rotary_steps' output
+ * rot_dim      a multiple of 16, 16 <= rot_dim <= d
+ * Computed in fp32 and rounded once to dtype. No workspace, no status word.
+ */
+ORTHROS_API orthros_status orthros_rotate(const void *x, long long x_stride, const int32_t *positions,
+                                          const float *alpha, const float *beta, const uint64_t *steps, int rot_dim,
+                                          orthros_rope_layout layout, float amplitude, int n, int H, int d,
+                                          orthros_dtype dtype, void *y, long long y_stride, orthros_stream_t stream);
+
+/* Workspace bytes orthros_rotate_backward needs for these sizes (0 if rejected). */
+ORTHROS_API size_t orthros_rotate_backward_workspace_size(int n, int H, int d, orthros_dtype dtype);
+
+/*
+ * Gradients of orthros_rotate: with g = amplitude R(-t) dy (g = dy past
+ * rot_dim), dx = alpha (.) g, d_alpha = sum over tokens of g (.) x, d_beta =
+ * sum over tokens of g.
+ *
+ * dy, dx       [n, H, d] with strides as for orthros_rotate; dx may be dy
+ * x, x_stride  the forward's input; read only for d_alpha
+ * alpha        [H, d] float, or NULL (1)
+ * d_alpha, d_beta [H, d] float, overwritten, or both NULL (then x and the
+ *              workspace are not read and may be NULL). The sums run in a fixed
+ *              order: the same call gives the same bits.
+ * workspace    at least orthros_rotate_backward_workspace_size() bytes,
+ *              256-byte aligned; contents on entry do not matter.
+ */
+ORTHROS_API orthros_status orthros_rotate_backward(const void *dy, long long dy_stride, const void *x,
+                                                   long long x_stride, const int32_t *positions, const float *alpha,
+                                                   const uint64_t *steps, int rot_dim, orthros_rope_layout layout,
+                                                   float amplitude, int n, int H, int d, orthros_dtype dtype, void *dx,
+                                                   long long dx_stride, float *d_alpha, float *d_beta,
+                                                   void *workspace, size_t workspace_bytes, orthros_stream_t stream);
+
+/*
+ * Appends new tokens to the paged cache with the rotation applied on the way,
+ * and rotates both query streams in the same call.
+ *   - new token i (sequence token_seq[i], position token_pos[i]): its key
+ *     heads are rotated and written to its page slot (page
+ *     block_table[seq*max_pages + pos/page_size], slot pos % page_size), its
+ *     values are copied there;
+ *   - q_rot[i] = R(token_pos[i]) (alpha_base (.) q[i] + beta_base) (skipped
+ *     when q is NULL);
+ *   - q_out_rot[r] = R(out_positions[r]) (alpha_out (.) q_out[r] + beta_out)
+ *     for the n_out output-stream rows.
+ *
+ * q [n_new, Hq, d], q_out [n_out, Hq, d], k_new, v_new [n_new, Hkv, d], each
+ *              with its token stride in elements (a multiple of 16 bytes), as
+ *              slices of a packed projection have them
+ * alpha_*, beta_* [Hq, d] float, each pair both set or both NULL (identity; as
+ *              after orthros_qkv_project, which applies the affines itself)
+ * token_seq, token_pos [n_new], out_positions [n_out] device int32. No two
+ *              new tokens may share a slot.
+ * steps, rot_dim, layout, amplitude as for orthros_rotate
+ * q_rot [n_new, Hq, d], q_out_rot [n_out, Hq, d], contiguous
+ * k_cache, v_cache [num_pages, page_size, Hkv, d], block_table [B, max_pages]
+ * workspace    at least 256 bytes (status word), 256-byte aligned
+ * A sequence outside [0, B) or a position outside its block table sets
+ * ORTHROS_DEV_BAD_POSITION, a page id outside [0, num_pages)
+ * ORTHROS_DEV_BAD_PAGE; that token's cache write is skipped.
+ */
+ORTHROS_API orthros_status orthros_rotate_append(
+    const void *q, long long q_stride, const void *q_out, long long q_out_stride, const void *k_new, long long k_stride,
+    const void *v_new, long long v_stride, const float *alpha_base, const float *beta_base, const float *alpha_out,
+    const float *beta_out, const uint64_t *steps, int rot_dim, orthros_rope_layout layout, float amplitude,
+    const int32_t *token_seq, const int32_t *token_pos, const int32_t *out_positions, int n_new, int n_out, int Hq,
+    int Hkv, int d, orthros_dtype dtype, void *q_rot, void *q_out_rot, void *k_cache, void *v_cache,
+    const int32_t *block_table, int B, int max_pages, int page_size, int num_pages, void *workspace,
+    size_t workspace_bytes, orthros_stream_t stream);
+
+/*
  * Synchronises `stream`, reads the status word that the last call using
  * `workspace` left there and returns ORTHROS_OK, ORTHROS_EDEVICE (data bits) or
  * ORTHROS_ETIMEOUT (timeout bit). *bits (if not NULL) receives the raw
