@@ -13,6 +13,8 @@ from ._binding import (  # noqa: F401
     lib_path,
     load_library,
     orthros_check,
+    orthros_chunk_attention,
+    orthros_chunk_attention_workspace_size,
     orthros_decode,
     orthros_decode_static,
     orthros_decode_workspace_size,

@@ -28,7 +28,8 @@ EXPORTS = ("orthros_prefill_workspace_size", "orthros_prefill", "orthros_prefill
            "orthros_decode_workspace_size",
            "orthros_decode", "orthros_decode_static", "orthros_rotary_frequencies", "orthros_rotary_steps",
            "orthros_rotate", "orthros_rotate_backward_workspace_size", "orthros_rotate_backward",
-           "orthros_rotate_append", "orthros_check", "orthros_profile_begin", "orthros_profile_end",
+           "orthros_rotate_append", "orthros_chunk_attention_workspace_size", "orthros_chunk_attention",
+           "orthros_check", "orthros_profile_begin", "orthros_profile_end",
            "orthros_selftest_wait_timeout", "orthros_status_string", "orthros_last_error")
 
 
@@ -123,6 +124,11 @@ def load_library(path: str | None = None):
         lib.orthros_rotate_append.argtypes = [vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, i32, i32, f32, vp, vp,
                                               vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                               vp, sz, vp]
+        lib.orthros_chunk_attention_workspace_size.restype = sz
+        lib.orthros_chunk_attention_workspace_size.argtypes = [i32] * 9
+        lib.orthros_chunk_attention.restype = i32
+        lib.orthros_chunk_attention.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32,
+                                                i32, i32, i32, vp, vp, vp, sz, vp]
         lib.orthros_selftest_wait_timeout.restype = i32
         lib.orthros_selftest_wait_timeout.argtypes = [ctypes.c_longlong, vp, sz, vp]
         lib.orthros_check.restype = i32
@@ -721,6 +727,54 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
         max_pages, page_size, num_pages, _ptr(workspace), workspace.numel(), _stream(stream))
     _raise_if(rc, lib)
     return q_rot, q_out_rot
+
+
+def orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size,
+                                           dtype=torch.bfloat16) -> int:
+    return int(load_library().orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size,
+                                                                     _DTYPES[dtype]))
+
+
+def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table, window, scale=None, *, max_new=None,
+                            out=None, workspace=None, stream=None):
+    """orthros_chunk_attention of include/orthros_attn.h on torch CUDA tensors.
+
+    q [n, Hq, d] with the tokens of sequence b at q_indptr[b] .. q_indptr[b+1];
+    q_indptr and kv_lens are int32 tensors on the GPU. max_new bounds the new
+    tokens of a sequence (default n). Returns (o [n, Hq, d], lse [n, Hq]).
+    """
+    lib = load_library()
+    n, Hq, d = q.shape
+    num_pages, page_size, Hkv = k_cache.shape[:3]
+    B, max_pages = block_table.shape
+    if scale is None:
+        scale = d ** -0.5
+    if max_new is None:
+        max_new = n
+    _contig("q", q)
+    if tuple(k_cache.shape) != (num_pages, page_size, Hkv, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise OrthrosError(1, f"k_cache and v_cache must both be [num_pages, page_size, Hkv, {d}]")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _contig(name, t)
+    _same_type(q.dtype, k_cache=k_cache, v_cache=v_cache)
+    if out is None:
+        out = (torch.empty_like(q), torch.empty((n, Hq), dtype=torch.float32, device=q.device))
+    o, lse = out
+    if tuple(o.shape) != (n, Hq, d) or (lse is not None and (tuple(lse.shape) != (n, Hq) or lse.dtype != torch.float32)):
+        raise OrthrosError(1, f"out must be (o {(n, Hq, d)}, lse float32 {(n, Hq)} or None)")
+    _same_type(q.dtype, o=o)
+    for name, t in (("o", o), ("lse", lse)):
+        _contig(name, t)
+    if workspace is None:
+        ws = orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, q.dtype)
+        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=q.device)
+    rc = lib.orthros_chunk_attention(
+        _ptr(q), _ptr(_index("q_indptr", q_indptr, B + 1)), _ptr(_index("kv_lens", kv_lens, B)), _ptr(k_cache),
+        _ptr(v_cache), _ptr(_index("block_table", block_table, B * max_pages)), B, n, int(max_new), Hq, Hkv, d,
+        int(window), float(scale), _dtype(q), max_pages, page_size, num_pages, _ptr(o), _ptr(lse), _ptr(workspace),
+        workspace.numel(), _stream(stream))
+    _raise_if(rc, lib)
+    return o, lse
 
 
 def orthros_selftest_wait_timeout(limit_cycles, workspace, stream=None):

@@ -1,0 +1,1017 @@
+// chunk_attn.cu -- attention of new tokens over a paged cache that already
+// holds their keys: one token per sequence (decoding), chunks of a prompt, or
+// both mixed, on the tensor cores (tcgen05, TMEM, TMA).
+//
+// What it computes. Token i of a sequence's n_b new ones sits at position
+// t = kv_len - n_b + i and sees keys max(0, t - w + 1) .. t:
+//   o = sum_j p_j v_j / l,  p_j = exp(scale q.k_j - m),  l = sum_j p_j,
+// one pass over the keys with a running maximum m and sum l per row.
+//
+// Rows. The g query heads that share a kv head are rows of one product: a
+// 128-row tile holds 128 / g consecutive tokens, all their g heads (row = token
+// * g + head), so a key/value tile staged once serves g times as many rows and a
+// decoding token fills g rows instead of one.
+//
+// Units and the split of the key axis. A unit is up to two row tiles of one
+// sequence and the key tiles (128 tokens) they see. The plan kernel lists the
+// units with the running count of their key tiles; all kv heads have the same
+// list. The CTAs form lanes = gcd(Hkv, CTAs) lanes; lane c % lanes serves kv
+// heads c % lanes, + lanes, ..., and its CTAs cut the lane's key tiles, laid end
+// to end, into equal shares. So every CTA gets the same number of key tiles
+// whatever the batch looks like, a long history of one sequence is spread over
+// the whole GPU, and neighbouring CTAs (one per lane) read the same token rows
+// of the cache at the same time. A unit cut by a share's border leaves partials
+// (m, l, unnormalised o; fp32) that the merge kernel joins; a CTA has at most
+// two of those, so the workspace does not grow with the batch.
+//
+// Two ways through a unit. With two row tiles, slot s works on row tile s and
+// both read each key tile. With one (decoding and short chunks), both slots work
+// on the same rows, slot s on every second key tile, with accumulators of their
+// own that the epilogue adds up, so that the softmax of one tile still runs
+// beside the products of the other.
+//
+// Roles (320 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
+// one thread per row), warp 8 copies (page lookups by its lanes, TMA boxes of
+// up to 128 tokens within a page), warp 9 issues tcgen05.mma. S = Q K^T (bf16,
+// M = 128, N = 128) goes to TMEM, P returns there as bf16 over S, O += P V. TMEM:
+// S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [384,384+d).
+//
+// Precision: products of bf16 values accumulate in fp32; m, l and o are fp32;
+// P is rounded to bf16 for the product with V (the sum l takes it unrounded),
+// at most half a bf16 step of each term, which the sum averages below the rounding
+// of o itself.
+//
+// Keys outside the sequence's length or before every row's window are never
+// read into a result: their copy boxes are skipped (zero fill), their logits
+// replaced by -inf and, where a page reaches past them, their value rows
+// cleared in shared memory, so whatever a stale page holds does not matter.
+#include "ptx.cuh"
+
+namespace orthros {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kRows = 128;  // rows of a tile
+constexpr int kKeys = 128;  // keys of a tile
+constexpr int kNumK = 3, kNumV = 2;
+constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+// Three of the ten warps sit on two of the four schedulers: 168 registers a
+// thread fit (3 x 32 x 168 of 16K), so the bound is taken for 384 threads.
+constexpr int kBound = 384;
+constexpr int kFlagRing = 8;
+// A share of fewer key tiles than this is not worth a CTA of its own.
+constexpr int kMinTiles = 2;
+
+template <int D> struct Cfg {
+    static constexpr int kSub = D / 64;             // 128-byte swizzle atoms per row
+    static constexpr int kTile = kRows * D * 2;     // one 128 x D bf16 tile
+    static constexpr int kQ0 = 0;
+    static constexpr int kK0 = 2 * kTile;
+    static constexpr int kV0 = kK0 + kNumK * kTile;
+    static constexpr int kMeta = kV0 + kNumV * kTile;
+    static constexpr int kSmem = kMeta + 2048 + 1024;  // + alignment slack
+    static constexpr int kTmemO = 256;
+};
+
+// One run of key tiles of one unit, as the roles need it.
+struct Segment {
+    int end;                 // no more segments
+    int b, kv, tok0, cnt;    // sequence, kv head, first token and tokens of the unit
+    int pos0;                // position of the unit's first token
+    int kt0, nkt;            // key tiles kt0 .. kt0 + nkt - 1
+    int pair;                // two row tiles (else both slots share one)
+    int partial;             // partial index, or -1: the unit is complete here
+    int lo[2], hi[2];        // pair: tiles of the run that slot s works on (lo > hi: none)
+};
+
+constexpr int kSegRing = 2;
+
+struct Meta {
+    uint64_t k_full[kNumK], k_empty[kNumK], v_full[kNumV], v_empty[kNumV];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_free[2];
+    uint64_t o_full[2];  // slot s's O complete, for slot s's threads
+    uint64_t ox_full;    // slot 1's O of a shared row tile complete, for slot 0's threads
+    uint64_t ml_full, ml_free;
+    uint64_t g_full[kSegRing], g_empty[kSegRing];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    volatile int bad[kFlagRing];  // per key tile (running count): a page id of its keys was outside the pool
+    Segment seg[kSegRing];
+    float2 ml[kRows];             // slot 1's running max and sum, for slot 0 (shared row tile)
+};
+static_assert(sizeof(Meta) <= 2048, "barriers and metadata must fit their shared-memory region");
+
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                   "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                   "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Byte offset of (row, 16-byte chunk c) in a 128-byte-swizzled tile of 128 rows.
+__device__ __forceinline__ uint32_t sw128(int row, int c) {
+    return (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// Key tiles a run of tokens at positions [first, last] sees.
+__device__ __forceinline__ void key_tiles(int first, int last, int window, int &lo, int &hi) {
+    lo = max(0, first - window + 1) / kKeys;
+    hi = last / kKeys;
+}
+
+// ---------------------------------------------------------------------------
+// Plan: one block. Checks the lengths, lists the units and their key tiles.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+__device__ void fill_nan(const ChunkParams &p, long long tok0, long long tok1, int d, int tid, int nthreads) {
+    const long long e0 = tok0 * p.Hq * d, e1 = tok1 * p.Hq * d;
+    for (long long i = e0 + tid; i < e1; i += nthreads) p.o[i] = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+    if (p.lse)
+        for (long long i = tok0 * p.Hq + tid; i < tok1 * p.Hq; i += nthreads) p.lse[i] = __int_as_float(0x7fc00000);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p, int d) {
+    __shared__ long long wsum[2][32];
+    __shared__ long long carry[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        *p.status = 0;
+        carry[0] = carry[1] = 0;
+    }
+    int bad = 0;
+    for (int b = tid; b < p.B; b += kPlanThreads) bad |= p.q_indptr[b + 1] < p.q_indptr[b];
+    if (tid == 0) bad |= p.q_indptr[0] != 0 || p.q_indptr[p.B] != p.n;
+    if (__syncthreads_or(bad)) {  // no token's sequence is known
+        if (tid == 0) {
+            set_status(p.status, ORTHROS_DEV_BAD_LENGTH);
+            *p.plan = ChunkPlan{0, 0, 0};
+        }
+        fill_nan(p, 0, p.n, d, tid, kPlanThreads);
+        return;
+    }
+    const int ut = 2 * p.tile_tokens;
+    // new tokens of sequence b, or 0 when there are none or its lengths are impossible
+    auto tokens_of = [&](int b, int &tok0, int &len, bool &wrong) -> int {
+        tok0 = p.q_indptr[b];
+        const int nb = p.q_indptr[b + 1] - tok0;
+        len = p.kv_lens[b];
+        wrong = nb > 0 && (nb > p.max_new || len < nb || (long long)len > (long long)p.max_pages * p.page_size);
+        return wrong ? 0 : nb;
+    };
+    // key tiles of the unit that begins at token i of nb, whose first position is t0
+    auto unit_tiles = [&](int i, int nb, int t0, int &lo) -> int {
+        int hi;
+        key_tiles(t0 + i, t0 + min(nb, i + ut) - 1, p.window, lo, hi);
+        return hi - lo + 1;
+    };
+    for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+        int tok0, len, lo;
+        bool wrong;
+        const int nb = tokens_of(b, tok0, len, wrong);
+        if (wrong) {
+            if (lane == 0) set_status(p.status, ORTHROS_DEV_BAD_LENGTH);
+            fill_nan(p, tok0, p.q_indptr[b + 1], d, lane, 32);
+        }
+        long long tiles = 0;
+        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_tiles(i, nb, len - nb, lo);
+        tiles = warp_scan(tiles, lane);
+        if (lane == 31) {
+            p.seq_units[b] = (nb + ut - 1) / ut;
+            p.seq_tiles[b] = tiles;
+        }
+    }
+    __syncthreads();
+    // exclusive prefix sums over the sequences, 1024 at a time
+    for (int base = 0; base < p.B; base += kPlanThreads) {
+        const int b = base + tid;
+        const long long u = b < p.B ? p.seq_units[b] : 0, t = b < p.B ? p.seq_tiles[b] : 0;
+        long long su = warp_scan(u, lane), st = warp_scan(t, lane);
+        if (lane == 31) {
+            wsum[0][warp] = su;
+            wsum[1][warp] = st;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            wsum[0][lane] = warp_scan(wsum[0][lane], lane);
+            wsum[1][lane] = warp_scan(wsum[1][lane], lane);
+        }
+        __syncthreads();
+        su += carry[0] + (warp ? wsum[0][warp - 1] : 0);
+        st += carry[1] + (warp ? wsum[1][warp - 1] : 0);
+        if (b < p.B) {
+            p.seq_units[b] = (int)(su - u);
+            p.seq_tiles[b] = st - t;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            carry[0] += wsum[0][31];
+            carry[1] += wsum[1][31];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) *p.plan = ChunkPlan{(int)carry[0], 0, carry[1]};
+    for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+        int tok0, len;
+        bool wrong;
+        const int nb = tokens_of(b, tok0, len, wrong);
+        const int u0 = p.seq_units[b];
+        long long at = p.seq_tiles[b];
+        for (int i0 = 0; i0 < nb; i0 += 32 * ut) {
+            const int i = i0 + lane * ut;
+            int lo = 0;
+            const int w = i < nb ? unit_tiles(i, nb, len - nb, lo) : 0;
+            const long long sum = warp_scan(w, lane);
+            if (i < nb) {
+                ChunkUnit u;
+                u.b = b;
+                u.tok0 = tok0 + i;
+                u.cnt = min(ut, nb - i);
+                u.pos0 = len - nb + i;
+                u.kt_lo = lo;
+                u.n_kt = w;
+                u.start = at + sum - w;
+                p.units[u0 + i / ut] = u;
+            }
+            at += __shfl_sync(0xffffffffu, sum, 31);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Main kernel
+// ---------------------------------------------------------------------------
+// The shares of a lane: `total` key tiles over `eff` CTAs.
+struct Shares {
+    long long total;
+    int eff;
+    __device__ long long begin(int j) const { return total * j / eff; }
+    // the CTA of the lane whose share holds tile x
+    __device__ int owner(long long x) const { return (int)(((x + 1) * eff - 1) / total); }
+};
+__device__ __forceinline__ Shares shares_of(const ChunkParams &p, const ChunkPlan &pl) {
+    Shares s;
+    s.total = (long long)(p.Hkv / p.lanes) * pl.tiles;
+    const long long fit = s.total / kMinTiles;
+    s.eff = (int)max(1LL, min((long long)p.per_lane, fit));
+    return s;
+}
+
+// Last unit whose start is <= x (all 32 lanes; units are sorted by start).
+__device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int i = lo + lane * step;
+        const bool le = i < lo + len && units[i].start <= x;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // lane 0 always holds
+        const int at = k * step;
+        lo += at;
+        len = min(step, len - at);
+    }
+    return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBound, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Meta &mt = *reinterpret_cast<Meta *>(smem + C::kMeta);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort = &mt.abort;
+    const int g = p.Hq / p.Hkv;
+    const int tt = p.tile_tokens;
+
+    if (tid == 0) {
+        for (int i = 0; i < kNumK; ++i) {
+            mbar_init(&mt.k_full[i], 1);
+            mbar_init(&mt.k_empty[i], 1);
+        }
+        for (int i = 0; i < kNumV; ++i) {
+            mbar_init(&mt.v_full[i], 1);
+            mbar_init(&mt.v_empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&mt.q_full[s], 1);
+            mbar_init(&mt.q_empty[s], 1);
+            mbar_init(&mt.s_full[s], 1);
+            mbar_init(&mt.p_full[s], kRows);
+            mbar_init(&mt.o_full[s], 1);
+            mbar_init(&mt.o_free[s], kRows);
+        }
+        mbar_init(&mt.ox_full, 1);
+        mbar_init(&mt.ml_full, kRows);
+        mbar_init(&mt.ml_free, kRows);
+        for (int r = 0; r < kSegRing; ++r) {
+            mbar_init(&mt.g_full[r], 1);
+            mbar_init(&mt.g_empty[r], kSoftmaxWarps + 1);
+        }
+        mbar_init(&mt.mma_done, 1);
+        mt.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&mt.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = mt.tmem_base;
+    // the plan's kernel must have finished; the merge may start its set-up
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == kCopyWarp) {
+        // ---------------- segments and copies ----------------
+        const ChunkPlan pl = *p.plan;
+        const int ln = blockIdx.x % p.lanes, j = blockIdx.x / p.lanes;
+        ChunkHead head{0, 0, 0, 0};
+        uint32_t gk = 0, gv = 0;  // key and value copies issued
+        uint32_t nq[2] = {0, 0};  // query tiles issued per slot
+        int ring = 0;
+        bool alive = true;
+        auto publish = [&](const Segment &sg) -> bool {
+            const int r = ring % kSegRing;
+            if (ring >= kSegRing && !mbar_wait_warp(&mt.g_empty[r], ((ring / kSegRing) - 1) & 1, abort, p.status))
+                return false;
+            if (lane == 0) {
+                mt.seg[r] = sg;
+                mbar_arrive(&mt.g_full[r]);
+            }
+            __syncwarp();
+            ++ring;
+            return true;
+        };
+        if (pl.tiles > 0) {
+            const Shares sh = shares_of(p, pl);
+            if (j < sh.eff) {
+                long long x = sh.begin(j);
+                const long long x1 = sh.begin(j + 1);
+                int kvo = (int)(x / pl.tiles);
+                int u = find_unit(p.units, pl.units, x - kvo * pl.tiles, lane);
+                while (x < x1 && alive) {
+                    const ChunkUnit un = p.units[u];
+                    const int a = (int)(x - kvo * pl.tiles - un.start);
+                    const int n_tiles = (int)min((long long)(un.n_kt - a), x1 - x);
+                    Segment sg;
+                    sg.end = 0;
+                    sg.b = un.b;
+                    sg.kv = ln + kvo * p.lanes;
+                    sg.tok0 = un.tok0;
+                    sg.cnt = un.cnt;
+                    sg.pos0 = un.pos0;
+                    sg.kt0 = un.kt_lo + a;
+                    sg.nkt = n_tiles;
+                    sg.pair = un.cnt > tt;
+                    const bool starts = a == 0, ends = a + n_tiles == un.n_kt;
+                    sg.partial = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
+                    if (starts && !ends) {
+                        head.n_parts = sh.owner(x + un.n_kt - 1) - j + 1;
+                        head.tok0 = un.tok0;
+                        head.cnt = un.cnt;
+                        head.kv = sg.kv;
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        int lo = 0, hi = n_tiles - 1;
+                        if (sg.pair) {
+                            const int c0 = s * tt, c1 = s ? un.cnt : tt;
+                            int kl, kh;
+                            key_tiles(un.pos0 + c0, un.pos0 + c1 - 1, p.window, kl, kh);
+                            lo = max(lo, kl - sg.kt0);
+                            hi = min(hi, kh - sg.kt0);
+                        }
+                        sg.lo[s] = lo;
+                        sg.hi[s] = hi;
+                    }
+                    if (!(alive = publish(sg))) break;
+                    // query tiles (rows past the tile's tokens keep whatever was there: their results are dropped)
+                    for (int s = 0; alive && s < (sg.pair ? 2 : 1); ++s) {
+                        if (nq[s] > 0 && !mbar_wait_warp(&mt.q_empty[s], (nq[s] - 1) & 1, abort, p.status)) {
+                            alive = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&mt.q_full[s], C::kSub * 128 * g * tt);
+                            for (int h = 0; h < C::kSub; ++h)
+                                tma_load_3d(smem + C::kQ0 + s * C::kTile + h * (kRows * 128), &tm_q, &mt.q_full[s],
+                                            64 * h, sg.kv * g, sg.tok0 + s * tt);
+                        }
+                        __syncwarp();
+                        ++nq[s];
+                    }
+                    if (!alive) break;
+                    // key/value tiles: keys [key_lo, key_hi] exist for this unit
+                    const int32_t *bt = p.block_table + (long long)sg.b * p.max_pages;
+                    const int key_hi = un.pos0 + un.cnt - 1;
+                    const int key_lo = max(0, un.pos0 - p.window + 1);
+                    const int oob = p.num_pages * p.page_size;  // past the pool: the copy fills zeros
+                    const int box = p.box;
+                    const int n_box = box ? kKeys / box : 0;
+                    // first token row of this lane's box of a tile (TMA), or oob; bad: page id outside the pool
+                    auto look = [&](int kt, int &bad) -> int {
+                        bad = 0;
+                        if (lane >= n_box) return oob;
+                        const int key = kt * kKeys + lane * box;
+                        if (key > key_hi || key + box - 1 < key_lo) return oob;
+                        const int pg = bt[key / p.page_size];
+                        if (pg < 0 || pg >= p.num_pages) {
+                            bad = 1;
+                            return oob;
+                        }
+                        return pg * p.page_size + key % p.page_size;
+                    };
+                    int bad_next = 0, tok_next = look(sg.kt0, bad_next);
+                    for (int it = 0; it < sg.nkt; ++it) {
+                        const uint32_t gi = gk;
+                        const int sk = gi % kNumK, sv = gi % kNumV;
+                        const int tok = tok_next, bad = bad_next;
+                        if (it + 1 < sg.nkt) tok_next = look(sg.kt0 + it + 1, bad_next);
+                        if (gi >= (uint32_t)kNumK &&
+                            !mbar_wait_warp(&mt.k_empty[sk], ((gi / kNumK) - 1) & 1, abort, p.status)) {
+                            alive = false;
+                            break;
+                        }
+                        uint8_t *ks = smem + C::kK0 + sk * C::kTile, *vs = smem + C::kV0 + sv * C::kTile;
+                        if (box) {
+                            const bool any_bad = __any_sync(0xffffffffu, bad);
+                            if (any_bad && lane == 0) set_status(p.status, ORTHROS_DEV_BAD_PAGE);
+                            if (lane == 0) {
+                                mt.bad[gi % kFlagRing] = any_bad;
+                                mbar_arrive_expect_tx(&mt.k_full[sk], C::kTile);
+                            }
+                            __syncwarp();
+                            if (lane < n_box)
+                                for (int h = 0; h < C::kSub; ++h)
+                                    tma_load_3d(ks + h * (kRows * 128) + lane * box * 128, &tm_k, &mt.k_full[sk], 64 * h,
+                                                sg.kv, tok);
+                            if (gi >= (uint32_t)kNumV &&
+                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, p.status)) {
+                                ++gk;
+                                alive = false;
+                                break;
+                            }
+                            if (lane == 0) mbar_arrive_expect_tx(&mt.v_full[sv], C::kTile);
+                            __syncwarp();
+                            if (lane < n_box)
+                                for (int h = 0; h < C::kSub; ++h)
+                                    tma_load_3d(vs + h * (kRows * 128) + lane * box * 128, &tm_v, &mt.v_full[sv], 64 * h,
+                                                sg.kv, tok);
+                            ++gv;
+                        } else {
+                            // page sizes without a copy box: the lanes gather the rows, 16 bytes at a time
+                            if (gi >= (uint32_t)kNumV &&
+                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, p.status)) {
+                                alive = false;
+                                break;
+                            }
+                            int wrong = 0;
+                            constexpr int kCh = D / 8;
+                            for (int e = lane; e < kRows * kCh; e += 32) {
+                                const int row = e / kCh, c = e % kCh;
+                                const int key = (sg.kt0 + it) * kKeys + row;
+                                long long src = -1;
+                                if (key >= key_lo && key <= key_hi) {
+                                    const int pg = bt[key / p.page_size];
+                                    if (pg < 0 || pg >= p.num_pages) wrong = 1;
+                                    else src = (((long long)pg * p.page_size + key % p.page_size) * p.Hkv + sg.kv) * D + 8 * c;
+                                }
+                                const uint32_t dk = smem_u32(ks + sw128(row, c)), dv = smem_u32(vs + sw128(row, c));
+                                const uint32_t bytes = src >= 0 ? 16 : 0;  // 0: zero fill
+                                const __nv_bfloat16 *a = p.k + max(src, 0LL), *b2 = p.v + max(src, 0LL);
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk), "l"(a), "r"(bytes) : "memory");
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dv), "l"(b2), "r"(bytes) : "memory");
+                            }
+                            asm volatile("cp.async.wait_all;" ::: "memory");
+                            fence_proxy_async_smem();
+                            wrong = __any_sync(0xffffffffu, wrong);
+                            if (lane == 0) {
+                                if (wrong) set_status(p.status, ORTHROS_DEV_BAD_PAGE);
+                                mt.bad[gi % kFlagRing] = wrong;
+                                mbar_arrive(&mt.k_full[sk]);
+                                mbar_arrive(&mt.v_full[sv]);
+                            }
+                            __syncwarp();
+                        }
+                        ++gk;
+                    }
+                    x += n_tiles;
+                    if (++u == pl.units) {
+                        u = 0;
+                        ++kvo;
+                    }
+                }
+            }
+        }
+        if (alive) {
+            Segment sg{};
+            sg.end = 1;
+            publish(sg);
+        }
+        if (lane == 0) {
+            p.heads[blockIdx.x] = head;
+            // nothing may be in flight when the CTA leaves
+            if (p.box) {
+                for (uint32_t i = gk > (uint32_t)kNumK ? gk - kNumK : 0; i < gk; ++i)
+                    mbar_wait_drain(&mt.k_full[i % kNumK], (i / kNumK) & 1, p.status);
+                for (uint32_t i = gv > (uint32_t)kNumV ? gv - kNumV : 0; i < gv; ++i)
+                    mbar_wait_drain(&mt.v_full[i % kNumV], (i / kNumV) & 1, p.status);
+            }
+            for (int s = 0; s < 2; ++s)
+                if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, p.status);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- tcgen05.mma issuer (lane 0 issues, the warp waits together) ----------------
+        constexpr uint32_t kIdescS = idesc_f16(1, 1, 0, 0, kRows, kKeys);  // bf16, both K-major
+        constexpr uint32_t kIdescO = idesc_f16(1, 1, 0, 1, kRows, D);      // bf16, V MN-major
+        constexpr uint32_t kTileU = C::kTile >> 4;
+        const uint64_t dq = desc_sw128(smem_u32(smem + C::kQ0), 16, 1024);
+        const uint64_t dk = desc_sw128(smem_u32(smem + C::kK0), 16, 1024);
+        const uint64_t dv = desc_sw128(smem_u32(smem + C::kV0), kKeys * 128, 1024);
+        auto issue_s = [&](int s, uint64_t qd, uint64_t kd) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+                mma_ss(tmem + s * 128, qd + off, kd + off, kIdescS, ks > 0);
+            }
+            tc_commit(&mt.s_full[s]);
+        };
+        auto issue_pv = [&](int s, uint64_t vd, uint32_t acc0) {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(tmem + C::kTmemO + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
+                       kk > 0 ? 1u : acc0);
+        };
+        uint32_t gk = 0;                // key tiles consumed
+        uint32_t nq[2] = {0, 0};        // query tiles consumed per slot
+        uint32_t pc[2] = {0, 0};        // P tiles consumed per slot
+        uint32_t oc[2] = {0, 0};        // segments in which the slot had tiles
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int r = i % kSegRing;
+            if (!(ok = mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
+            const Segment sg = mt.seg[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mt.g_empty[r]);
+            if (sg.end) break;
+            const int key_hi = sg.pos0 + sg.cnt - 1, key_lo = max(0, sg.pos0 - p.window + 1);
+            // waits for value tile `it` and clears its rows outside [key_lo, key_hi] (a page that
+            // reaches past them holds anything, and 0 * NaN is NaN)
+            auto value_tile = [&](int it) -> bool {
+                const uint32_t gi = gk + it;
+                uint8_t *vs = smem + C::kV0 + (gi % kNumV) * C::kTile;
+                if (!mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status)) return false;
+                const int key0 = (sg.kt0 + it) * kKeys;
+                const int r0 = max(0, key_lo - key0), r1 = min(kKeys, key_hi + 1 - key0);  // rows [r0, r1) stay
+                if (r0 > 0 || r1 < kKeys) {
+                    const int n = r0 + kKeys - r1;  // rows to clear
+                    constexpr int kCh = D / 8;
+                    for (int e = lane; e < n * kCh; e += 32) {
+                        const int k = e / kCh, row = k < r0 ? k : r1 + k - r0;
+                        *reinterpret_cast<uint4 *>(vs + sw128(row, e % kCh)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto key_tile = [&](int it) -> bool {
+                const uint32_t gi = gk + it;
+                return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
+            };
+            auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
+            auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
+            // the slot's P of its next tile is there; before its first product of the segment, its O is free
+            auto p_tile = [&](int s, bool first) -> bool {
+                if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
+                ++pc[s];
+                if (first) {
+                    if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
+                    ++oc[s];
+                }
+                tc_fence_after();
+                return true;
+            };
+            if (sg.pair) {
+                const int n = sg.nkt;
+                for (int it = -1; ok && it < n; ++it) {
+                    const bool more = it + 1 < n;
+                    if (it >= 0 && !(ok = value_tile(it))) break;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (it >= 0 && it >= sg.lo[s] && it <= sg.hi[s]) {
+                            if (!(ok = p_tile(s, it == sg.lo[s]))) break;
+                            if (lane == 0) {
+                                issue_pv(s, vdesc(it), it > sg.lo[s]);
+                                if (it == sg.hi[s]) tc_commit(&mt.o_full[s]);
+                            }
+                            __syncwarp();
+                        }
+                        if (more) {
+                            if (it < 0 && !(ok = mbar_wait_warp(&mt.q_full[s], nq[s] & 1, abort, p.status))) break;
+                            if (s == 0 && !(ok = key_tile(it + 1))) break;
+                            tc_fence_after();
+                            if (lane == 0) {
+                                if (it + 1 >= sg.lo[s] && it + 1 <= sg.hi[s]) issue_s(s, dq + s * kTileU, kdesc(it + 1));
+                                if (it + 2 == n) tc_commit(&mt.q_empty[s]);
+                                if (s == 1) tc_commit(&mt.k_empty[(gk + it + 1) % kNumK]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    if (it >= 0 && lane == 0) tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                    __syncwarp();
+                }
+                ++nq[0];
+                ++nq[1];
+            } else {
+                const int n = sg.nkt;
+                if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
+                ++nq[0];
+                // S of tile it into slot it & 1
+                auto s_tile = [&](int it) -> bool {
+                    if (!key_tile(it)) return false;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        issue_s(it & 1, dq, kdesc(it));
+                        if (it + 1 == n) tc_commit(&mt.q_empty[0]);
+                        tc_commit(&mt.k_empty[(gk + it) % kNumK]);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                ok = s_tile(0) && (n < 2 || s_tile(1));
+                for (int it = 0; ok && it < n; ++it) {
+                    const int s = it & 1;
+                    if (!(ok = value_tile(it) && p_tile(s, it < 2))) break;
+                    if (lane == 0) {
+                        issue_pv(s, vdesc(it), it >= 2);
+                        if (it + 2 >= n) tc_commit(s ? &mt.ox_full : &mt.o_full[0]);
+                        tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                    }
+                    __syncwarp();
+                    if (it + 2 < n) ok = s_tile(it + 2);
+                }
+            }
+            gk += sg.nkt;
+        }
+        // every product issued must be complete before tensor memory is freed
+        if (lane == 0) {
+            tc_commit(&mt.mma_done);
+            mbar_wait_drain(&mt.mma_done, 0, p.status);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax: one thread per row ----------------
+        const int s = warp >> 2;
+        const int row = ((warp & 3) << 5) | lane;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + s * 128;
+        const uint32_t t_o = tmem + lane_off + C::kTmemO;  // slot 0's O (slot 1's: + 128)
+        const float c2 = p.scale_log2;
+        uint32_t cnt = 0;              // S tiles of this slot handled
+        uint32_t oc = 0, ox = 0;       // phases of o_full[s] and ox_full waited for
+        uint32_t shared = 0;           // segments with one row tile
+        uint32_t gk = 0;               // key tiles of earlier segments
+        for (int i = 0;; ++i) {
+            const int r = i % kSegRing;
+            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status)) break;
+            const Segment sg = mt.seg[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mt.g_empty[r]);
+            if (sg.end) break;
+            const int c0 = sg.pair && s ? tt : 0;                    // first token of this slot's row tile
+            const int n_tok = min(tt, sg.cnt - c0);
+            const bool mine = row < n_tok * g;                       // a real row
+            const bool idle = (warp & 3) * 32 >= n_tok * g;          // no real row in this warp
+            const int t_first = sg.pos0 + c0, t_last = t_first + n_tok - 1;
+            const int t_row = mine ? t_first + row / g : t_last;
+            const int lo_row = max(0, t_row - p.window + 1);
+            const int lo_max = max(0, t_last - p.window + 1);
+            const int it0 = sg.pair ? sg.lo[s] : s, step = sg.pair ? 1 : 2, it1 = sg.pair ? sg.hi[s] : sg.nkt - 1;
+            const int tiles = it0 <= it1 ? (it1 - it0) / step + 1 : 0;
+            float m_ref = -INFINITY, l = 0.f;
+            bool ok = true, bad = false;
+            for (int it = it0; it <= it1; it += step) {
+                if (!(ok = mbar_wait_warp(&mt.s_full[s], cnt & 1, abort, p.status))) break;
+                ++cnt;
+                if (idle) {
+                    mbar_arrive(&mt.p_full[s]);
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t xr[kKeys];
+                using Cols = uint32_t[32];
+#pragma unroll
+                for (int q = 0; q < kKeys / 32; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<Cols *>(xr + 32 * q));
+                const int key0 = (sg.kt0 + it) * kKeys;
+                if (mt.bad[(gk + it) % kFlagRing] && key0 <= t_row && key0 + kKeys - 1 >= lo_row) bad = true;
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < kKeys / 32; ++q) reg_fence(*reinterpret_cast<Cols *>(xr + 32 * q));
+                if (key0 + kKeys - 1 > t_first || key0 < lo_max) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (key0 + c > t_row || key0 + c < lo_row) xr[c] = __float_as_uint(-INFINITY);
+                }
+                const float *x = reinterpret_cast<const float *>(xr);
+                float mq[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    mq[q] = max3(max3(x[8 * q], x[8 * q + 1], x[8 * q + 2]), max3(x[8 * q + 3], x[8 * q + 4], x[8 * q + 5]),
+                                 fmaxf(x[8 * q + 6], x[8 * q + 7]));
+                const float m_tile = max3(max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), max3(mq[6], mq[7], mq[8])),
+                                          max3(mq[9], mq[10], mq[11]), max3(mq[12], mq[13], fmaxf(mq[14], mq[15])));
+                // the shift follows the maximum only when it grew by more than 2^8 (P stays finite in bf16)
+                const float m_new = fmaxf(m_ref, m_tile);
+                const bool resc = (m_new - m_ref) * c2 > 8.f;  // true on the first finite maximum
+                const bool any_resc = __any_sync(0xffffffffu, resc);
+                const float alpha = resc ? ex2((m_ref - m_new) * c2) : 1.f;
+                if (resc) {
+                    l *= alpha;
+                    m_ref = m_new;
+                }
+                const float mb = m_ref == -INFINITY ? 0.f : m_ref * c2;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t cv = f32x2(c2, c2), mv = f32x2(-mb, -mb);
+#pragma unroll
+                for (int j = 0; j < kKeys / 32; ++j) {
+                    const float *xj = x + 32 * j;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a0, a1;
+                        fma_f32x2(xj[2 * e], xj[2 * e + 1], cv, mv, a0, a1);
+                        float p0, p1;
+                        if (j == kKeys / 32 - 1 && e == 15) exp2_fma_x2(a0, a1, p0, p1);
+                        else p0 = ex2(a0), p1 = ex2(a1);
+                        add_f32x2(ls[2 * (e & 1)], ls[2 * (e & 1) + 1], p0, p1);
+                        pk[e] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(t_s + 16 * j, pk);
+                }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                // O of this slot is idle here: the product of its previous tile completed before this S
+                if (any_resc && it != it0) {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + s * 128 + 32 * j, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(t_o + s * 128 + 32 * j, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&mt.p_full[s]);
+            }
+            if (!ok) break;
+            if (bad) l = __int_as_float(0x7fc00000);  // the row saw a page that does not exist: NaN
+
+            // ---- epilogue ----
+            const int n0 = sg.pair ? (s == 0 ? tiles : 0) : (sg.nkt + 1) / 2;  // slot 0's tiles
+            const int n1 = sg.pair ? (s == 1 ? tiles : 0) : sg.nkt / 2;        // slot 1's
+            gk += sg.nkt;
+            if (!sg.pair && s == 1) {
+                // slot 0 finishes the shared rows
+                if (shared > 0 && !mbar_wait_warp(&mt.ml_free, (shared - 1) & 1, abort, p.status)) break;
+                mt.ml[row] = make_float2(m_ref, l);
+                mbar_arrive(&mt.ml_full);
+                ++shared;
+                continue;
+            }
+            // weights of the two accumulators (a slot with its own row tile: 1 and 0)
+            float w0 = 1.f, w1 = 0.f, m = m_ref;
+            bool two = false;
+            if (n0 + n1 > 0 && !mbar_wait_warp(&mt.o_full[s], oc++ & 1, abort, p.status)) break;
+            if (!sg.pair) {
+                two = n1 > 0;
+                if (two && !mbar_wait_warp(&mt.ox_full, ox++ & 1, abort, p.status)) break;
+                if (!mbar_wait_warp(&mt.ml_full, shared & 1, abort, p.status)) break;
+                ++shared;
+                const float2 o = mt.ml[row];
+                mbar_arrive(&mt.ml_free);
+                if (two) {
+                    m = fmaxf(m_ref, o.x);
+                    const float mb = m == -INFINITY ? 0.f : m * c2;
+                    w0 = ex2(m_ref * c2 - mb);
+                    w1 = ex2(o.x * c2 - mb);
+                    l = l * w0 + o.y * w1;
+                }
+            }
+            if (!idle) {
+                tc_fence_after();
+                const long long tok = sg.tok0 + c0 + row / g;
+                const int h = sg.kv * g + row % g;
+                const uint32_t t_a = t_o + (sg.pair ? s * 128 : 0);
+                if (sg.partial < 0) {
+                    const float inv = l > 0.f ? 1.f / l : l;  // a NaN sum stays
+                    w0 *= inv;
+                    w1 *= inv;
+                    __nv_bfloat16 *dst = p.o + (tok * p.Hq + h) * D;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t o[32];
+                        tmem_ld32(t_a + 32 * j, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+                        if (two) {
+                            tmem_ld32(t_a + 128 + 32 * j, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
+                        }
+                        if (mine) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                reinterpret_cast<uint4 *>(dst + 32 * j)[e] =
+                                    make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                               pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                        }
+                    }
+                    if (mine && p.lse) p.lse[tok * p.Hq + h] = m * p.scale + logf(l);
+                } else {
+                    const long long at = ((long long)sg.partial * p.slots_cap + (sg.pair ? s : 0)) * p.rows_cap + row;
+                    if (mine) p.part_ml[at] = make_float2(m, l);
+                    float *dst = p.part_o + at * D;
+                    if (n0 + n1 > 0) {
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) {
+                            uint32_t o[32];
+                            tmem_ld32(t_a + 32 * j, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+                            float f[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+                            if (two) {
+                                tmem_ld32(t_a + 128 + 32 * j, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
+                            }
+                            if (mine) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    reinterpret_cast<float4 *>(dst + 32 * j)[e] =
+                                        make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            if (n0) mbar_arrive(&mt.o_free[0]);
+            if (n1) mbar_arrive(&mt.o_free[1]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the units that a share's border cut: one warp per row, the parts'
+// weights found by its lanes, the outputs added in the order of the parts.
+// ---------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
+template <int D> __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ChunkHead hd = p.heads[blockIdx.x];
+    if (hd.n_parts == 0) return;
+    const int lane = threadIdx.x & 31;
+    const int g = p.Hq / p.Hkv;
+    const int rr = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the unit, slot-major
+    const int s = rr / p.rows_cap, row = rr % p.rows_cap;
+    const int n_tok = min(p.tile_tokens, hd.cnt - s * p.tile_tokens);
+    if (s >= p.slots_cap || row >= n_tok * g) return;
+    // part i: the head's own (second) partial, then the first partial of the lane's next CTAs
+    auto index = [&](int i) -> long long {
+        const long long id = i == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + (long long)i * p.lanes);
+        return (id * p.slots_cap + s) * p.rows_cap + row;
+    };
+    const float c2 = p.scale_log2;
+    float M = -INFINITY;
+    for (int i = lane; i < hd.n_parts; i += 32) M = fmaxf(M, p.part_ml[index(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mb = M == -INFINITY ? 0.f : M * c2;
+    constexpr int E = D / 32;
+    float acc[E], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < hd.n_parts; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < hd.n_parts) {
+            const float2 ml = p.part_ml[index(i0 + lane)];
+            w = ex2(ml.x * c2 - mb);
+            L += w * ml.y;
+        }
+        const int k1 = min(32, hd.n_parts - i0);
+        for (int k = 0; k < k1; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            if (wk == 0.f) continue;  // a part without keys for this row wrote no output
+            const float *src = p.part_o + index(i0 + k) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, src[e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L > 0.f ? 1.f / L : L;  // a NaN sum stays
+    const long long out = ((long long)hd.tok0 + s * p.tile_tokens + row / g) * p.Hq + hd.kv * g + row % g;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + out * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[out] = M * p.scale + logf(L);
+}
+
+template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
+    CUtensorMap tq, tk, tv;
+    const long long tokens = (long long)p.num_pages * p.page_size;
+    const int box = p.box ? p.box : 8;  // (unused maps are valid ones)
+    if (!encode_rows_map_3d(&tq, p.q, p.n, p.Hq, D, p.Hq / p.Hkv, p.tile_tokens) ||
+        !encode_kv_map_3d(&tk, p.k, tokens, p.Hkv, D, box) || !encode_kv_map_3d(&tv, p.v, tokens, p.Hkv, D, box))
+        return cudaErrorInvalidValue;
+    static SmemLimit limit;
+    if (cudaError_t e = limit.ensure((const void *)chunk_attn_kernel<D>, Cfg<D>::kSmem); e != cudaSuccess) return e;
+    {
+        ProfScope ps("chunk_plan", stream);
+        chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, D);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    // the attention's set-up overlaps the plan, the merge's launch the attention
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.lanes * p.per_lane);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    {
+        ProfScope ps("chunk_attn", stream);
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t mc = {};
+    mc.gridDim = dim3(p.lanes * p.per_lane, (p.slots_cap * p.rows_cap + kMergeWarps - 1) / kMergeWarps);
+    mc.blockDim = dim3(kMergeWarps * 32);
+    mc.stream = stream;
+    mc.attrs = attr;
+    mc.numAttrs = 1;
+    ProfScope ps("chunk_merge", stream);
+    if (cudaError_t e = cudaLaunchKernelEx(&mc, chunk_merge_kernel<D>, p); e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+long long chunk_max_units(long long n, int B, int tile_tokens) { return n / (2 * tile_tokens) + B; }
+
+cudaError_t launch_chunk_attention(const ChunkParams &p, int d, cudaStream_t stream) {
+    return d == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
+}
+
+}  // namespace orthros

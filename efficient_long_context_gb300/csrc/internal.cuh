@@ -216,6 +216,9 @@ cudaError_t launch_splitkv_tma(const SplitParams &p, int d, int rows_per_group, 
 // prefill_tc.cu: 3-D tensor map (d, Hkv, tokens) over bf16 [tokens, Hkv, d] rows,
 // box (64 channels, 1 head, box_tokens), 128-byte swizzle, zero fill.
 bool encode_kv_map_3d(CUtensorMap *m, const void *base, long long tokens, int Hkv, int d, int box_tokens);
+// The same over bf16 [tokens, heads, d] rows with a box of several heads.
+bool encode_rows_map_3d(CUtensorMap *m, const void *base, long long tokens, int heads, int d, int box_heads,
+                        int box_tokens);
 
 // simt_rows.cu: one warp per (row, head); any element type; the fp32 path.
 cudaError_t launch_rows_simt(const RowsArgs &a, RowKind kind, int d, orthros_dtype dtype,
@@ -324,6 +327,52 @@ cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cud
 cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t stream);
 cudaError_t launch_rotate_append(const RotateAppendParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
+
+// chunk_attn.cu: attention of new tokens over the paged cache (orthros_chunk_attention).
+// A unit is up to two 128-row query tiles of one sequence (a row is one query
+// head of a GQA group at one token) that read the same key/value tiles; the
+// plan lists the units of the batch once, for one kv head.
+struct ChunkUnit {
+    int b, tok0, cnt, pos0;  // sequence, first token (row of q), tokens, position of the first one
+    int kt_lo, n_kt;         // key tiles the unit's tokens see
+    long long start;         // key tiles of the units before it
+};
+struct ChunkPlan {
+    int units;
+    int pad;
+    long long tiles;  // key tiles of all units (of one kv head)
+};
+// The unit that a CTA begins but does not finish: its output is the merge of
+// n_parts CTAs' partials (0: none).
+struct ChunkHead {
+    int n_parts, tok0, cnt, kv;
+};
+struct ChunkParams {
+    const __nv_bfloat16 *q;          // [n, Hq, d]
+    const __nv_bfloat16 *k, *v;      // caches [num_pages, page_size, Hkv, d]
+    const int32_t *q_indptr;         // device [B + 1]
+    const int32_t *kv_lens;          // device [B]
+    const int32_t *block_table;      // [B, max_pages]
+    int B, n, max_new, Hq, Hkv, window, max_pages, page_size, num_pages;
+    int tile_tokens;                 // tokens of a 128-row tile: 128 / (Hq / Hkv)
+    int box;                         // tokens of a K/V copy box, a divisor of page_size (0: rows are gathered)
+    int lanes, per_lane;             // CTAs: lanes x per_lane; a lane serves Hkv / lanes kv heads
+    int rows_cap, slots_cap;         // rows and slots of a partial
+    float scale, scale_log2;
+    __nv_bfloat16 *o;                // [n, Hq, d]
+    float *lse;                      // [n, Hq] or null
+    uint32_t *status;
+    int32_t *seq_units;              // [B] scratch of the plan
+    long long *seq_tiles;            // [B]
+    ChunkPlan *plan;
+    ChunkUnit *units;
+    ChunkHead *heads;                // [CTAs]
+    float2 *part_ml;                 // [2 CTAs, slots_cap, rows_cap]: running max and sum
+    float *part_o;                   // [2 CTAs, slots_cap, rows_cap, d] unnormalised
+};
+// Units a call with these sizes can have at most (bound for the workspace).
+long long chunk_max_units(long long n, int B, int tile_tokens);
+cudaError_t launch_chunk_attention(const ChunkParams &p, int d, cudaStream_t stream);
 
 // merge.cu: exact merge of normalised partials over disjoint key sets.
 cudaError_t launch_merge_partials(const float *o_parts, const float *lse_parts, int n_parts, int n_rows, int Hq, int d,

@@ -565,6 +565,48 @@ ORTHROS_API orthros_status orthros_rotate_append(
     const int32_t *block_table, int B, int max_pages, int page_size, int num_pages, void *workspace,
     size_t workspace_bytes, orthros_stream_t stream);
 
+/* Workspace bytes orthros_chunk_attention needs for these sizes (0 if rejected). */
+ORTHROS_API size_t orthros_chunk_attention_workspace_size(int B, int n, int max_new, int Hq, int Hkv, int d,
+                                                          int max_pages, int page_size, orthros_dtype dtype);
+
+/*
+ * Attention of new tokens over a paged cache that already holds their keys
+ * and values (orthros_rotate_append or orthros_qkv_project wrote them): one
+ * query stream of a serving step, any mix of single tokens (decoding) and
+ * chunks of a prompt. Sequence b's n_b = q_indptr[b+1] - q_indptr[b] tokens
+ * are the last n_b of its kv_lens[b] cached ones: token i sits at position
+ * t = kv_lens[b] - n_b + i and attends keys max(0, t-w+1) .. t. With the
+ * window of the base stream this is Eq. 4; with window >= kv_lens it is Eq. 5,
+ * the output stream's row (its last token alone, or a whole chunk).
+ *
+ * q            [n, Hq, d] bf16, used as they are (affine and rotation applied
+ *              before)
+ * q_indptr     [B+1] int32 DEVICE, 0 .. n, non-decreasing
+ * kv_lens      [B] int32 DEVICE: cached tokens, the new ones included
+ * max_new      upper bound of the n_b (sizes the workspace; n always serves)
+ * k_cache, v_cache [num_pages, page_size, Hkv, d], block_table [B, max_pages]
+ *              DEVICE int32; any page_size (multiples of 8 are copied by TMA,
+ *              others row by row, slower)
+ * o [n, Hq, d] bf16, lse [n, Hq] float or NULL
+ * scale        > 0
+ * workspace    at least orthros_chunk_attention_workspace_size() bytes,
+ *              256-byte aligned; contents on entry do not matter.
+ * Every length is read on the device: a step can be captured once and replayed
+ * while the lengths grow. bf16 only; at most 128 query heads per kv head.
+ * Keys and values at visible positions must be finite; what pages hold past a
+ * sequence's length, or before every window of the call, does not matter.
+ * A q_indptr that does not run from 0 to n sets ORTHROS_DEV_BAD_LENGTH and
+ * every row is NaN; n_b > max_new, kv_lens[b] < n_b or past the block table
+ * sets it for that sequence's rows. A page id outside [0, num_pages) sets
+ * ORTHROS_DEV_BAD_PAGE and the rows that see its 128-key tile are NaN.
+ */
+ORTHROS_API orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, const int32_t *kv_lens,
+                                                   const void *k_cache, const void *v_cache,
+                                                   const int32_t *block_table, int B, int n, int max_new, int Hq,
+                                                   int Hkv, int d, int window, float scale, orthros_dtype dtype,
+                                                   int max_pages, int page_size, int num_pages, void *o, float *lse,
+                                                   void *workspace, size_t workspace_bytes, orthros_stream_t stream);
+
 /*
  * Synchronises `stream`, reads the status word that the last call using
  * `workspace` left there and returns ORTHROS_OK, ORTHROS_EDEVICE (data bits) or

@@ -1,0 +1,306 @@
+"""orthros_chunk_attention (new tokens over a paged cache that holds their keys)
+against softmax attention in fp64.
+
+Tolerances, with S = max_j scale sum_c |q_c k_jc| of a row and A = sum_j p_j |v_j| / l:
+logits are 128 products accumulated in fp32, off by at most 128 * 2^-24 S; one
+exponential in 64 comes from a cubic that is off by 7.5e-5, the rest from
+ex2.approx (2^-22). So |lse| is off by at most 2^-17 S + 8e-5 + 2^-20 |lse| (sum, log,
+product with scale), and o by the same relative error of every weight and of the
+sum (2 (2^-17 S + 8e-5) A), by P's rounding to bf16 (half a step: 2^-8 A) and by its
+own (2^-8 |o|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import efficient_long_context_gb300 as ola
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from efficient_long_context_gb300 import build
+
+    build.build()
+    return ola.load_library()
+
+
+P = 1 << 12
+
+
+def _call(lib, **o):
+    a = dict(q=P, qi=P, kl=P, kc=P, vc=P, bt=P, B=2, n=3, mn=2, Hq=4, Hkv=2, d=64, w=8, sc=0.1, dt=0, mp=4, ps=16, np_=8,
+             o=P, lse=P, ws=P, wsb=1 << 30)
+    a.update(o)
+    return lib.orthros_chunk_attention(a["q"], a["qi"], a["kl"], a["kc"], a["vc"], a["bt"], a["B"], a["n"], a["mn"], a["Hq"],
+                                       a["Hkv"], a["d"], a["w"], a["sc"], a["dt"], a["mp"], a["ps"], a["np_"], a["o"],
+                                       a["lse"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(B=-1), 1), (dict(n=-1), 1), (dict(B=0), 1), (dict(mn=0), 1), (dict(Hq=3), 1), (dict(Hkv=0), 1), (dict(d=96), 2),
+    (dict(dt=1), 2), (dict(dt=9), 1), (dict(Hq=258, Hkv=2), 2), (dict(w=0), 1), (dict(sc=0.0), 1), (dict(sc=-1.0), 1),
+    (dict(sc=float("nan")), 1), (dict(sc=float("inf")), 1), (dict(mp=0), 1), (dict(ps=0), 1), (dict(np_=0), 1),
+    (dict(np_=1 << 28), 2), (dict(mp=1 << 28), 2), (dict(ws=None), 4), (dict(wsb=1024), 4), (dict(ws=P + 16), 1),
+    (dict(q=None), 1), (dict(o=None), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(qi=None), 1), (dict(kl=None), 1),
+    (dict(bt=None), 1), (dict(q=P + 8), 1), (dict(o=P + 8), 1), (dict(kc=P + 4), 1)])
+def test_refusals(lib, over, code):
+    assert _call(lib, **over) == code
+    assert ola.orthros_last_error() != ""
+
+
+def test_workspace_size(lib):
+    f = ola.orthros_chunk_attention_workspace_size
+    assert f(32, 32, 1, 32, 8, 128, 512, 64) > 0
+    assert f(32, 32, 1, 32, 8, 128, 512, 64) < f(32, 3200, 100, 32, 8, 128, 512, 64)
+    assert f(1, 100000, 100000, 32, 8, 128, 4096, 64) < 200 << 20  # partials do not grow with the tokens
+    assert f(0, 0, 0, 4, 2, 64, 1, 64) > 0
+    for bad in ((1, 4, 0, 4, 2, 64, 1, 64), (1, 4, 4, 4, 3, 64, 1, 64), (1, 4, 4, 4, 2, 32, 1, 64), (1, 4, 4, 4, 2, 64, 0, 64),
+                (0, 4, 4, 4, 2, 64, 1, 64)):
+        assert f(*bad) == 0
+    assert f(1, 4, 4, 4, 2, 64, 1, 64, torch.float32) == 0
+
+
+# ---------------------------------------------------------------------------
+# GPU parity
+# ---------------------------------------------------------------------------
+def make(new, total, Hq, Hkv, d, page, window, seed, spare=3, fill=float("nan"), qscale=1.5):
+    """A batch whose pages hold `fill` wherever no token of the batch looks."""
+    g = torch.Generator().manual_seed(seed)
+    B = len(new)
+    mp = max(1, max((t + page - 1) // page for t in total))
+    need = [(t + page - 1) // page for t in total]
+    pool = sum(need) + spare
+    perm = torch.randperm(pool, generator=g)
+    bt = torch.full((B, mp), pool + 7, dtype=torch.int32)  # entries nobody may follow
+    kc = torch.full((pool, page, Hkv, d), fill)
+    vc = torch.full((pool, page, Hkv, d), fill)
+    off = torch.randn(Hkv, d, generator=g) * 0.5
+    K, V = [], []
+    o = 0
+    for b in range(B):
+        k = torch.randn(total[b], Hkv, d, generator=g) + off
+        v = torch.randn(total[b], Hkv, d, generator=g)
+        K.append(k.bfloat16())
+        V.append(v.bfloat16())
+        first = max(0, total[b] - new[b] - window + 1) if new[b] else total[b]
+        for i in range(need[b]):
+            pg = int(perm[o + i])
+            lo, hi = max(i * page, first), min(total[b], (i + 1) * page)
+            if lo < hi:
+                bt[b, i] = pg
+                kc[pg, lo - i * page:hi - i * page] = K[b][lo:hi].float()
+                vc[pg, lo - i * page:hi - i * page] = V[b][lo:hi].float()
+        o += need[b]
+    n = sum(new)
+    q = (torch.randn(n, Hq, d, generator=g) * qscale).bfloat16()
+    indptr = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32)
+    return dict(q=q, K=K, V=V, kc=kc.bfloat16(), vc=vc.bfloat16(), bt=bt, indptr=indptr,
+                lens=torch.tensor(total, dtype=torch.int32), new=new, total=total, window=window)
+
+
+def plain(w, scale, rows=None):
+    """fp64 (o, lse, A, S) of the batch's rows, computed on the GPU in fp64."""
+    q = w["q"].cuda().double()
+    n, Hq, d = q.shape
+    out = [torch.empty(n, Hq, d, dtype=torch.float64, device="cuda"), torch.empty(n, Hq, dtype=torch.float64, device="cuda"),
+           torch.empty(n, Hq, d, dtype=torch.float64, device="cuda"), torch.empty(n, Hq, dtype=torch.float64, device="cuda")]
+    i0 = 0
+    for b, (nb, L) in enumerate(zip(w["new"], w["total"])):
+        if nb == 0:
+            continue
+        K, V = w["K"][b].cuda().double(), w["V"][b].cuda().double()
+        g = Hq // K.shape[1]
+        t = torch.arange(L - nb, L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")[None, :]
+        seen = (j <= t) & (j > t - w["window"])
+        for h in range(Hq):
+            qq, kk, vv = q[i0:i0 + nb, h], K[:, h // g], V[:, h // g]
+            z = (qq @ kk.T * scale).masked_fill(~seen, float("-inf"))
+            p = torch.softmax(z, -1)
+            out[0][i0:i0 + nb, h] = p @ vv
+            out[1][i0:i0 + nb, h] = torch.logsumexp(z, -1)
+            out[2][i0:i0 + nb, h] = p @ vv.abs()
+            out[3][i0:i0 + nb, h] = (qq.abs() @ kk.abs().T * scale).masked_fill(~seen, 0).amax(-1)
+        i0 += nb
+    return out
+
+
+def check(got, ref, what=""):
+    o, lse = got[0].double(), got[1].double()
+    ro, rl, A, S = ref
+    weight = 2.0 ** -17 * S + 8e-5
+    tol_l = weight + 2.0 ** -20 * rl.abs()
+    tol_o = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2 * weight[..., None]) * A + 1e-30
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all()), f"{what}: not finite"
+    el, eo = ((lse - rl).abs() / tol_l).max(), ((o - ro).abs() / tol_o).max()
+    assert float(el) <= 1 and float(eo) <= 1, f"{what}: lse {float(el):.3f}, o {float(eo):.3f} of the tolerance"
+
+
+def call(w, scale=None, **kw):
+    return ola.orthros_chunk_attention(w["q"].cuda(), w["indptr"].cuda(), w["lens"].cuda(), w["kc"].cuda(), w["vc"].cuda(),
+                                       w["bt"].cuda(), w["window"], scale, **kw)
+
+
+CASES = [
+    # new, total, Hq, Hkv, d, page, window
+    ([1], [1], 1, 1, 64, 64, 1 << 20),
+    ([1], [1], 32, 8, 128, 64, 1),
+    ([1], [129], 4, 2, 128, 64, 1 << 20),
+    ([1], [5000], 32, 8, 128, 64, 1 << 20),
+    ([1, 1, 1], [1, 700, 128], 8, 2, 128, 16, 1 << 20),
+    ([1, 1, 1, 1], [300, 2, 4097, 1000], 16, 16, 64, 128, 256),
+    ([3], [3], 4, 4, 64, 8, 1 << 20),
+    ([128], [128], 1, 1, 128, 64, 1 << 20),
+    ([129], [129], 2, 2, 128, 64, 1 << 20),
+    ([257], [1000], 1, 1, 64, 32, 100),
+    ([33], [33], 8, 2, 128, 48, 2),
+    ([70], [200], 32, 8, 128, 16, 127),
+    ([65, 0, 1, 31, 64], [65, 9, 400, 31, 777], 8, 2, 128, 24, 128),
+    ([300, 17], [5300, 17], 32, 8, 128, 64, 129),
+    ([300, 17], [5300, 17], 32, 8, 64, 64, 1 << 20),
+    ([700], [700], 16, 16, 128, 64, 512),
+    ([1000, 1, 500], [9000, 6000, 500], 12, 4, 128, 64, 4096),
+    ([40, 1, 3], [45, 260, 1003], 12, 1, 64, 16, 1 << 20),
+    ([9, 1], [500, 300], 40, 1, 128, 64, 1 << 20),
+    ([3, 2], [130, 5], 128, 1, 64, 8, 1 << 20),
+    ([5, 1], [400, 40], 3, 1, 64, 8, 77),
+    # page sizes without a copy box
+    ([1, 1], [300, 7], 8, 2, 128, 1, 1 << 20),
+    ([60, 1], [300, 129], 8, 2, 128, 5, 1 << 20),
+    ([200], [900], 4, 4, 64, 12, 130),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,total,Hq,Hkv,d,page,window", CASES,
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_parity(new, total, Hq, Hkv, d, page, window):
+    w = make(new, total, Hq, Hkv, d, page, window, seed=sum(total) + page)
+    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(len(new), sum(new), max(new), Hq, Hkv, d, w["bt"].shape[1],
+                                                                page), dtype=torch.uint8, device="cuda")
+    got = call(w, max_new=max(new), workspace=ws)
+    assert ola.orthros_check(ws) == (0, 0)
+    check(got, plain(w, d ** -0.5))
+    # the same call gives the same bits, whatever bound of the new tokens it is given
+    again = call(w)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 8, 128), (16, 16, 64)])
+def test_many_sequences(Hq, Hkv, d):
+    """More sequences than the plan's block has threads, one token or a few each, some none."""
+    rng = np.random.default_rng(1)
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 5], 1100)]
+    total = [n + int(h) for n, h in zip(new, rng.integers(0, 40, 1100))]
+    w = make(new, total, Hq, Hkv, d, 16, 20, seed=4)
+    check(call(w, max_new=5), plain(w, d ** -0.5))
+
+
+@pytest.mark.gpu
+def test_long_history_and_large_logits():
+    """One token over 40000 keys; logits in the hundreds, whose maxima keep moving."""
+    for qs in (1.0, 60.0):
+        w = make([1], [40000], 8, 2, 128, 64, 1 << 20, seed=6, qscale=qs)
+        check(call(w), plain(w, 128 ** -0.5), f"q scale {qs}")
+    w = make([130], [2000], 8, 2, 128, 64, 1 << 20, seed=7, qscale=60.0)
+    check(call(w), plain(w, 128 ** -0.5))
+    w = make([20], [700], 8, 2, 64, 64, 1 << 20, seed=8)
+    check(call(w, 0.7), plain(w, 0.7), "scale 0.7")
+    o, lse = ola.orthros_chunk_attention(w["q"].cuda(), w["indptr"].cuda(), w["lens"].cuda(), w["kc"].cuda(), w["vc"].cuda(),
+                                         w["bt"].cuda(), w["window"], 0.7, out=(torch.empty_like(w["q"].cuda()), None))
+    assert lse is None and torch.equal(o, call(w, 0.7)[0])
+
+
+@pytest.mark.gpu
+def test_pool_past_32_bit_offsets():
+    """Pages whose elements lie past 2^31 of the pool."""
+    page, Hkv, d = 64, 8, 128
+    pool = (1 << 31) // (page * Hkv * d) + 200
+    w = make([1, 40], [500, 900], 32, Hkv, d, page, 1 << 20, seed=9)
+    small = w["kc"].shape[0]
+    kc = torch.empty((pool, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty((pool, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    kc[pool - small:] = w["kc"].cuda()
+    vc[pool - small:] = w["vc"].cuda()
+    bt = torch.where(w["bt"] < small, w["bt"] + (pool - small), w["bt"])
+    got = ola.orthros_chunk_attention(w["q"].cuda(), w["indptr"].cuda(), w["lens"].cuda(), kc, vc, bt.cuda(), w["window"])
+    check(got, plain(w, d ** -0.5))
+
+
+@pytest.mark.gpu
+def test_bad_lengths_and_pages():
+    """Impossible data set their status bit and give NaN for the rows they concern, no others."""
+    new, total = [2, 70, 1], [300, 400, 90]
+    w = make(new, total, 8, 2, 64, 16, 1 << 20, seed=10)
+    ref = plain(w, 0.125)
+    rows = [slice(0, 2), slice(2, 72), slice(72, 73)]
+    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(3, 73, 73, 8, 2, 64, w["bt"].shape[1], 16),
+                     dtype=torch.uint8, device="cuda")
+
+    def expect(bad, bits, **kw):
+        v = dict(w, **kw)
+        o, lse = call(v, workspace=ws, max_new=kw.get("max_new", 73))
+        assert ola.orthros_check(ws) == (5, bits)
+        for b in range(3):
+            if b in bad:
+                assert bool(torch.isnan(o[rows[b]]).all()) and bool(torch.isnan(lse[rows[b]]).all())
+            else:
+                check((o[rows[b]], lse[rows[b]]), [r[rows[b]] for r in ref])
+
+    lens = lambda *v: torch.tensor(v, dtype=torch.int32)
+    expect([0], 4, lens=lens(1, 400, 90))                           # fewer cached tokens than new ones
+    expect([2], 4, lens=lens(300, 400, -5))
+    expect([1], 4, lens=lens(300, w["bt"].shape[1] * 16 + 1, 90))   # past the block table
+    expect([1], 4, max_new=69)
+    bt = w["bt"].clone()
+    bt[2, 0] = -1
+    expect([2], 2, bt=bt)
+    for indptr in ([0, 2, 72, 72], [1, 2, 72, 73], [0, 72, 2, 73], [0, 2, 72, 74]):
+        expect([0, 1, 2], 4, indptr=lens(*indptr))
+    # a bad page in the middle of a chunk's keys: rows whose keys stop before its tile are untouched
+    v = make([256], [256], 1, 1, 64, 16, 1 << 20, seed=11)
+    ref = plain(v, 0.125)
+    bt = v["bt"].clone()
+    bt[0, 9] = 1 << 20
+    o, lse = call(dict(v, bt=bt))
+    check((o[:128], lse[:128]), [r[:128] for r in ref])
+    assert bool(torch.isnan(o[128:]).all()) and bool(torch.isnan(lse[128:]).all())
+
+
+@pytest.mark.gpu
+def test_empty_calls():
+    w = make([0, 0], [5, 9], 4, 2, 64, 16, 8, seed=1)
+    o, lse = call(w)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.gpu
+def test_graph_replays_growing_lengths_and_side_stream():
+    """A captured step reads its lengths on the device: replayed with longer ones it follows them."""
+    w = make([1, 30], [1000, 700], 8, 2, 128, 64, 1 << 20, seed=12)
+    t = {k: w[k].cuda() for k in ("q", "indptr", "lens", "kc", "vc", "bt")}
+    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(2, 31, 30, 8, 2, 128, w["bt"].shape[1], 64),
+                     dtype=torch.uint8, device="cuda")
+
+    def step():
+        return ola.orthros_chunk_attention(t["q"], t["indptr"], t["lens"], t["kc"], t["vc"], t["bt"], 1 << 20, max_new=30,
+                                           workspace=ws)
+
+    t["lens"].copy_(torch.tensor([300, 40]))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for lens in ([300, 40], [999, 333], [1000, 700]):
+        t["lens"].copy_(torch.tensor(lens))
+        graph.replay()
+        v = dict(w, total=lens, K=[k[:n] for k, n in zip(w["K"], lens)], V=[x[:n] for x, n in zip(w["V"], lens)])
+        check(out, plain(v, 128 ** -0.5), str(lens))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        side = step()
+    s.synchronize()
+    assert torch.equal(side[0], out[0]) and torch.equal(side[1], out[1])
