@@ -557,6 +557,30 @@ def orthros_decode_static(q, k_new, v_new, k_cache, v_cache, block_table, cache_
     return o_base, lse_base, o_out, lse_out
 
 
+# The calls below are also made once per layer and decoding step on tensors of a
+# few hundred KB, where the marshalling is what takes the time: one look-up of
+# the current device and stream per call, plain integers for addresses.
+def _here():
+    """(current CUDA device, its current stream's handle); without a driver a
+    device that no tensor is on, so that every tensor is refused."""
+    if not torch.cuda.is_initialized():
+        try:
+            torch.cuda.init()
+        except RuntimeError:
+            return -2, None
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _addr(t, dev):
+    """_ptr for a known current device: the address as an integer (None for no or no elements)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise OrthrosError(1, f"tensor on {t.device}: every tensor argument must be on the current CUDA device")
+    return t.data_ptr() or None
+
+
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "stretch": 2, "bands": 3, "bands_tempered": 4}
 
@@ -567,37 +591,42 @@ def _rope_layout(layout) -> int:
     return _ROPE_LAYOUTS[layout]
 
 
-def _token_rows(name, t):
-    """Elements between the tokens of t [n, heads, d], whose tokens' heads must be contiguous."""
-    n, H, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+def _rows(name, t, dev, dtype, shape):
+    """(address, elements between tokens) of t [n, heads, d], whose tokens' heads must be contiguous."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype != dtype:
+        raise OrthrosError(1, f"{name} must be a {dtype} {list(shape)} tensor, not {t.dtype} {list(t.shape)}")
+    n, H, d = shape
+    st = t.stride()
+    if (st[2] != 1 or (H > 1 and st[1] != d)) and t.numel():
         raise OrthrosError(1, f"{name}: the heads of a token must be contiguous")
-    return int(t.stride(0)) if n > 1 else H * d
+    return _addr(t, dev), st[0] if n > 1 else H * d
 
 
-def _index(name, t, n):
-    """A contiguous int32 index tensor of n entries."""
-    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
+def _index(name, t, dev, n):
+    """Address of a contiguous int32 index tensor of n entries."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
         raise OrthrosError(1, f"{name} must be a contiguous int32 tensor of {n} entries")
-    return t
+    return _addr(t, dev)
 
 
-def _affine(name, t, H, d):
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (H, d)):
-        raise OrthrosError(1, f"{name} must be a contiguous float32 [{H}, {d}] tensor")
-    return t
+def _block(name, t, dev, dtype, shape):
+    """Address of a contiguous tensor of this type and shape."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise OrthrosError(1, f"{name} must be a contiguous {dtype} {list(shape)} tensor")
+    return _addr(t, dev)
 
 
-def _same_type(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise OrthrosError(1, f"{name} is {t.dtype}, not {dtype}")
-
-
-def _steps(t):
+def _steps(t, dev):
+    """(address, rotated channels) of a vector of rotary steps."""
     if t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous():
         raise OrthrosError(1, "steps must be a contiguous int64 vector (orthros_rotary_steps)")
-    return t
+    return _addr(t, dev), 2 * t.numel()
 
 
 def orthros_rotary_frequencies(rot_dim, base, scaling="plain", *, factor=1.0, original_length=0.0, low_turns=1.0,
@@ -635,17 +664,18 @@ def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=N
     x [n, H, d] (any token stride), positions [n] int32, steps from
     orthros_rotary_steps on the GPU. Returns y [n, H, d] (`out` may be x).
     """
-    lib = load_library()
-    n, H, d = x.shape
+    lib = _lib or load_library()
+    dev, here = _here()
+    shape = x.shape
+    n, H, d = shape
     if out is None:
-        out = torch.empty((n, H, d), dtype=x.dtype, device=x.device)
-    if tuple(out.shape) != (n, H, d):
-        raise OrthrosError(1, f"out has shape {tuple(out.shape)}, not {(n, H, d)}")
-    _same_type(x.dtype, out=out)
-    rc = lib.orthros_rotate(_ptr(x), _token_rows("x", x), _ptr(_index("positions", positions, n)),
-                            _ptr(_affine("alpha", alpha, H, d)), _ptr(_affine("beta", beta, H, d)), _ptr(_steps(steps)),
-                            2 * steps.numel(), _rope_layout(layout), float(amplitude), n, H, d, _dtype(x), _ptr(out),
-                            _token_rows("out", out), _stream(stream))
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    xa, xs = _rows("x", x, dev, x.dtype, shape)
+    ya, ys = _rows("out", out, dev, x.dtype, shape)
+    st, rot = _steps(steps, dev)
+    rc = lib.orthros_rotate(xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)),
+                            _block("beta", beta, dev, torch.float32, (H, d)), st, rot, _rope_layout(layout), amplitude, n, H,
+                            d, _dtype(x), ya, ys, here if stream is None else _stream(stream))
     _raise_if(rc, lib)
     return out
 
@@ -662,25 +692,27 @@ def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude
     Returns (dx, d_alpha, d_beta), the last two float [H, d], or None without
     affine_grads; `out` gives the three tensors.
     """
-    lib = load_library()
-    n, H, d = dy.shape
+    lib = _lib or load_library()
+    dev, here = _here()
+    shape, dtype = dy.shape, dy.dtype
+    n, H, d = shape
     if out is None:
-        out = (torch.empty((n, H, d), dtype=dy.dtype, device=dy.device),
+        out = (torch.empty(shape, dtype=dtype, device=dy.device),
                torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None,
                torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None)
     dx, da, db = out
-    if tuple(dx.shape) != (n, H, d) or (x is not None and tuple(x.shape) != (n, H, d)):
-        raise OrthrosError(1, f"x and dx must have the shape of dy, {(n, H, d)}")
-    _same_type(dy.dtype, x=x, dx=dx)
     if workspace is None and da is not None:
-        workspace = torch.empty(max(orthros_rotate_backward_workspace_size(n, H, d, dy.dtype), 256),
+        workspace = torch.empty(max(orthros_rotate_backward_workspace_size(n, H, d, dtype), 256),
                                 dtype=torch.uint8, device=dy.device)
+    ga, gs = _rows("dy", dy, dev, dtype, shape)
+    xa, xs = _rows("x", x, dev, dtype, shape)
+    oa, os_ = _rows("dx", dx, dev, dtype, shape)
+    st, rot = _steps(steps, dev)
     rc = lib.orthros_rotate_backward(
-        _ptr(dy), _token_rows("dy", dy), _ptr(x), _token_rows("x", x) if x is not None else 0,
-        _ptr(_index("positions", positions, n)), _ptr(_affine("alpha", alpha, H, d)), _ptr(_steps(steps)),
-        2 * steps.numel(), _rope_layout(layout), float(amplitude), n, H, d, _dtype(dy), _ptr(dx),
-        _token_rows("dx", dx), _ptr(_affine("d_alpha", da, H, d)), _ptr(_affine("d_beta", db, H, d)), _ptr(workspace),
-        workspace.numel() if workspace is not None else 0, _stream(stream))
+        ga, gs, xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)), st, rot,
+        _rope_layout(layout), amplitude, n, H, d, _dtype(dy), oa, os_, _block("d_alpha", da, dev, torch.float32, (H, d)),
+        _block("d_beta", db, dev, torch.float32, (H, d)), _addr(workspace, dev),
+        workspace.numel() if workspace is not None else 0, here if stream is None else _stream(stream))
     _raise_if(rc, lib)
     return dx, da, db
 
@@ -694,37 +726,36 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     d] (or None) and q_out [n_out, Hq, d] are rotated. Returns (q_rot or None,
     q_out_rot or None); k_cache / v_cache are updated in place.
     """
-    lib = load_library()
+    lib = _lib or load_library()
+    dev, here = _here()
+    dtype = k_new.dtype
     n, Hkv, d = k_new.shape
     n_out = q_out.shape[0] if q_out is not None else 0
     Hq = q.shape[1] if q is not None else (q_out.shape[1] if q_out is not None else Hkv)
-    num_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    num_pages, page_size = k_cache.shape[:2]
     B, max_pages = block_table.shape
-    for name, t, rows, heads in (("q", q, n, Hq), ("q_out", q_out, n_out, Hq), ("v_new", v_new, n, Hkv)):
-        if t is not None and tuple(t.shape) != (rows, heads, d):
-            raise OrthrosError(1, f"{name} has shape {tuple(t.shape)}, not {(rows, heads, d)}")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if tuple(t.shape) != (num_pages, page_size, Hkv, d) or not t.is_contiguous():
-            raise OrthrosError(1, f"{name} must be a contiguous [{num_pages}, {page_size}, {Hkv}, {d}] tensor")
-    _same_type(k_new.dtype, q=q, q_out=q_out, v_new=v_new, k_cache=k_cache, v_cache=v_cache)
     if out is None:
-        out = (torch.empty((n, Hq, d), dtype=q.dtype, device=q.device) if q is not None else None,
-               torch.empty((n_out, Hq, d), dtype=q_out.dtype, device=q_out.device) if q_out is not None else None)
+        out = (torch.empty((n, Hq, d), dtype=dtype, device=k_new.device) if q is not None else None,
+               torch.empty((n_out, Hq, d), dtype=dtype, device=k_new.device) if q_out is not None else None)
     q_rot, q_out_rot = out
-    for name, t in (("q_rot", q_rot), ("q_out_rot", q_out_rot)):
-        _contig(name, t)
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=k_new.device)
+    qa, qs = _rows("q", q, dev, dtype, (n, Hq, d))
+    qoa, qos = _rows("q_out", q_out, dev, dtype, (n_out, Hq, d))
+    ka, ks = _rows("k_new", k_new, dev, dtype, (n, Hkv, d))
+    va, vs = _rows("v_new", v_new, dev, dtype, (n, Hkv, d))
+    aff = [_block(name, t, dev, torch.float32, (Hq, d)) for name, t in
+           (("alpha_base", alpha_base), ("beta_base", beta_base), ("alpha_out", alpha_out), ("beta_out", beta_out))]
+    st, rot = _steps(steps, dev)
+    pool = (num_pages, page_size, Hkv, d)
     rc = lib.orthros_rotate_append(
-        _ptr(q), _token_rows("q", q) if q is not None else 0, _ptr(q_out),
-        _token_rows("q_out", q_out) if q_out is not None else 0, _ptr(k_new), _token_rows("k_new", k_new), _ptr(v_new),
-        _token_rows("v_new", v_new), _ptr(_affine("alpha_base", alpha_base, Hq, d)),
-        _ptr(_affine("beta_base", beta_base, Hq, d)), _ptr(_affine("alpha_out", alpha_out, Hq, d)),
-        _ptr(_affine("beta_out", beta_out, Hq, d)), _ptr(_steps(steps)), 2 * steps.numel(), _rope_layout(layout),
-        float(amplitude), _ptr(_index("token_seq", token_seq, n)), _ptr(_index("token_pos", token_pos, n)),
-        _ptr(_index("out_positions", out_positions, n_out)), n, n_out, Hq, Hkv, d, _dtype(k_new), _ptr(q_rot),
-        _ptr(q_out_rot), _ptr(k_cache), _ptr(v_cache), _ptr(_index("block_table", block_table, B * max_pages)), B,
-        max_pages, page_size, num_pages, _ptr(workspace), workspace.numel(), _stream(stream))
+        qa, qs, qoa, qos, ka, ks, va, vs, *aff, st, rot, _rope_layout(layout), amplitude,
+        _index("token_seq", token_seq, dev, n), _index("token_pos", token_pos, dev, n),
+        _index("out_positions", out_positions, dev, n_out), n, n_out, Hq, Hkv, d, _dtype(k_new),
+        _block("q_rot", q_rot, dev, dtype, (n, Hq, d)), _block("q_out_rot", q_out_rot, dev, dtype, (n_out, Hq, d)),
+        _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
+        _index("block_table", block_table, dev, B * max_pages), B, max_pages, page_size, num_pages, _addr(workspace, dev),
+        workspace.numel(), here if stream is None else _stream(stream))
     _raise_if(rc, lib)
     return q_rot, q_out_rot
 
@@ -743,36 +774,29 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     q_indptr and kv_lens are int32 tensors on the GPU. max_new bounds the new
     tokens of a sequence (default n). Returns (o [n, Hq, d], lse [n, Hq]).
     """
-    lib = load_library()
-    n, Hq, d = q.shape
+    lib = _lib or load_library()
+    dev, here = _here()
+    shape, dtype = q.shape, q.dtype
+    n, Hq, d = shape
     num_pages, page_size, Hkv = k_cache.shape[:3]
     B, max_pages = block_table.shape
-    if scale is None:
-        scale = d ** -0.5
     if max_new is None:
         max_new = n
-    _contig("q", q)
-    if tuple(k_cache.shape) != (num_pages, page_size, Hkv, d) or tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise OrthrosError(1, f"k_cache and v_cache must both be [num_pages, page_size, Hkv, {d}]")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _contig(name, t)
-    _same_type(q.dtype, k_cache=k_cache, v_cache=v_cache)
     if out is None:
-        out = (torch.empty_like(q), torch.empty((n, Hq), dtype=torch.float32, device=q.device))
+        out = (torch.empty(shape, dtype=dtype, device=q.device),
+               torch.empty((n, Hq), dtype=torch.float32, device=q.device))
     o, lse = out
-    if tuple(o.shape) != (n, Hq, d) or (lse is not None and (tuple(lse.shape) != (n, Hq) or lse.dtype != torch.float32)):
-        raise OrthrosError(1, f"out must be (o {(n, Hq, d)}, lse float32 {(n, Hq)} or None)")
-    _same_type(q.dtype, o=o)
-    for name, t in (("o", o), ("lse", lse)):
-        _contig(name, t)
     if workspace is None:
-        ws = orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, q.dtype)
+        ws = orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype)
         workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=q.device)
+    pool = (num_pages, page_size, Hkv, d)
     rc = lib.orthros_chunk_attention(
-        _ptr(q), _ptr(_index("q_indptr", q_indptr, B + 1)), _ptr(_index("kv_lens", kv_lens, B)), _ptr(k_cache),
-        _ptr(v_cache), _ptr(_index("block_table", block_table, B * max_pages)), B, n, int(max_new), Hq, Hkv, d,
-        int(window), float(scale), _dtype(q), max_pages, page_size, num_pages, _ptr(o), _ptr(lse), _ptr(workspace),
-        workspace.numel(), _stream(stream))
+        _block("q", q, dev, dtype, shape), _index("q_indptr", q_indptr, dev, B + 1), _index("kv_lens", kv_lens, dev, B),
+        _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
+        _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq, Hkv, d, window,
+        d ** -0.5 if scale is None else scale, _dtype(q), max_pages, page_size, num_pages,
+        _block("o", o, dev, dtype, shape), _block("lse", lse, dev, torch.float32, (n, Hq)), _addr(workspace, dev),
+        workspace.numel(), here if stream is None else _stream(stream))
     _raise_if(rc, lib)
     return o, lse
 

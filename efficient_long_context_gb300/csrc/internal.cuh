@@ -283,7 +283,7 @@ cudaError_t launch_project_tc(const ProjParams &p, cudaStream_t stream);
 
 // rotary.cu: rotary positions (orthros_rotate, _backward, _append).
 struct RotateParams {
-    const void *x;
+    const void *x;  // [n, H, d] (append: the base stream's queries, or null)
     void *y;
     long long x_stride, y_stride;  // elements between tokens
     const int32_t *positions;
@@ -293,6 +293,21 @@ struct RotateParams {
     int H, rot, heads_per_block;  // heads_per_block: set by the launcher
     bool interleaved;
     float amplitude;
+    // append only: the output stream's queries, and the new tokens' keys and values
+    const void *x_out;
+    void *y_out;
+    long long x_out_stride;
+    const float *alpha_out, *beta_out;
+    const int32_t *out_positions;
+    int n_out;
+    const void *k, *v;
+    long long k_stride, v_stride;
+    const int32_t *token_seq, *block_table;
+    void *k_cache, *v_cache;
+    int Hkv, B, max_pages, page_size, num_pages;
+    uint32_t *status;
+    bool status_here;  // one block writes the whole status word (short calls), else a launch resets it
+    int blocks;        // set by the launcher: blocks along the new tokens
 };
 struct RotateBwdParams {
     const void *dy, *x;
@@ -309,24 +324,11 @@ struct RotateBwdParams {
     int n_part;
     float *d_alpha, *d_beta;  // both null: not wanted
 };
-struct RotateAppendParams {
-    const void *q, *q_out, *k, *v;  // q, q_out may be null
-    long long q_stride, q_out_stride, k_stride, v_stride;
-    const float *alpha_base, *beta_base, *alpha_out, *beta_out;
-    const uint64_t *steps;
-    const int32_t *token_seq, *token_pos, *out_positions, *block_table;
-    int n_new, n_out, Hq, Hkv, rot, heads_per_block;
-    bool interleaved;
-    float amplitude;
-    void *q_rot, *q_out_rot, *k_cache, *v_cache;
-    int B, max_pages, page_size, num_pages;
-    uint32_t *status;
-};
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes);
 cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t stream);
-cudaError_t launch_rotate_append(const RotateAppendParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
+cudaError_t launch_rotate_append(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 
 // chunk_attn.cu: attention of new tokens over the paged cache (orthros_chunk_attention).
 // A unit is up to two 128-row query tiles of one sequence (a row is one query

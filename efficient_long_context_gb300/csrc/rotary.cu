@@ -23,11 +23,14 @@
 namespace orthros {
 namespace {
 
-// A row (one head of one token) is moved in work items of two 16-byte vectors:
-// a rotated item holds VEC pairs (vectors i and i + rot/2/VEC in the half
-// layout, vectors 2i and 2i + 1 in the interleaved one); the channels past
-// `rot` are items of two consecutive vectors. rot is a multiple of 16, so no
-// vector is split between the two kinds.
+// A row (one head of one token) is moved in work items of two 16-byte vectors.
+// Half layout: a rotated item holds the two vectors of VEC pairs, i and i +
+// rot/2/VEC; the channels past `rot` are items of two consecutive vectors.
+// Interleaved layout: pairs lie within a vector, so item i takes vectors i and
+// i + D/2/VEC, and neighbouring lanes move neighbouring vectors (two consecutive
+// vectors per lane left every 32-byte sector to two instructions: 189 against
+// 133 us for 32768 x 32 x 128 bf16). rot is a multiple of 16, so every vector is
+// rotated or not as a whole.
 template <typename T> struct Vec {
     static constexpr int kN = 16 / (int)sizeof(T);
 };
@@ -70,33 +73,52 @@ __device__ __forceinline__ void angle(int t, uint64_t step, float amp, float &c,
     s *= amp;
 }
 
-// Where the two vectors of item i start, in channels.
-template <int VEC>
-__device__ __forceinline__ void item_channels(int i, int rot, bool interleaved, int &ca, int &cb) {
-    const bool split = !interleaved && 2 * VEC * i < rot;  // a rotated item of the half layout
-    ca = split ? VEC * i : 2 * VEC * i;
-    cb = split ? VEC * i + (rot >> 1) : 2 * VEC * i + VEC;
-}
+// The two vectors of a work item: first channels, and which of them rotate.
+// Pair j of the item's angles is pair first_a + j (vector a and, in the half
+// layout, b) for j < n_a, and first_b + j - VEC/2 for an interleaved vector b.
+template <int VEC, int D> struct Item {
+    int ca, cb;
+    bool ra, rb;
+    __device__ __forceinline__ Item(int i, int rot, bool interleaved) {
+        const bool split = !interleaved && 2 * VEC * i < rot;  // a rotated item of the half layout
+        ca = interleaved || split ? VEC * i : 2 * VEC * i;
+        cb = interleaved ? ca + D / 2 : split ? ca + (rot >> 1) : ca + VEC;
+        ra = interleaved ? ca < rot : split;
+        rb = interleaved ? cb < rot : split;
+    }
+    // pair of the item's j-th angle (interleaved: the first VEC/2 are vector a's, the others b's)
+    __device__ __forceinline__ int pair(int j, bool interleaved) const {
+        return !interleaved ? ca + j : j < VEC / 2 ? ca / 2 + j : cb / 2 + j - VEC / 2;
+    }
+    __device__ __forceinline__ bool turns(int j, bool interleaved) const {
+        return !interleaved || j < VEC / 2 ? ra : rb;
+    }
+};
 
 // Rotates the pairs of an item in place: (a[j], b[j]) in the half layout,
 // neighbours of the 2 VEC channels in the interleaved one.
-template <int VEC>
+template <int VEC, int D>
 __device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC], const float (&s)[VEC],
-                                     bool interleaved) {
+                                     const Item<VEC, D> &it, bool interleaved) {
     if (!interleaved) {
+        if (!it.ra) return;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             const float x = a[j], y = b[j];
             a[j] = fmaf(x, c[j], -y * s[j]);
             b[j] = fmaf(x, s[j], y * c[j]);
         }
-    } else {
+        return;
+    }
+    if (it.ra) {
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             const float x = a[2 * j], y = a[2 * j + 1];
             a[2 * j] = fmaf(x, c[j], -y * s[j]);
             a[2 * j + 1] = fmaf(x, s[j], y * c[j]);
         }
+    }
+    if (it.rb) {
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             const float x = b[2 * j], y = b[2 * j + 1];
@@ -117,160 +139,226 @@ __device__ __forceinline__ void load_affine(const float *p, int ca, int cb, floa
     }
 }
 
-// ---------------------------------------------------------------------------
-// Forward. A thread owns one (token, item) and walks heads, so the item's
-// cosines and sines stay in registers; a warp's lanes are the items of a few
-// tokens at the same head, so its affine loads are shared. Bound by HBM: every
-// element read once and written once.
-// ---------------------------------------------------------------------------
-constexpr int kFwdThreads = 128;
-constexpr int kHeadsInFlight = 4;  // heads whose loads a thread has in flight
-
-// Heads [h0, h1) of one token's item: src and dst point at the token's head 0.
-template <typename T, int D>
-__device__ __forceinline__ void rotate_heads(const T *src, T *dst, int h0, int h1, int ca, int cb, bool rotated,
-                                             bool interleaved, const float *alpha, const float *beta,
-                                             const float (&c)[Vec<T>::kN], const float (&s)[Vec<T>::kN]) {
-    constexpr int VEC = Vec<T>::kN;
-    for (int hb = h0; hb < h1; hb += kHeadsInFlight) {
-        uint4 ra[kHeadsInFlight], rb[kHeadsInFlight];
-#pragma unroll
-        for (int u = 0; u < kHeadsInFlight; ++u) {
-            if (hb + u < h1) {
-                ra[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (hb + u) * D + ca));
-                rb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (hb + u) * D + cb));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kHeadsInFlight; ++u) {
-            if (hb + u >= h1) break;
-            float a[VEC], b[VEC];
-            unpack<T>(ra[u], a);
-            unpack<T>(rb[u], b);
-            if (alpha) {
-                float ka[VEC], kb[VEC];
-                load_affine<VEC>(alpha + (hb + u) * D, ca, cb, ka, kb);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) a[j] *= ka[j], b[j] *= kb[j];
-                load_affine<VEC>(beta + (hb + u) * D, ca, cb, ka, kb);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) a[j] += ka[j], b[j] += kb[j];
-            }
-            if (rotated) turn<VEC>(a, b, c, s, interleaved);
-            *reinterpret_cast<uint4 *>(dst + (hb + u) * D + ca) = pack<T>(a);
-            *reinterpret_cast<uint4 *>(dst + (hb + u) * D + cb) = pack<T>(b);
+// Cosines and sines of a few tokens, computed once by the block and shared by its
+// heads: entry (token, j / 2, item) holds angles j and j + 1 of the item, so the
+// lanes of a row read consecutive 16-byte words.
+constexpr int kTabTokens = 16;  // at most
+constexpr int kRunTokens = 64;  // positions (and page slots) a block looks up at a time
+// Tokens of a table (a divisor of kRunTokens): two batches' worth of loads of one
+// token a thread; more when tokens go side by side. A longer table delays its
+// first rows (16 and 32 tokens: 1 and 5 % at 32 heads).
+__device__ __forceinline__ int table_tokens(int lanes) { return lanes > 1 ? kTabTokens : kTabTokens / 2; }
+template <typename T, int D> struct Table {
+    static constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kQ = VEC / 2;
+    float4 e[kTabTokens][kQ][IPR];
+    // angles of cnt positions; sign -1 for the transposed rotation
+    __device__ __forceinline__ void fill(const int *pos, int cnt, const uint64_t *steps, int rot, bool interleaved, float amp,
+                                         float sign) {
+        const int half = rot >> 1;
+        for (int x = threadIdx.x; x < cnt * half; x += blockDim.x) {
+            const int k = x / half, pr = x % half;
+            float c, s;
+            angle(pos[k], __ldg(steps + pr), amp, c, s);
+            int i, j;  // the item and its angle that pair pr is
+            if (!interleaved) i = pr / VEC, j = pr % VEC;
+            else i = (pr % (D / 4)) / kQ, j = pr % kQ + (pr >= D / 4 ? kQ : 0);
+            reinterpret_cast<float2 *>(&e[k][j / 2][i])[j & 1] = make_float2(c, sign * s);
         }
     }
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kFwdThreads) rotate_kernel(const RotateParams p) {
-    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
-    const long long gid = (long long)blockIdx.x * kFwdThreads + threadIdx.x;
-    const long long tok = gid / IPR;
-    const int item = (int)(gid % IPR);
-    if (tok >= p.n) return;
-    const bool rotated = 2 * VEC * item < p.rot;
-    int ca, cb;
-    item_channels<VEC>(item, p.rot, p.interleaved, ca, cb);
-    float c[VEC], s[VEC];
-    if (rotated) {
-        const int t = p.positions[tok];
+    __device__ __forceinline__ void read(int k, int item, float (&c)[VEC], float (&s)[VEC]) const {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) angle(t, __ldg(p.steps + VEC * item + j), p.amplitude, c[j], s[j]);
-    }
-    const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.H, h0 + p.heads_per_block);
-    rotate_heads<T, D>(static_cast<const T *>(p.x) + tok * p.x_stride, static_cast<T *>(p.y) + tok * p.y_stride, h0, h1,
-                       ca, cb, rotated, p.interleaved, p.alpha, p.beta, c, s);
-}
-
-// ---------------------------------------------------------------------------
-// Append. Rows 0 .. n_new - 1 are the new tokens: their queries (base stream)
-// are rotated to q_rot, their keys rotated into the page slot, their values
-// copied there. Rows n_new .. n_new + n_out - 1 are the output stream's
-// queries. The virtual heads of a token are its Hq query heads, Hkv key heads
-// and Hkv value heads, cut over blockIdx.y.
-// ---------------------------------------------------------------------------
-template <typename T, int D>
-__global__ void __launch_bounds__(kFwdThreads) rotate_append_kernel(const RotateAppendParams p) {
-    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
-    const long long gid = (long long)blockIdx.x * kFwdThreads + threadIdx.x;
-    const long long row = gid / IPR;
-    const int item = (int)(gid % IPR);
-    if (row >= (long long)p.n_new + p.n_out) return;
-    const bool out = row >= p.n_new;
-    const int nq = (out ? p.q_out : p.q) ? p.Hq : 0;
-    const int v0 = blockIdx.y * p.heads_per_block, v1 = v0 + p.heads_per_block;  // virtual heads
-    const int nv = nq + (out ? 0 : 2 * p.Hkv);
-    if (v0 >= nv) return;
-    const bool rotated = 2 * VEC * item < p.rot;
-    int ca, cb;
-    item_channels<VEC>(item, p.rot, p.interleaved, ca, cb);
-    const int t = out ? p.out_positions[row - p.n_new] : p.token_pos[row];
-    float c[VEC], s[VEC];
-    if (rotated && v0 < nq + p.Hkv) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) angle(t, __ldg(p.steps + VEC * item + j), p.amplitude, c[j], s[j]);
-    }
-    if (v0 < nq) {
-        const int h1 = min(nq, v1);
-        if (out) {
-            const long long r = row - p.n_new;
-            rotate_heads<T, D>(static_cast<const T *>(p.q_out) + r * p.q_out_stride,
-                               static_cast<T *>(p.q_out_rot) + r * p.Hq * D, v0, h1, ca, cb, rotated, p.interleaved,
-                               p.alpha_out, p.beta_out, c, s);
-        } else {
-            rotate_heads<T, D>(static_cast<const T *>(p.q) + row * p.q_stride,
-                               static_cast<T *>(p.q_rot) + row * p.Hq * D, v0, h1, ca, cb, rotated, p.interleaved,
-                               p.alpha_base, p.beta_base, c, s);
+        for (int q = 0; q < kQ; ++q) {
+            const float4 v = e[k][q][item];
+            c[2 * q] = v.x, s[2 * q] = v.y, c[2 * q + 1] = v.z, s[2 * q + 1] = v.w;
         }
     }
-    if (out || v1 <= nq) return;
-    // the token's page slot
-    const int b = p.token_seq[row];
+};
+
+// ---------------------------------------------------------------------------
+// Forward and append: one kernel moves rows. A thread owns one (head, item) with
+// the affine's channels in registers and walks the tokens of its block, kBatch
+// tokens' loads in flight; the angles come from the block's table. Blocks take
+// equal runs of tokens, as many as fit the GPU at once. Bound by HBM: every
+// element read once and written once. 32768 x 32 x 128 bf16 with the affine: 86 us,
+// 6.2 TB/s (92 % of the measured copy rate). Threads that owned a token and
+// walked its heads read the affine from L1 for every head (116 us, L1 70 % busy);
+// two tokens in flight instead of four, 117 us; eight do not fit the registers.
+//
+// The virtual heads of a token are its Hq query heads, then (append) its Hkv key
+// heads and Hkv value heads. Blocks from p.blocks on (along x) move the output
+// stream's rows.
+// ---------------------------------------------------------------------------
+constexpr int kMoveThreads = 512;  // at most
+constexpr int kBatch = 4;
+
+// Token slot of new token i in the page pool; wrong: its status bit when it has none.
+__device__ __forceinline__ long long page_slot(const RotateParams &p, long long i, uint32_t &wrong) {
+    const int b = p.token_seq[i], t = p.positions[i];
     if (b < 0 || b >= p.B || t < 0 || t / p.page_size >= p.max_pages) {
-        if (item == 0) set_status(p.status, ORTHROS_DEV_BAD_POSITION);
-        return;
+        wrong |= ORTHROS_DEV_BAD_POSITION;
+        return 0;
     }
     const int pg = p.block_table[(long long)b * p.max_pages + t / p.page_size];
     if (pg < 0 || pg >= p.num_pages) {
-        if (item == 0) set_status(p.status, ORTHROS_DEV_BAD_PAGE);
-        return;
+        wrong |= ORTHROS_DEV_BAD_PAGE;
+        return 0;
     }
-    const long long slot = ((long long)pg * p.page_size + t % p.page_size) * p.Hkv * D;
-    const int k0 = max(v0 - nq, 0), k1 = min(v1 - nq, p.Hkv);
-    if (k0 < k1)
-        rotate_heads<T, D>(static_cast<const T *>(p.k) + row * p.k_stride, static_cast<T *>(p.k_cache) + slot, k0, k1,
-                           ca, cb, rotated, p.interleaved, nullptr, nullptr, c, s);
-    const T *vs = static_cast<const T *>(p.v) + row * p.v_stride;
-    T *vd = static_cast<T *>(p.v_cache) + slot;
-    for (int h = max(v0 - nq - p.Hkv, 0); h < min(v1 - nq - p.Hkv, p.Hkv); ++h) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(vs + h * D + ca));
-        const uint4 b2 = __ldcs(reinterpret_cast<const uint4 *>(vs + h * D + cb));
-        *reinterpret_cast<uint4 *>(vd + h * D + ca) = a;
-        *reinterpret_cast<uint4 *>(vd + h * D + cb) = b2;
+    return (long long)pg * p.page_size + t % p.page_size;
+}
+
+// The status word of an append: one block checks every new token and writes the
+// word, with no reset before it and no atomics.
+__device__ __forceinline__ void write_status(const RotateParams &p) {
+    uint32_t wrong = 0;
+    for (long long i = threadIdx.x; i < p.n; i += blockDim.x) page_slot(p, i, wrong);
+    const int pos = __syncthreads_or(wrong & ORTHROS_DEV_BAD_POSITION), pg = __syncthreads_or(wrong & ORTHROS_DEV_BAD_PAGE);
+    if (threadIdx.x == 0) *p.status = (pos ? ORTHROS_DEV_BAD_POSITION : 0u) | (pg ? ORTHROS_DEV_BAD_PAGE : 0u);
+}
+
+// The reset of a long append's status word, which the moving kernel starts beside;
+// only a block that found something wrong waits for it before it adds its bit.
+__global__ void rotate_status_reset_kernel(uint32_t *status) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) *status = 0;
+}
+
+template <typename T, int D, bool kAppend>
+__global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateParams p) {
+    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
+    __shared__ Table<T, D> tab[2];
+    __shared__ int pos[kRunTokens];
+    __shared__ long long slot[kRunTokens];  // append: first element of the token's page slot, or -1
+    const int tid = threadIdx.x;
+    const int hb = p.heads_per_block;
+    const int lanes = blockDim.x / (hb * IPR);  // tokens handled side by side
+    const int tl = tid / (hb * IPR);
+    const int h = blockIdx.y * hb + (tid / IPR) % hb;
+    const int item = tid % IPR;
+    const bool out = kAppend && (int)blockIdx.x >= p.blocks;
+    const int bx = out ? blockIdx.x - p.blocks : blockIdx.x, nbx = out ? gridDim.x - p.blocks : p.blocks;
+    const long long n = out ? p.n_out : p.n;
+    const int32_t *positions = out ? p.out_positions : p.positions;
+    // what this thread's virtual head moves
+    const T *src = static_cast<const T *>(out ? p.x_out : p.x);
+    T *dst = static_cast<T *>(out ? p.y_out : p.y);
+    long long ss = out ? p.x_out_stride : p.x_stride, ds = p.y_stride;
+    const float *alpha = out ? p.alpha_out : p.alpha, *beta = out ? p.beta_out : p.beta;
+    int hh = h;                  // head within its tensor
+    bool paged = false, value = false;
+    if (kAppend && h >= p.H) {
+        hh = h - p.H;
+        paged = true;
+        value = hh >= p.Hkv;
+        if (value) hh -= p.Hkv;
+        src = static_cast<const T *>(value ? p.v : p.k);
+        dst = static_cast<T *>(value ? p.v_cache : p.k_cache);
+        ss = value ? p.v_stride : p.k_stride;
+        alpha = beta = nullptr;
     }
+    const bool active = tl < lanes && (kAppend ? (paged ? !out && h < p.H + 2 * p.Hkv : src != nullptr) : h < p.H);
+    Item<VEC, D> it(item, p.rot, p.interleaved);
+    if (value) it.ra = it.rb = false;
+    src += hh * D;
+    dst += hh * D;
+    float al[2][VEC], be[2][VEC];
+    const bool affine = active && alpha;
+    if (affine) {
+        load_affine<VEC>(alpha + hh * D, it.ca, it.cb, al[0], al[1]);
+        load_affine<VEC>(beta + hh * D, it.ca, it.cb, be[0], be[1]);
+    }
+    if (kAppend && p.status_here && blockIdx.x == 0 && blockIdx.y == 0) write_status(p);  // a short call's
+    const long long n0 = n * bx / nbx, n1 = n * (bx + 1) / nbx;
+    const int step = table_tokens(lanes);
+    int buf = 0;
+    for (long long base = n0; base < n1; base += step, buf ^= 1) {
+        const int cnt = (int)min((long long)step, n1 - base);
+        const int run = (int)((base - n0) % kRunTokens);  // first entry of these tokens in pos and slot
+        // the first batch's loads are under way while the angles are computed
+        uint4 ra[kBatch], rb[kBatch];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * lanes;
+                if (k < cnt) {
+                    ra[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (base + k) * ss + it.ca));
+                    rb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (base + k) * ss + it.cb));
+                }
+            }
+        };
+        if (active) load(tl);
+        if (run == 0) {
+            __syncthreads();  // the last run's entries have been used
+            for (int k = tid; k < kRunTokens && base + k < n1; k += blockDim.x) {
+                pos[k] = positions[base + k];
+                if (kAppend && !out) {
+                    uint32_t wrong = 0;
+                    const long long at = page_slot(p, base + k, wrong);
+                    slot[k] = wrong ? -1 : at * p.Hkv * D;
+                    if (wrong && !p.status_here) {
+                        asm volatile("griddepcontrol.wait;" ::: "memory");
+                        set_status(p.status, wrong);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        tab[buf].fill(pos + run, cnt, p.steps, p.rot, p.interleaved, p.amplitude, 1.f);
+        __syncthreads();
+        if (!active) continue;
+        for (int k0 = tl; k0 < cnt; k0 += kBatch * lanes) {
+            if (k0 != tl) load(k0);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * lanes;
+                if (k >= cnt) break;
+                T *to = kAppend && paged ? dst + slot[run + k] : dst + (base + k) * ds;
+                if (kAppend && paged && slot[run + k] < 0) continue;
+                if (value) {
+                    *reinterpret_cast<uint4 *>(to + it.ca) = ra[u];
+                    *reinterpret_cast<uint4 *>(to + it.cb) = rb[u];
+                    continue;
+                }
+                float a[VEC], b[VEC], c[VEC], s[VEC];
+                unpack<T>(ra[u], a);
+                unpack<T>(rb[u], b);
+                if (affine) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        a[j] = fmaf(a[j], al[0][j], be[0][j]);
+                        b[j] = fmaf(b[j], al[1][j], be[1][j]);
+                    }
+                }
+                tab[buf].read(k, item, c, s);
+                turn<VEC, D>(a, b, c, s, it, p.interleaved);
+                *reinterpret_cast<uint4 *>(to + it.ca) = pack<T>(a);
+                *reinterpret_cast<uint4 *>(to + it.cb) = pack<T>(b);
+            }
+        }
+    }
+    // (append) the call is complete when the status word's reset is, too
+    if (kAppend) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
-// Backward. A block covers a range of tokens and a group of heads; a thread
-// owns one (head, item) and walks the block's tokens with the affine's gradient
-// in registers, so d_alpha and d_beta cost no traffic per token. The angles of
-// kTabTokens tokens at a time are computed once by the block and shared by its
-// heads. The block's sums go to the workspace as one partial each, and
-// rotate_grad_sum_kernel adds the partials in a fixed order (no atomics: the
-// same call gives the same bits). Bound by HBM: dy and x read once, dx written.
+// Backward. A block covers a run of tokens and a group of heads; a thread owns one
+// (head, item) and walks the block's tokens with the affine's gradient in
+// registers, so d_alpha and d_beta cost no traffic per token. The block's sums go
+// to the workspace as one partial each, and rotate_grad_sum_kernel adds the
+// partials in a fixed order (no atomics: the same call gives the same bits).
+// Bound by HBM: dy and x read once, dx written. 32768 x 32 x 128 bf16: 139 us,
+// 5.8 TB/s (85 % of the measured copy rate; the sum of the partials is 5 us of
+// it). One block of 256 threads with four tokens in flight fills the SM's
+// registers; two blocks with two in flight spill (143 us), with one, 153 us.
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 256;
-constexpr int kTabTokens = 32;
+constexpr int kBwdBatch = 4;   // tokens whose loads a thread has in flight
+constexpr int kBwdBlocks = 1;  // blocks per SM
 
 template <typename T, int D, bool kGrads>
-__global__ void __launch_bounds__(kBwdThreads, 2) rotate_backward_kernel(const RotateBwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kernel(const RotateBwdParams p) {
     constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
-    // table entry (token, quarter q, item): two (cos, sin) pairs, so that the
-    // lanes of a row read consecutive 16-byte words
-    constexpr int kQ = VEC / 2;
-    __shared__ float4 tab[kTabTokens][kQ][IPR];
+    __shared__ Table<T, D> tab[2];
+    __shared__ int pos[kRunTokens];
     __shared__ float red[kBwdThreads * 2];
     const int tid = threadIdx.x;
     const int hb = p.heads_per_block;            // heads of this block
@@ -279,9 +367,8 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rotate_backward_kernel(const R
     const int h = blockIdx.y * hb + (tid / IPR) % hb;
     const int item = tid % IPR;
     const bool active = tl < lanes && h < p.H;
-    const bool rotated = 2 * VEC * item < p.rot;
-    int ca, cb;
-    item_channels<VEC>(item, p.rot, p.interleaved, ca, cb);
+    const Item<VEC, D> it(item, p.rot, p.interleaved);
+    const int ca = it.ca, cb = it.cb;
     const long long n0 = p.n * blockIdx.x / gridDim.x, n1 = p.n * (blockIdx.x + 1) / gridDim.x;
     float al[2][VEC], da[2][VEC], db[2][VEC];
 #pragma unroll
@@ -290,62 +377,68 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rotate_backward_kernel(const R
         da[0][j] = da[1][j] = db[0][j] = db[1][j] = 0.f;
     }
     if (active && p.alpha) load_affine<VEC>(p.alpha + h * D, ca, cb, al[0], al[1]);
-    const int half = p.rot >> 1;
-    for (long long base = n0; base < n1; base += kTabTokens) {
-        const int cnt = (int)min((long long)kTabTokens, n1 - base);
-        __syncthreads();
-        for (int e = tid; e < cnt * half; e += kBwdThreads) {
-            const int k = e / half, pr = e % half;  // token of the table, pair
-            float c, s;
-            angle(p.positions[base + k], __ldg(p.steps + pr), p.amplitude, c, s);
-            float2 *dst = reinterpret_cast<float2 *>(&tab[k][(pr % VEC) / 2][pr / VEC]);
-            dst[pr & 1] = make_float2(c, -s);  // the opposite angle
+    const int step = table_tokens(lanes);
+    int buf = 0;
+    for (long long base = n0; base < n1; base += step, buf ^= 1) {
+        const int cnt = (int)min((long long)step, n1 - base);
+        uint4 ra[kBwdBatch], rb[kBwdBatch], xa[kBwdBatch], xb[kBwdBatch];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int u = 0; u < kBwdBatch; ++u) {
+                const int k = k0 + u * lanes;
+                if (k >= cnt) break;
+                const T *dy = static_cast<const T *>(p.dy) + (base + k) * p.dy_stride + h * D;
+                ra[u] = __ldcs(reinterpret_cast<const uint4 *>(dy + ca));
+                rb[u] = __ldcs(reinterpret_cast<const uint4 *>(dy + cb));
+                if constexpr (kGrads) {
+                    const T *x = static_cast<const T *>(p.x) + (base + k) * p.x_stride + h * D;
+                    xa[u] = __ldcs(reinterpret_cast<const uint4 *>(x + ca));
+                    xb[u] = __ldcs(reinterpret_cast<const uint4 *>(x + cb));
+                }
+            }
+        };
+        if (active) load(tl);
+        const int run = (int)((base - n0) % kRunTokens);
+        if (run == 0) {
+            __syncthreads();
+            for (int k = tid; k < kRunTokens && base + k < n1; k += kBwdThreads) pos[k] = p.positions[base + k];
+            __syncthreads();
         }
+        tab[buf].fill(pos + run, cnt, p.steps, p.rot, p.interleaved, p.amplitude, -1.f);  // the opposite angle
         __syncthreads();
         if (!active) continue;
-#pragma unroll 2
-        for (int k = tl; k < cnt; k += lanes) {
-            const long long tok = base + k;
-            const T *dy = static_cast<const T *>(p.dy) + tok * p.dy_stride + h * D;
-            uint4 ra = __ldcs(reinterpret_cast<const uint4 *>(dy + ca));
-            uint4 rb = __ldcs(reinterpret_cast<const uint4 *>(dy + cb));
-            uint4 xa, xb;
-            if constexpr (kGrads) {
-                const T *x = static_cast<const T *>(p.x) + tok * p.x_stride + h * D;
-                xa = __ldcs(reinterpret_cast<const uint4 *>(x + ca));
-                xb = __ldcs(reinterpret_cast<const uint4 *>(x + cb));
-            }
-            float a[VEC], b[VEC];
-            unpack<T>(ra, a);
-            unpack<T>(rb, b);
-            if (rotated) {
-                float c[VEC], s[VEC];
+        for (int k0 = tl; k0 < cnt; k0 += kBwdBatch * lanes) {
+            if (k0 != tl) load(k0);
 #pragma unroll
-                for (int q = 0; q < kQ; ++q) {
-                    const float4 v = tab[k][q][item];
-                    c[2 * q] = v.x, s[2 * q] = v.y, c[2 * q + 1] = v.z, s[2 * q + 1] = v.w;
+            for (int u = 0; u < kBwdBatch; ++u) {
+                const int k = k0 + u * lanes;
+                if (k >= cnt) break;
+                float a[VEC], b[VEC], c[VEC], s[VEC];
+                unpack<T>(ra[u], a);
+                unpack<T>(rb[u], b);
+                tab[buf].read(k, item, c, s);
+                turn<VEC, D>(a, b, c, s, it, p.interleaved);
+                if constexpr (kGrads) {
+                    float x0[VEC], x1[VEC];
+                    unpack<T>(xa[u], x0);
+                    unpack<T>(xb[u], x1);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        da[0][j] = fmaf(a[j], x0[j], da[0][j]);
+                        da[1][j] = fmaf(b[j], x1[j], da[1][j]);
+                        db[0][j] += a[j];
+                        db[1][j] += b[j];
+                    }
                 }
-                turn<VEC>(a, b, c, s, p.interleaved);
-            }
-            if constexpr (kGrads) {
-                float x0[VEC], x1[VEC];
-                unpack<T>(xa, x0);
-                unpack<T>(xb, x1);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    da[0][j] = fmaf(a[j], x0[j], da[0][j]);
-                    da[1][j] = fmaf(b[j], x1[j], da[1][j]);
-                    db[0][j] += a[j];
-                    db[1][j] += b[j];
-                }
+                for (int j = 0; j < VEC; ++j) a[j] *= al[0][j], b[j] *= al[1][j];
+                T *dx = static_cast<T *>(p.dx) + (base + k) * p.dx_stride + h * D;
+                *reinterpret_cast<uint4 *>(dx + ca) = pack<T>(a);
+                *reinterpret_cast<uint4 *>(dx + cb) = pack<T>(b);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) a[j] *= al[0][j], b[j] *= al[1][j];
-            T *dx = static_cast<T *>(p.dx) + tok * p.dx_stride + h * D;
-            *reinterpret_cast<uint4 *>(dx + ca) = pack<T>(a);
-            *reinterpret_cast<uint4 *>(dx + cb) = pack<T>(b);
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (kGrads) {
         // sum over the token lanes of the block, one channel of every thread at a time
         float *part = p.partial + (long long)blockIdx.x * 2 * p.H * D;
@@ -374,12 +467,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) rotate_backward_kernel(const R
 
 // d_alpha and d_beta: column sums over the n_part partials [n_part, 2, H d].
 // A block takes 32 columns; its 8 warps stride over the partials.
-__global__ void __launch_bounds__(256) rotate_grad_sum_kernel(const float *__restrict__ partial, int n_part, int cols,
-                                                              float *__restrict__ d_alpha, float *__restrict__ d_beta) {
+__global__ void __launch_bounds__(256) rotate_grad_sum_kernel(const float *partial, int n_part, int cols, float *d_alpha,
+                                                              float *d_beta) {
     __shared__ float red[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;  // cols (= H d) is a multiple of 32: no block straddles the two
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (a dependent launch: the partials are there now)
     int i = w;
     for (; i + 24 < n_part; i += 32) {
         s0 += partial[(long long)i * 2 * cols + col];
@@ -399,33 +493,63 @@ __global__ void __launch_bounds__(256) rotate_grad_sum_kernel(const float *__res
     }
 }
 
-// Heads a thread walks: as many as leave at least four blocks per SM, so that
-// its angles are shared by many heads on long inputs while a decoding step
-// still spreads over the GPU.
-int heads_per_block(long long token_blocks, int heads) {
-    const long long want = 4LL * device_sm_count();
-    int hp = heads;
-    while (hp > 1 && token_blocks * ((heads + hp - 1) / hp) < want) hp = (hp + 1) / 2;
-    return hp;
+// The heads of a token are cut into equal groups, a block per group: as few groups
+// as fill the SM's registers with threads to within a tenth (a token's 48
+// virtual heads of 8 items in one group are a block of 384 threads where 512
+// fit, three groups of 16 fill them), since every group computes the token's
+// angles again. Several tokens go side by side when a group is narrow. Blocks
+// along the tokens: as many as run at once, with equal runs of tokens.
+template <typename T, int D, bool kAppend> cudaError_t move_t(RotateParams p, int heads, cudaStream_t s) {
+    constexpr int IPR = D / (2 * Vec<T>::kN);
+    static std::atomic<int> resident{0};  // threads of this kernel an SM's registers hold
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaFuncAttributes at;
+        if (cudaError_t e = cudaFuncGetAttributes(&at, (const void *)rotate_move_kernel<T, D, kAppend>); e != cudaSuccess) return e;
+        per_sm = 65536 / ((at.numRegs + 7) / 8 * 8);
+        resident.store(per_sm, std::memory_order_relaxed);
+    }
+    int groups = 0, hb = 0, threads = 0, best = 0;
+    const int g0 = (heads * IPR + kMoveThreads - 1) / kMoveThreads;
+    for (int g = g0; g <= g0 + 3 && g <= heads; ++g) {
+        const int h = (heads + g - 1) / g, row = h * IPR;
+        const int side = row >= 256 ? 1 : 256 / row < kTabTokens ? 256 / row : kTabTokens;
+        const int t = (row * side + 31) / 32 * 32;
+        const int busy = (int)((long long)(per_sm / t) * (side * row) * heads / ((long long)h * g));  // threads with work
+        if (busy > best + best / 10) groups = g, hb = h, threads = t, best = busy;
+    }
+    p.heads_per_block = hb;
+    const int lanes = threads / (hb * IPR);  // (the kernel's)
+    const long long rows = p.n > 0 ? p.n : p.n_out;
+    long long blocks = (long long)device_sm_count() * (per_sm / threads < 32 ? per_sm / threads : 32) / groups;
+    if (blocks > (rows + lanes - 1) / lanes) blocks = (rows + lanes - 1) / lanes;
+    if (blocks < 1) blocks = 1;
+    p.blocks = p.n > 0 ? (int)blocks : 0;
+    const long long out_blocks = (p.n_out + lanes - 1) / lanes;
+    const dim3 grid((unsigned)(p.blocks + (out_blocks < blocks ? out_blocks : blocks)), groups);
+    if (!kAppend || p.status_here) {
+        rotate_move_kernel<T, D, kAppend><<<grid, threads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    rotate_status_reset_kernel<<<1, 32, 0, s>>>(p.status);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rotate_move_kernel<T, D, kAppend>, p);
 }
 
-template <typename T, int D> cudaError_t rotate_t(RotateParams p, cudaStream_t s) {
-    constexpr int IPR = D / (2 * Vec<T>::kN);
-    const long long tb = (p.n * IPR + kFwdThreads - 1) / kFwdThreads;
-    p.heads_per_block = heads_per_block(tb, p.H);
-    const dim3 grid((unsigned)tb, (p.H + p.heads_per_block - 1) / p.heads_per_block);
-    rotate_kernel<T, D><<<grid, kFwdThreads, 0, s>>>(p);
-    return cudaGetLastError();
+template <typename T, int D> cudaError_t rotate_t(const RotateParams &p, cudaStream_t s) {
+    return move_t<T, D, false>(p, p.H, s);
 }
-
-template <typename T, int D> cudaError_t append_t(RotateAppendParams p, cudaStream_t s) {
-    constexpr int IPR = D / (2 * Vec<T>::kN);
-    const long long tb = (((long long)p.n_new + p.n_out) * IPR + kFwdThreads - 1) / kFwdThreads;
-    const int heads = (p.q || p.q_out ? p.Hq : 0) + 2 * p.Hkv;
-    p.heads_per_block = heads_per_block(tb, heads);
-    const dim3 grid((unsigned)tb, (heads + p.heads_per_block - 1) / p.heads_per_block);
-    rotate_append_kernel<T, D><<<grid, kFwdThreads, 0, s>>>(p);
-    return cudaGetLastError();
+template <typename T, int D> cudaError_t append_t(const RotateParams &p, cudaStream_t s) {
+    return move_t<T, D, true>(p, p.H + 2 * p.Hkv, s);
 }
 
 template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStream_t s) {
@@ -444,7 +568,7 @@ template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStrea
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes) {
     const int per = kBwdThreads / (d * elem_bytes / 32);  // heads of a block
     const int groups = (H + per - 1) / per;
-    long long parts = 2LL * device_sm_count() / groups;
+    long long parts = (long long)kBwdBlocks * device_sm_count() / groups;
     if (parts > (n + 15) / 16) parts = (n + 15) / 16;
     return parts < 1 ? 1 : (int)parts;
 }
@@ -456,7 +580,7 @@ int rotate_grad_parts(long long n, int H, int d, int elem_bytes) {
 cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream) {
     return ORTHROS_BY_TYPE(rotate_t, p);
 }
-cudaError_t launch_rotate_append(const RotateAppendParams &p, int d, orthros_dtype dtype, cudaStream_t stream) {
+cudaError_t launch_rotate_append(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream) {
     return ORTHROS_BY_TYPE(append_t, p);
 }
 cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream) {
@@ -464,8 +588,16 @@ cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtyp
 }
 cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t stream) {
     const int cols = p.H * d;
-    rotate_grad_sum_kernel<<<2 * cols / 32, 256, 0, stream>>>(p.partial, p.n_part, cols, p.d_alpha, p.d_beta);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * cols / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rotate_grad_sum_kernel, (const float *)p.partial, p.n_part, cols, p.d_alpha, p.d_beta);
 }
 #undef ORTHROS_BY_TYPE
 
