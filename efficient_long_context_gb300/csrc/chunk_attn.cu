@@ -30,9 +30,10 @@
 // own that the epilogue adds up, so that the softmax of one tile still runs
 // beside the products of the other.
 //
-// Roles (320 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
+// Roles (352 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
 // one thread per row), warp 8 copies (page lookups by its lanes, TMA boxes of
-// up to 128 tokens within a page), warp 9 issues tcgen05.mma. S = Q K^T (bf16,
+// up to 128 tokens within a page), warp 9 issues tcgen05.mma, warp 10 clears value
+// rows that no row of the unit sees. S = Q K^T (bf16,
 // M = 128, N = 128) goes to TMEM, P returns there as bf16 over S, O += P V. TMEM:
 // S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [384,384+d).
 //
@@ -56,10 +57,11 @@ namespace {
 constexpr int kRows = 128;  // rows of a tile
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kNumK = 3, kNumV = 2;
-constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
-// Three of the ten warps sit on two of the four schedulers: 168 registers a
-// thread fit (3 x 32 x 168 of 16K), so the bound is taken for 384 threads.
+static_assert(kNumV == 2, "the clearing warp counts two stages");
+constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+constexpr int kThreads = 352;
+// At most three of the eleven warps sit on a scheduler: 168 registers a thread
+// fit (3 x 32 x 168 of 16K), so the bound is taken for 384 threads.
 constexpr int kBound = 384;
 constexpr int kFlagRing = 8;
 // A share of fewer key tiles than this is not worth a CTA of its own.
@@ -92,6 +94,7 @@ constexpr int kSegRing = 2;
 struct Meta {
     uint64_t k_full[kNumK], k_empty[kNumK], v_full[kNumV], v_empty[kNumV];
     uint64_t q_full[2], q_empty[2];
+    uint64_t ve_full[kNumV];  // a value tile with unseen rows arrived: warp 10 clears them, then completes v_full
     uint64_t s_full[2], p_full[2], o_free[2];
     uint64_t o_full[2];  // slot s's O complete, for slot s's threads
     uint64_t ox_full;    // slot 1's O of a shared row tile complete, for slot 0's threads
@@ -289,6 +292,15 @@ __device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
     return lo;
 }
 
+// Whether key tile `it` of a segment has rows that none of its unit's tokens sees:
+// all but rows [r0, r1).
+__device__ __forceinline__ bool unseen_rows(const Segment &sg, int window, int it, int &r0, int &r1) {
+    const int key0 = (sg.kt0 + it) * kKeys;
+    r0 = max(0, sg.pos0 - window + 1 - key0);
+    r1 = min(kKeys, sg.pos0 + sg.cnt - key0);
+    return r0 > 0 || r1 < kKeys;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kBound, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -310,6 +322,7 @@ __global__ void __launch_bounds__(kBound, 1)
         for (int i = 0; i < kNumV; ++i) {
             mbar_init(&mt.v_full[i], 1);
             mbar_init(&mt.v_empty[i], 1);
+            mbar_init(&mt.ve_full[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&mt.q_full[s], 1);
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kBound, 1)
         mbar_init(&mt.ml_free, kRows);
         for (int r = 0; r < kSegRing; ++r) {
             mbar_init(&mt.g_full[r], 1);
-            mbar_init(&mt.g_empty[r], kSoftmaxWarps + 1);
+            mbar_init(&mt.g_empty[r], kSoftmaxWarps + 2);
         }
         mbar_init(&mt.mma_done, 1);
         mt.abort = 0;
@@ -477,12 +490,14 @@ __global__ void __launch_bounds__(kBound, 1)
                                 alive = false;
                                 break;
                             }
-                            if (lane == 0) mbar_arrive_expect_tx(&mt.v_full[sv], C::kTile);
+                            int r0, r1;
+                            const bool edge = unseen_rows(sg, p.window, it, r0, r1);
+                            uint64_t *full = edge ? &mt.ve_full[sv] : &mt.v_full[sv];
+                            if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
                             __syncwarp();
                             if (lane < n_box)
                                 for (int h = 0; h < C::kSub; ++h)
-                                    tma_load_3d(vs + h * (kRows * 128) + lane * box * 128, &tm_v, &mt.v_full[sv], 64 * h,
-                                                sg.kv, tok);
+                                    tma_load_3d(vs + h * (kRows * 128) + lane * box * 128, &tm_v, full, 64 * h, sg.kv, tok);
                             ++gv;
                         } else {
                             // page sizes without a copy box: the lanes gather the rows, 16 bytes at a time
@@ -547,147 +562,163 @@ __global__ void __launch_bounds__(kBound, 1)
                 if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, p.status);
         }
     } else if (warp == kMmaWarp) {
-        // ---------------- tcgen05.mma issuer (lane 0 issues, the warp waits together) ----------------
-        constexpr uint32_t kIdescS = idesc_f16(1, 1, 0, 0, kRows, kKeys);  // bf16, both K-major
-        constexpr uint32_t kIdescO = idesc_f16(1, 1, 0, 1, kRows, D);      // bf16, V MN-major
-        constexpr uint32_t kTileU = C::kTile >> 4;
-        const uint64_t dq = desc_sw128(smem_u32(smem + C::kQ0), 16, 1024);
-        const uint64_t dk = desc_sw128(smem_u32(smem + C::kK0), 16, 1024);
-        const uint64_t dv = desc_sw128(smem_u32(smem + C::kV0), kKeys * 128, 1024);
-        auto issue_s = [&](int s, uint64_t qd, uint64_t kd) {
+        // ---------------- tcgen05.mma issuer (one thread) ----------------
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_f16(1, 1, 0, 0, kRows, kKeys);  // bf16, both K-major
+            constexpr uint32_t kIdescO = idesc_f16(1, 1, 0, 1, kRows, D);      // bf16, V MN-major
+            constexpr uint32_t kTileU = C::kTile >> 4;
+            const uint64_t dq = desc_sw128(smem_u32(smem + C::kQ0), 16, 1024);
+            const uint64_t dk = desc_sw128(smem_u32(smem + C::kK0), 16, 1024);
+            const uint64_t dv = desc_sw128(smem_u32(smem + C::kV0), kKeys * 128, 1024);
+            auto issue_s = [&](int s, uint64_t qd, uint64_t kd) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
-                mma_ss(tmem + s * 128, qd + off, kd + off, kIdescS, ks > 0);
-            }
-            tc_commit(&mt.s_full[s]);
-        };
-        auto issue_pv = [&](int s, uint64_t vd, uint32_t acc0) {
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+                    mma_ss(tmem + s * 128, qd + off, kd + off, kIdescS, ks > 0);
+                }
+                tc_commit(&mt.s_full[s]);
+            };
+            auto issue_pv = [&](int s, uint64_t vd, uint32_t acc0) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ts(tmem + C::kTmemO + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescO,
-                       kk > 0 ? 1u : acc0);
-        };
-        uint32_t gk = 0;                // key tiles consumed
-        uint32_t nq[2] = {0, 0};        // query tiles consumed per slot
-        uint32_t pc[2] = {0, 0};        // P tiles consumed per slot
-        uint32_t oc[2] = {0, 0};        // segments in which the slot had tiles
-        bool ok = true;
-        for (int i = 0; ok; ++i) {
-            const int r = i % kSegRing;
-            if (!(ok = mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
-            const Segment sg = mt.seg[r];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mt.g_empty[r]);
-            if (sg.end) break;
-            const int key_hi = sg.pos0 + sg.cnt - 1, key_lo = max(0, sg.pos0 - p.window + 1);
-            // waits for value tile `it` and clears its rows outside [key_lo, key_hi] (a page that
-            // reaches past them holds anything, and 0 * NaN is NaN)
-            auto value_tile = [&](int it) -> bool {
-                const uint32_t gi = gk + it;
-                uint8_t *vs = smem + C::kV0 + (gi % kNumV) * C::kTile;
-                if (!mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status)) return false;
-                const int key0 = (sg.kt0 + it) * kKeys;
-                const int r0 = max(0, key_lo - key0), r1 = min(kKeys, key_hi + 1 - key0);  // rows [r0, r1) stay
-                if (r0 > 0 || r1 < kKeys) {
-                    const int n = r0 + kKeys - r1;  // rows to clear
-                    constexpr int kCh = D / 8;
-                    for (int e = lane; e < n * kCh; e += 32) {
-                        const int k = e / kCh, row = k < r0 ? k : r1 + k - r0;
-                        *reinterpret_cast<uint4 *>(vs + sw128(row, e % kCh)) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                return true;
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts(tmem + C::kTmemO + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                           kIdescO, kk > 0 ? 1u : acc0);
             };
-            auto key_tile = [&](int it) -> bool {
-                const uint32_t gi = gk + it;
-                return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
-            };
-            auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
-            auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
-            // the slot's P of its next tile is there; before its first product of the segment, its O is free
-            auto p_tile = [&](int s, bool first) -> bool {
-                if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
-                ++pc[s];
-                if (first) {
-                    if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
-                    ++oc[s];
-                }
-                tc_fence_after();
-                return true;
-            };
-            if (sg.pair) {
+            uint32_t gk = 0;                   // key tiles consumed
+            uint32_t nq[2] = {0, 0};           // query tiles consumed per slot
+            uint32_t pc[2] = {0, 0};           // P tiles consumed per slot
+            uint32_t oc[2] = {0, 0};           // segments in which the slot had tiles
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int r = i % kSegRing;
+                if (!(ok = mbar_wait(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
+                const Segment sg = mt.seg[r];
+                mbar_arrive(&mt.g_empty[r]);
+                if (sg.end) break;
                 const int n = sg.nkt;
-                for (int it = -1; ok && it < n; ++it) {
-                    const bool more = it + 1 < n;
-                    if (it >= 0 && !(ok = value_tile(it))) break;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (it >= 0 && it >= sg.lo[s] && it <= sg.hi[s]) {
-                            if (!(ok = p_tile(s, it == sg.lo[s]))) break;
-                            if (lane == 0) {
-                                issue_pv(s, vdesc(it), it > sg.lo[s]);
-                                if (it == sg.hi[s]) tc_commit(&mt.o_full[s]);
-                            }
-                            __syncwarp();
+                auto value_tile = [&](int it) -> bool {
+                    const uint32_t gi = gk + it;
+                    return mbar_wait(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status);
+                };
+                auto key_tile = [&](int it) -> bool {
+                    const uint32_t gi = gk + it;
+                    return mbar_wait(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
+                };
+                auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
+                auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
+                // the slot's P of its next tile is there; before its first product of the segment, its O is free
+                auto p_tile = [&](int s, bool first) -> bool {
+                    if (!mbar_wait(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
+                    ++pc[s];
+                    if (first) {
+                        if (oc[s] > 0 && !mbar_wait(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
+                        ++oc[s];
+                    }
+                    tc_fence_after();
+                    return true;
+                };
+                if (sg.pair) {
+                    const int lo0 = sg.lo[0], hi0 = sg.hi[0], lo1 = sg.lo[1], hi1 = sg.hi[1];
+                    // first tile's S of both slots
+                    if (!(ok = mbar_wait(&mt.q_full[0], nq[0] & 1, abort, p.status) && key_tile(0))) break;
+                    tc_fence_after();
+                    if (lo0 <= 0 && hi0 >= 0) issue_s(0, dq, kdesc(0));
+                    if (n == 1) tc_commit(&mt.q_empty[0]);
+                    if (!(ok = mbar_wait(&mt.q_full[1], nq[1] & 1, abort, p.status))) break;
+                    tc_fence_after();
+                    if (lo1 <= 0 && hi1 >= 0) issue_s(1, dq + kTileU, kdesc(0));
+                    if (n == 1) tc_commit(&mt.q_empty[1]);
+                    tc_commit(&mt.k_empty[gk % kNumK]);
+                    // per tile and slot: P V, then the next tile's S into the columns that held P
+                    for (int it = 0; it < n; ++it) {
+                        const bool more = it + 1 < n;
+                        if (!(ok = value_tile(it))) break;
+                        if (it >= lo0 && it <= hi0) {
+                            if (!(ok = p_tile(0, it == lo0))) break;
+                            issue_pv(0, vdesc(it), it > lo0);
+                            if (it == hi0) tc_commit(&mt.o_full[0]);
                         }
                         if (more) {
-                            if (it < 0 && !(ok = mbar_wait_warp(&mt.q_full[s], nq[s] & 1, abort, p.status))) break;
-                            if (s == 0 && !(ok = key_tile(it + 1))) break;
+                            if (!(ok = key_tile(it + 1))) break;
                             tc_fence_after();
-                            if (lane == 0) {
-                                if (it + 1 >= sg.lo[s] && it + 1 <= sg.hi[s]) issue_s(s, dq + s * kTileU, kdesc(it + 1));
-                                if (it + 2 == n) tc_commit(&mt.q_empty[s]);
-                                if (s == 1) tc_commit(&mt.k_empty[(gk + it + 1) % kNumK]);
-                            }
-                            __syncwarp();
+                            if (it + 1 >= lo0 && it + 1 <= hi0) issue_s(0, dq, kdesc(it + 1));
+                            if (it + 2 == n) tc_commit(&mt.q_empty[0]);
+                        }
+                        if (it >= lo1 && it <= hi1) {
+                            if (!(ok = p_tile(1, it == lo1))) break;
+                            issue_pv(1, vdesc(it), it > lo1);
+                            if (it == hi1) tc_commit(&mt.o_full[1]);
+                        }
+                        tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                        if (more) {
+                            if (it + 1 >= lo1 && it + 1 <= hi1) issue_s(1, dq + kTileU, kdesc(it + 1));
+                            if (it + 2 == n) tc_commit(&mt.q_empty[1]);
+                            tc_commit(&mt.k_empty[(gk + it + 1) % kNumK]);
                         }
                     }
-                    if (!ok) break;
-                    if (it >= 0 && lane == 0) tc_commit(&mt.v_empty[(gk + it) % kNumV]);
-                    __syncwarp();
-                }
-                ++nq[0];
-                ++nq[1];
-            } else {
-                const int n = sg.nkt;
-                if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
-                ++nq[0];
-                // S of tile it into slot it & 1
-                auto s_tile = [&](int it) -> bool {
-                    if (!key_tile(it)) return false;
-                    tc_fence_after();
-                    if (lane == 0) {
+                    ++nq[0];
+                    ++nq[1];
+                } else {
+                    if (!(ok = mbar_wait(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
+                    ++nq[0];
+                    // S of tile it into slot it & 1
+                    auto s_tile = [&](int it) -> bool {
+                        if (!key_tile(it)) return false;
+                        tc_fence_after();
                         issue_s(it & 1, dq, kdesc(it));
                         if (it + 1 == n) tc_commit(&mt.q_empty[0]);
                         tc_commit(&mt.k_empty[(gk + it) % kNumK]);
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                ok = s_tile(0) && (n < 2 || s_tile(1));
-                for (int it = 0; ok && it < n; ++it) {
-                    const int s = it & 1;
-                    if (!(ok = value_tile(it) && p_tile(s, it < 2))) break;
-                    if (lane == 0) {
+                        return true;
+                    };
+                    ok = s_tile(0) && (n < 2 || s_tile(1));
+                    for (int it = 0; ok && it < n; ++it) {
+                        const int s = it & 1;
+                        if (!(ok = value_tile(it) && p_tile(s, it < 2))) break;
                         issue_pv(s, vdesc(it), it >= 2);
                         if (it + 2 >= n) tc_commit(s ? &mt.ox_full : &mt.o_full[0]);
                         tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                        if (it + 2 < n) ok = s_tile(it + 2);
                     }
-                    __syncwarp();
-                    if (it + 2 < n) ok = s_tile(it + 2);
                 }
+                gk += n;
             }
-            gk += sg.nkt;
-        }
-        // every product issued must be complete before tensor memory is freed
-        if (lane == 0) {
+            // every product issued must be complete before tensor memory is freed
             tc_commit(&mt.mma_done);
             mbar_wait_drain(&mt.mma_done, 0, p.status);
         }
         __syncwarp();
+    } else if (warp == kClearWarp) {
+        // ---------------- unseen value rows: a page that reaches past the unit's keys holds
+        // anything there, and 0 * NaN is NaN ----------------
+        uint32_t gk = 0;
+        uint32_t ne[kNumV] = {};  // such tiles handled per stage
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int r = i % kSegRing;
+            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status)) break;
+            const Segment sg = mt.seg[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mt.g_empty[r]);
+            if (sg.end) break;
+            if (!p.box) continue;  // gathered rows come clean
+            for (int it = 0; it < sg.nkt; ++it) {
+                int r0, r1;
+                if (!unseen_rows(sg, p.window, it, r0, r1)) continue;
+                const uint32_t sv = (gk + it) % kNumV;
+                if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (sv ? ne[1] : ne[0]) & 1, abort, p.status))) break;
+                if (sv) ++ne[1]; else ++ne[0];
+                uint8_t *vs = smem + C::kV0 + sv * C::kTile;
+                constexpr int kCh = D / 8;
+                for (int e = lane; e < (r0 + kKeys - r1) * kCh; e += 32) {
+                    const int k = e / kCh, row = k < r0 ? k : r1 + k - r0;
+                    *reinterpret_cast<uint4 *>(vs + sw128(row, e % kCh)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mt.v_full[sv]);
+            }
+            gk += sg.nkt;
+        }
     } else {
         // ---------------- softmax: one thread per row ----------------
         const int s = warp >> 2;
@@ -913,7 +944,7 @@ __global__ void __launch_bounds__(kBound, 1)
 // Merge of the units that a share's border cut: one warp per row, the parts'
 // weights found by its lanes, the outputs added in the order of the parts.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 8, kMergeBatch = 8;
 
 template <int D> __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -948,12 +979,29 @@ template <int D> __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge
             L += w * ml.y;
         }
         const int k1 = min(32, hd.n_parts - i0);
-        for (int k = 0; k < k1; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            if (wk == 0.f) continue;  // a part without keys for this row wrote no output
-            const float *src = p.part_o + index(i0 + k) * D + lane * E;
+        // eight parts' loads at a time; a part without keys for this row (weight 0) wrote no output
+        for (int k0 = 0; k0 < k1; k0 += kMergeBatch) {
+            float wk[kMergeBatch], x[kMergeBatch][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, src[e], acc[e]);
+            for (int k = 0; k < kMergeBatch; ++k) {
+                wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                if (k0 + k >= k1) wk[k] = 0.f;
+                if (wk[k] != 0.f) {
+                    const float *src = p.part_o + index(i0 + k0 + k) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(src);
+                        x[k][0] = f.x, x[k][1] = f.y, x[k][2] = f.z, x[k][3] = f.w;
+                    } else {
+                        const float2 f = *reinterpret_cast<const float2 *>(src);
+                        x[k][0] = f.x, x[k][1] = f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k)
+                if (wk[k] != 0.f)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
         }
     }
 #pragma unroll
