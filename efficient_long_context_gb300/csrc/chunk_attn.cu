@@ -109,6 +109,40 @@ struct Meta {
 };
 static_assert(sizeof(Meta) <= 2048, "barriers and metadata must fit their shared-memory region");
 
+// The products are issued under a predicate by a whole warp rather than inside a
+// one-lane branch: warp-uniform descriptors stay in uniform registers.
+template <typename T> __device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t el, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(el)
+        : "memory");
+}
+
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
     asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
@@ -562,8 +596,10 @@ __global__ void __launch_bounds__(kBound, 1)
                 if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, p.status);
         }
     } else if (warp == kMmaWarp) {
-        // ---------------- tcgen05.mma issuer (one thread) ----------------
-        if (lane == 0) {
+        // ---------------- tcgen05.mma issuer ----------------
+        {
+            const uint32_t el = elect_one();
+            const uint32_t tm = uniform(tmem);
             constexpr uint32_t kIdescS = idesc_f16(1, 1, 0, 0, kRows, kKeys);  // bf16, both K-major
             constexpr uint32_t kIdescO = idesc_f16(1, 1, 0, 1, kRows, D);      // bf16, V MN-major
             constexpr uint32_t kTileU = C::kTile >> 4;
@@ -574,14 +610,14 @@ __global__ void __launch_bounds__(kBound, 1)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
-                    mma_ss(tmem + s * 128, qd + off, kd + off, kIdescS, ks > 0);
+                    mma_ss_if(el, tm + s * 128, qd + off, kd + off, kIdescS, ks > 0);
                 }
-                tc_commit(&mt.s_full[s]);
+                tc_commit_if(el, &mt.s_full[s]);
             };
             auto issue_pv = [&](int s, uint64_t vd, uint32_t acc0) {
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts(tmem + C::kTmemO + s * 128, tmem + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                    mma_ts_if(el, tm + C::kTmemO + s * 128, tm + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
                            kIdescO, kk > 0 ? 1u : acc0);
             };
             uint32_t gk = 0;                   // key tiles consumed
@@ -591,44 +627,47 @@ __global__ void __launch_bounds__(kBound, 1)
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 const int r = i % kSegRing;
-                if (!(ok = mbar_wait(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
-                const Segment sg = mt.seg[r];
-                mbar_arrive(&mt.g_empty[r]);
-                if (sg.end) break;
-                const int n = sg.nkt;
+                if (!(ok = mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
+                // (broadcast: known to be the same in every lane, as everything that follows from them)
+                const Segment &sr = mt.seg[r];
+                const bool end = uniform(sr.end) != 0, pair = uniform(sr.pair) != 0;
+                const int n = uniform(sr.nkt);
+                const int lo0 = uniform(sr.lo[0]), hi0 = uniform(sr.hi[0]), lo1 = uniform(sr.lo[1]), hi1 = uniform(sr.hi[1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mt.g_empty[r]);
+                if (end) break;
                 auto value_tile = [&](int it) -> bool {
                     const uint32_t gi = gk + it;
-                    return mbar_wait(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status);
+                    return mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status);
                 };
                 auto key_tile = [&](int it) -> bool {
                     const uint32_t gi = gk + it;
-                    return mbar_wait(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
+                    return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
                 };
                 auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
                 auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
                 // the slot's P of its next tile is there; before its first product of the segment, its O is free
                 auto p_tile = [&](int s, bool first) -> bool {
-                    if (!mbar_wait(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
+                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
                     ++pc[s];
                     if (first) {
-                        if (oc[s] > 0 && !mbar_wait(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
+                        if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
                         ++oc[s];
                     }
                     tc_fence_after();
                     return true;
                 };
-                if (sg.pair) {
-                    const int lo0 = sg.lo[0], hi0 = sg.hi[0], lo1 = sg.lo[1], hi1 = sg.hi[1];
+                if (pair) {
                     // first tile's S of both slots
-                    if (!(ok = mbar_wait(&mt.q_full[0], nq[0] & 1, abort, p.status) && key_tile(0))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status) && key_tile(0))) break;
                     tc_fence_after();
                     if (lo0 <= 0 && hi0 >= 0) issue_s(0, dq, kdesc(0));
-                    if (n == 1) tc_commit(&mt.q_empty[0]);
-                    if (!(ok = mbar_wait(&mt.q_full[1], nq[1] & 1, abort, p.status))) break;
+                    if (n == 1) tc_commit_if(el, &mt.q_empty[0]);
+                    if (!(ok = mbar_wait_warp(&mt.q_full[1], nq[1] & 1, abort, p.status))) break;
                     tc_fence_after();
                     if (lo1 <= 0 && hi1 >= 0) issue_s(1, dq + kTileU, kdesc(0));
-                    if (n == 1) tc_commit(&mt.q_empty[1]);
-                    tc_commit(&mt.k_empty[gk % kNumK]);
+                    if (n == 1) tc_commit_if(el, &mt.q_empty[1]);
+                    tc_commit_if(el, &mt.k_empty[gk % kNumK]);
                     // per tile and slot: P V, then the next tile's S into the columns that held P
                     for (int it = 0; it < n; ++it) {
                         const bool more = it + 1 < n;
@@ -636,38 +675,38 @@ __global__ void __launch_bounds__(kBound, 1)
                         if (it >= lo0 && it <= hi0) {
                             if (!(ok = p_tile(0, it == lo0))) break;
                             issue_pv(0, vdesc(it), it > lo0);
-                            if (it == hi0) tc_commit(&mt.o_full[0]);
+                            if (it == hi0) tc_commit_if(el, &mt.o_full[0]);
                         }
                         if (more) {
                             if (!(ok = key_tile(it + 1))) break;
                             tc_fence_after();
                             if (it + 1 >= lo0 && it + 1 <= hi0) issue_s(0, dq, kdesc(it + 1));
-                            if (it + 2 == n) tc_commit(&mt.q_empty[0]);
+                            if (it + 2 == n) tc_commit_if(el, &mt.q_empty[0]);
                         }
                         if (it >= lo1 && it <= hi1) {
                             if (!(ok = p_tile(1, it == lo1))) break;
                             issue_pv(1, vdesc(it), it > lo1);
-                            if (it == hi1) tc_commit(&mt.o_full[1]);
+                            if (it == hi1) tc_commit_if(el, &mt.o_full[1]);
                         }
-                        tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                        tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
                         if (more) {
                             if (it + 1 >= lo1 && it + 1 <= hi1) issue_s(1, dq + kTileU, kdesc(it + 1));
-                            if (it + 2 == n) tc_commit(&mt.q_empty[1]);
-                            tc_commit(&mt.k_empty[(gk + it + 1) % kNumK]);
+                            if (it + 2 == n) tc_commit_if(el, &mt.q_empty[1]);
+                            tc_commit_if(el, &mt.k_empty[(gk + it + 1) % kNumK]);
                         }
                     }
                     ++nq[0];
                     ++nq[1];
                 } else {
-                    if (!(ok = mbar_wait(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
                     ++nq[0];
                     // S of tile it into slot it & 1
                     auto s_tile = [&](int it) -> bool {
                         if (!key_tile(it)) return false;
                         tc_fence_after();
                         issue_s(it & 1, dq, kdesc(it));
-                        if (it + 1 == n) tc_commit(&mt.q_empty[0]);
-                        tc_commit(&mt.k_empty[(gk + it) % kNumK]);
+                        if (it + 1 == n) tc_commit_if(el, &mt.q_empty[0]);
+                        tc_commit_if(el, &mt.k_empty[(gk + it) % kNumK]);
                         return true;
                     };
                     ok = s_tile(0) && (n < 2 || s_tile(1));
@@ -675,16 +714,16 @@ __global__ void __launch_bounds__(kBound, 1)
                         const int s = it & 1;
                         if (!(ok = value_tile(it) && p_tile(s, it < 2))) break;
                         issue_pv(s, vdesc(it), it >= 2);
-                        if (it + 2 >= n) tc_commit(s ? &mt.ox_full : &mt.o_full[0]);
-                        tc_commit(&mt.v_empty[(gk + it) % kNumV]);
+                        if (it + 2 >= n) tc_commit_if(el, s ? &mt.ox_full : &mt.o_full[0]);
+                        tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
                         if (it + 2 < n) ok = s_tile(it + 2);
                     }
                 }
                 gk += n;
             }
             // every product issued must be complete before tensor memory is freed
-            tc_commit(&mt.mma_done);
-            mbar_wait_drain(&mt.mma_done, 0, p.status);
+            tc_commit_if(el, &mt.mma_done);
+            if (lane == 0) mbar_wait_drain(&mt.mma_done, 0, p.status);
         }
         __syncwarp();
     } else if (warp == kClearWarp) {
