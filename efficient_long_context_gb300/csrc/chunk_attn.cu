@@ -95,7 +95,8 @@ struct Meta {
     uint64_t k_full[kNumK], k_empty[kNumK], v_full[kNumV], v_empty[kNumV];
     uint64_t q_full[2], q_empty[2];
     uint64_t ve_full[kNumV];  // a value tile with unseen rows arrived: warp 10 clears them, then completes v_full
-    uint64_t s_full[2], p_full[2], o_free[2];
+    uint64_t s_full[2], o_free[2];
+    uint64_t p_half[2], p_full[2];  // the first 64 keys of a P tile are stored (and O rescaled); all are
     uint64_t o_full[2];  // slot s's O complete, for slot s's threads
     uint64_t ox_full;    // slot 1's O of a shared row tile complete, for slot 0's threads
     uint64_t ml_full, ml_free;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kBound, 1)
             mbar_init(&mt.q_full[s], 1);
             mbar_init(&mt.q_empty[s], 1);
             mbar_init(&mt.s_full[s], 1);
+            mbar_init(&mt.p_half[s], kRows);
             mbar_init(&mt.p_full[s], kRows);
             mbar_init(&mt.o_full[s], 1);
             mbar_init(&mt.o_free[s], kRows);
@@ -614,11 +616,14 @@ __global__ void __launch_bounds__(kBound, 1)
                 }
                 tc_commit_if(el, &mt.s_full[s]);
             };
-            auto issue_pv = [&](int s, uint64_t vd, uint32_t acc0) {
+            // O += P V over half h of the tile's keys
+            auto issue_pv = [&](int s, int h, uint64_t vd, uint32_t acc0) {
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
+                for (int k = 0; k < kKeys / 32; ++k) {
+                    const int kk = h * (kKeys / 32) + k;
                     mma_ts_if(el, tm + C::kTmemO + s * 128, tm + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                           kIdescO, kk > 0 ? 1u : acc0);
+                              kIdescO, kk > 0 ? 1u : acc0);
+                }
             };
             uint32_t gk = 0;                   // key tiles consumed
             uint32_t nq[2] = {0, 0};           // query tiles consumed per slot
@@ -646,15 +651,20 @@ __global__ void __launch_bounds__(kBound, 1)
                 };
                 auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
                 auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
-                // the slot's P of its next tile is there; before its first product of the segment, its O is free
-                auto p_tile = [&](int s, bool first) -> bool {
-                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
-                    ++pc[s];
+                // the slot's next P V: the first half of the keys goes while the softmax finishes the second;
+                // before the slot's first product of the segment, its O is free
+                auto pv_tile = [&](int s, int it, bool first) -> bool {
                     if (first) {
                         if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
                         ++oc[s];
                     }
+                    if (!mbar_wait_warp(&mt.p_half[s], pc[s] & 1, abort, p.status)) return false;
                     tc_fence_after();
+                    issue_pv(s, 0, vdesc(it), !first);
+                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
+                    tc_fence_after();
+                    issue_pv(s, 1, vdesc(it), 1);
+                    ++pc[s];
                     return true;
                 };
                 if (pair) {
@@ -673,8 +683,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         const bool more = it + 1 < n;
                         if (!(ok = value_tile(it))) break;
                         if (it >= lo0 && it <= hi0) {
-                            if (!(ok = p_tile(0, it == lo0))) break;
-                            issue_pv(0, vdesc(it), it > lo0);
+                            if (!(ok = pv_tile(0, it, it == lo0))) break;
                             if (it == hi0) tc_commit_if(el, &mt.o_full[0]);
                         }
                         if (more) {
@@ -684,8 +693,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             if (it + 2 == n) tc_commit_if(el, &mt.q_empty[0]);
                         }
                         if (it >= lo1 && it <= hi1) {
-                            if (!(ok = p_tile(1, it == lo1))) break;
-                            issue_pv(1, vdesc(it), it > lo1);
+                            if (!(ok = pv_tile(1, it, it == lo1))) break;
                             if (it == hi1) tc_commit_if(el, &mt.o_full[1]);
                         }
                         tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
@@ -712,8 +720,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     ok = s_tile(0) && (n < 2 || s_tile(1));
                     for (int it = 0; ok && it < n; ++it) {
                         const int s = it & 1;
-                        if (!(ok = value_tile(it) && p_tile(s, it < 2))) break;
-                        issue_pv(s, vdesc(it), it >= 2);
+                        if (!(ok = value_tile(it) && pv_tile(s, it, it < 2))) break;
                         if (it + 2 >= n) tc_commit_if(el, s ? &mt.ox_full : &mt.o_full[0]);
                         tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
                         if (it + 2 < n) ok = s_tile(it + 2);
@@ -793,40 +800,57 @@ __global__ void __launch_bounds__(kBound, 1)
                 if (!(ok = mbar_wait_warp(&mt.s_full[s], cnt & 1, abort, p.status))) break;
                 ++cnt;
                 if (idle) {
+                    mbar_arrive(&mt.p_half[s]);
                     mbar_arrive(&mt.p_full[s]);
                     continue;
                 }
                 tc_fence_after();
-                uint32_t xr[kKeys];
-                using Cols = uint32_t[32];
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<Cols *>(xr + 32 * q));
                 const int key0 = (sg.kt0 + it) * kKeys;
                 if (mt.bad[(gk + it) % kFlagRing] && key0 <= t_row && key0 + kKeys - 1 >= lo_row) bad = true;
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) reg_fence(*reinterpret_cast<Cols *>(xr + 32 * q));
-                if (key0 + kKeys - 1 > t_first || key0 < lo_max) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (key0 + c > t_row || key0 + c < lo_row) xr[c] = __float_as_uint(-INFINITY);
-                }
+                uint32_t xr[kKeys];
+                using Cols = uint32_t[32];
                 const float *x = reinterpret_cast<const float *>(xr);
-                float mq[16];
+                for (int pass = 0;; ++pass) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    mq[q] = max3(max3(x[8 * q], x[8 * q + 1], x[8 * q + 2]), max3(x[8 * q + 3], x[8 * q + 4], x[8 * q + 5]),
-                                 fmaxf(x[8 * q + 6], x[8 * q + 7]));
-                const float m_tile = max3(max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), max3(mq[6], mq[7], mq[8])),
-                                          max3(mq[9], mq[10], mq[11]), max3(mq[12], mq[13], fmaxf(mq[14], mq[15])));
-                // the shift follows the maximum only when it grew by more than 2^8 (P stays finite in bf16)
-                const float m_new = fmaxf(m_ref, m_tile);
-                const bool resc = (m_new - m_ref) * c2 > 8.f;  // true on the first finite maximum
-                const bool any_resc = __any_sync(0xffffffffu, resc);
-                const float alpha = resc ? ex2((m_ref - m_new) * c2) : 1.f;
-                if (resc) {
-                    l *= alpha;
-                    m_ref = m_new;
+                    for (int q = 0; q < kKeys / 32; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<Cols *>(xr + 32 * q));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < kKeys / 32; ++q) reg_fence(*reinterpret_cast<Cols *>(xr + 32 * q));
+                    if (key0 + kKeys - 1 > t_first || key0 < lo_max) {
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            if (key0 + c > t_row || key0 + c < lo_row) xr[c] = __float_as_uint(-INFINITY);
+                    }
+                    if (pass) break;
+                    float mq[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        mq[q] = max3(max3(x[8 * q], x[8 * q + 1], x[8 * q + 2]), max3(x[8 * q + 3], x[8 * q + 4], x[8 * q + 5]),
+                                     fmaxf(x[8 * q + 6], x[8 * q + 7]));
+                    const float m_tile = max3(max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), max3(mq[6], mq[7], mq[8])),
+                                              max3(mq[9], mq[10], mq[11]), max3(mq[12], mq[13], fmaxf(mq[14], mq[15])));
+                    // the shift follows the maximum only when it grew by more than 2^8 (P stays finite in bf16)
+                    const float m_new = fmaxf(m_ref, m_tile);
+                    const bool resc = (m_new - m_ref) * c2 > 8.f;  // true on the first finite maximum
+                    const float alpha = resc ? ex2((m_ref - m_new) * c2) : 1.f;
+                    if (resc) {
+                        l *= alpha;
+                        m_ref = m_new;
+                    }
+                    if (!__any_sync(0xffffffffu, resc) || it == it0) break;
+                    // Rescales O, which is idle here (the product of the slot's previous tile completed
+                    // before this S); the logits are loaded again after it rather than held beside it.
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + s * 128 + 32 * j, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(t_o + s * 128 + 32 * j, o);
+                    }
+                    tmem_st_wait();
                 }
                 const float mb = m_ref == -INFINITY ? 0.f : m_ref * c2;
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
@@ -846,21 +870,13 @@ __global__ void __launch_bounds__(kBound, 1)
                         pk[e] = pack_bf16(p0, p1);
                     }
                     tmem_st16(t_s + 16 * j, pk);
-                }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                // O of this slot is idle here: the product of its previous tile completed before this S
-                if (any_resc && it != it0) {
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + s * 128 + 32 * j, o);
-                        tmem_ld_wait();
-                        reg_fence(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(t_o + s * 128 + 32 * j, o);
+                    if (j == 2) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&mt.p_half[s]);
                     }
                 }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&mt.p_full[s]);
