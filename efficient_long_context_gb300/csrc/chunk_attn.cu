@@ -869,9 +869,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     for (int e = 0; e < 16; ++e) {
                         float a0, a1;
                         fma_f32x2(xj[2 * e], xj[2 * e + 1], cv, mv, a0, a1);
-                        float p0, p1;
-                        if (j == kKeys / 32 - 1 && e == 15) exp2_fma_x2(a0, a1, p0, p1);
-                        else p0 = ex2(a0), p1 = ex2(a1);
+                        const float p0 = ex2(a0), p1 = ex2(a1);
                         add_f32x2(ls[2 * (e & 1)], ls[2 * (e & 1) + 1], p0, p1);
                         pk[e] = pack_bf16(p0, p1);
                     }
@@ -1002,77 +1000,95 @@ __global__ void __launch_bounds__(kBound, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the units that a share's border cut: one warp per row, the parts'
-// weights found by its lanes, the outputs added in the order of the parts.
+// Merge of the units that a share's border cut: o = sum_k w_k o_k / sum_k w_k l_k with
+// w_k = exp(scale (m_k - max m)), the parts in their order with a running maximum.
+// A warp joins kRowsW rows; kParts parts of each are loaded at once, outputs beside
+// their maxima and sums, so that a row costs one trip to L2 rather than two.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8, kMergeBatch = 8;
+constexpr int kMergeWarps = 8, kMergeBlocks = 8;  // blocks of a unit
 
-template <int D> __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+template <int D, int kRowsW, int kParts>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ChunkHead hd = p.heads[blockIdx.x];
     if (hd.n_parts == 0) return;
-    const int lane = threadIdx.x & 31;
-    const int g = p.Hq / p.Hkv;
-    const int rr = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the unit, slot-major
-    const int s = rr / p.rows_cap, row = rr % p.rows_cap;
-    const int n_tok = min(p.tile_tokens, hd.cnt - s * p.tile_tokens);
-    if (s >= p.slots_cap || row >= n_tok * g) return;
-    // part i: the head's own (second) partial, then the first partial of the lane's next CTAs
-    auto index = [&](int i) -> long long {
-        const long long id = i == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + (long long)i * p.lanes);
-        return (id * p.slots_cap + s) * p.rows_cap + row;
-    };
     const float c2 = p.scale_log2;
-    float M = -INFINITY;
-    for (int i = lane; i < hd.n_parts; i += 32) M = fmaxf(M, p.part_ml[index(i)].x);
+    // rows of the unit, slot-major: the blocks of a unit stride over them
+    for (int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kRowsW; r0 < p.slots_cap * p.rows_cap;
+         r0 += gridDim.y * kMergeWarps * kRowsW) {
+    int slot[kRowsW], row[kRowsW];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mb = M == -INFINITY ? 0.f : M * c2;
-    constexpr int E = D / 32;
-    float acc[E], L = 0.f;
+    for (int i = 0; i < kRowsW; ++i) {
+        slot[i] = (r0 + i) / p.rows_cap;
+        row[i] = (r0 + i) % p.rows_cap;
+    }
+    bool live[kRowsW];  // a token stands there
+    float M[kRowsW], L[kRowsW], acc[kRowsW][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int i0 = 0; i0 < hd.n_parts; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < hd.n_parts) {
-            const float2 ml = p.part_ml[index(i0 + lane)];
-            w = ex2(ml.x * c2 - mb);
-            L += w * ml.y;
-        }
-        const int k1 = min(32, hd.n_parts - i0);
-        // eight parts' loads at a time; a part without keys for this row (weight 0) wrote no output
-        for (int k0 = 0; k0 < k1; k0 += kMergeBatch) {
-            float wk[kMergeBatch], x[kMergeBatch][E];
+    for (int i = 0; i < kRowsW; ++i) {
+        live[i] = slot[i] < p.slots_cap && row[i] < min(p.tile_tokens, hd.cnt - slot[i] * p.tile_tokens) * g;
+        M[i] = -INFINITY;
+        L[i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kMergeBatch; ++k) {
-                wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-                if (k0 + k >= k1) wk[k] = 0.f;
-                if (wk[k] != 0.f) {
-                    const float *src = p.part_o + index(i0 + k0 + k) * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(src);
-                        x[k][0] = f.x, x[k][1] = f.y, x[k][2] = f.z, x[k][3] = f.w;
-                    } else {
-                        const float2 f = *reinterpret_cast<const float2 *>(src);
-                        x[k][0] = f.x, x[k][1] = f.y;
-                    }
+        for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+    }
+    for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
+        float2 ml[kParts][kRowsW];
+        float x[kParts][kRowsW][E];
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+            for (int i = 0; i < kRowsW; ++i) {
+                ml[k][i] = make_float2(-INFINITY, 0.f);
+                if (!live[i] || k0 + k >= hd.n_parts) continue;
+                // part k: the head's own (second) partial, then the first partial of the lane's next CTAs
+                const long long id = k0 + k == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + (long long)(k0 + k) * p.lanes);
+                const long long at = (id * p.slots_cap + slot[i]) * p.rows_cap + row[i];
+                ml[k][i] = p.part_ml[at];
+                const float *src = p.part_o + at * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src);
+                    x[k][i][0] = f.x, x[k][i][1] = f.y, x[k][i][2] = f.z, x[k][i][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2 *>(src);
+                    x[k][i][0] = f.x, x[k][i][1] = f.y;
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kMergeBatch; ++k)
-                if (wk[k] != 0.f)
+        for (int i = 0; i < kRowsW; ++i) {
+            float m = M[i];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], x[k][e], acc[e]);
+            for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k][i].x);
+            const float mb = m == -INFINITY ? 0.f : m * c2;
+            const float w0 = ex2(M[i] * c2 - mb);
+            M[i] = m;
+            L[i] *= w0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] *= w0;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (ml[k][i].x == -INFINITY) continue;  // a part without keys for this row wrote no output
+                const float w = ex2(ml[k][i].x * c2 - mb);
+                L[i] = fmaf(w, ml[k][i].y, L[i]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[i][e] = fmaf(w, x[k][i][e], acc[i][e]);
+            }
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = L > 0.f ? 1.f / L : L;  // a NaN sum stays
-    const long long out = ((long long)hd.tok0 + s * p.tile_tokens + row / g) * p.Hq + hd.kv * g + row % g;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + out * D + lane * E);
+    for (int i = 0; i < kRowsW; ++i) {
+        if (!live[i]) continue;
+        const float inv = L[i] > 0.f ? 1.f / L[i] : L[i];  // a NaN sum stays
+        const long long out = ((long long)hd.tok0 + slot[i] * p.tile_tokens + row[i] / g) * p.Hq + hd.kv * g + row[i] % g;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + out * D + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[out] = M * p.scale + logf(L);
+        for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[i][e] * inv, acc[i][e + 1] * inv);
+        if (lane == 0 && p.lse) p.lse[out] = M[i] * p.scale + logf(L[i]);
+    }
+    }
 }
 
 template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
@@ -1104,14 +1120,20 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
         ProfScope ps("chunk_attn", stream);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;
     }
+    const int rows = p.slots_cap * p.rows_cap;
+    const int per_warp = rows <= kMergeWarps ? 1 : 2;
     cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3(p.lanes * p.per_lane, (p.slots_cap * p.rows_cap + kMergeWarps - 1) / kMergeWarps);
+    const int row_blocks = (rows + kMergeWarps * per_warp - 1) / (kMergeWarps * per_warp);
+    mc.gridDim = dim3(p.lanes * p.per_lane, row_blocks < kMergeBlocks ? row_blocks : kMergeBlocks);
     mc.blockDim = dim3(kMergeWarps * 32);
     mc.stream = stream;
     mc.attrs = attr;
     mc.numAttrs = 1;
     ProfScope ps("chunk_merge", stream);
-    if (cudaError_t e = cudaLaunchKernelEx(&mc, chunk_merge_kernel<D>, p); e != cudaSuccess) return e;
+    if (cudaError_t e = per_warp == 1 ? cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, 1, 8>, p)
+                                      : cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, 2, 3>, p);
+        e != cudaSuccess)
+        return e;
     return cudaGetLastError();
 }
 
