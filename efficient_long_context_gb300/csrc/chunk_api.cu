@@ -130,6 +130,7 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o = static_cast<__nv_bfloat16 *>(o);
+    p.o_aligned32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
     p.lse = lse;
     p.status = reinterpret_cast<uint32_t *>(ws);
     p.plan = reinterpret_cast<ChunkPlan *>(ws + L.plan_off);

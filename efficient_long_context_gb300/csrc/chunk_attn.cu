@@ -56,18 +56,17 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a tile
 constexpr int kKeys = 128;  // keys of a tile
-constexpr int kNumK = 3, kNumV = 2;
-static_assert(kNumV == 2, "the clearing warp counts two stages");
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10;
 constexpr int kThreads = 352;
 // At most three of the eleven warps sit on a scheduler: 168 registers a thread
 // fit (3 x 32 x 168 of 16K), so the bound is taken for 384 threads.
 constexpr int kBound = 384;
-constexpr int kFlagRing = 8;
+constexpr int kFlagRing = 16;
 // A share of fewer key tiles than this is not worth a CTA of its own.
 constexpr int kMinTiles = 2;
 
 template <int D> struct Cfg {
+    static constexpr int kNumK = D == 128 ? 3 : 6, kNumV = D == 128 ? 2 : 4;  // stages: 160 KB in flight
     static constexpr int kSub = D / 64;             // 128-byte swizzle atoms per row
     static constexpr int kTile = kRows * D * 2;     // one 128 x D bf16 tile
     static constexpr int kQ0 = 0;
@@ -91,10 +90,11 @@ struct Segment {
 
 constexpr int kSegRing = 2;
 
+constexpr int kMaxK = 6, kMaxV = 4;
 struct Meta {
-    uint64_t k_full[kNumK], k_empty[kNumK], v_full[kNumV], v_empty[kNumV];
+    uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
     uint64_t q_full[2], q_empty[2];
-    uint64_t ve_full[kNumV];  // a value tile with unseen rows arrived: warp 10 clears them, then completes v_full
+    uint64_t ve_full[kMaxV];  // a value tile with unseen rows arrived: warp 10 clears them, then completes v_full
     uint64_t s_full[2], o_free[2];
     uint64_t p_half[2], p_full[2];  // the first 64 keys of a P tile are stored (and O rescaled); all are
     uint64_t o_full[2];  // slot s's O complete, for slot s's threads
@@ -109,6 +109,15 @@ struct Meta {
     float2 ml[kRows];             // slot 1's running max and sum, for slot 0 (shared row tile)
 };
 static_assert(sizeof(Meta) <= 2048, "barriers and metadata must fit their shared-memory region");
+
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
 
 // The products are issued under a predicate by a whole warp rather than inside a
 // one-lane branch: warp-uniform descriptors stay in uniform registers.
@@ -144,6 +153,12 @@ __device__ __forceinline__ void tc_commit_if(uint32_t el, uint64_t *bar) {
         : "memory");
 }
 
+__device__ __forceinline__ void st_global_32b(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
     asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
@@ -153,9 +168,11 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
                    "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-// Byte offset of (row, 16-byte chunk c) in a 128-byte-swizzled tile of 128 rows.
-__device__ __forceinline__ uint32_t sw128(int row, int c) {
-    return (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+// Key and value tiles lie in groups of 8 tokens, a 1 KB swizzle atom of 64 channels
+// after the other within a group, so that one copy box brings whole rows of any
+// multiple of 8 tokens. Byte offset of (token, 16-byte chunk c):
+template <int D> __device__ __forceinline__ uint32_t kv_offset(int row, int c) {
+    return (row >> 3) * (D * 16) + (c >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
 // Key tiles a run of tokens at positions [first, last] sees.
@@ -296,19 +313,25 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
 // ---------------------------------------------------------------------------
 // Main kernel
 // ---------------------------------------------------------------------------
-// The shares of a lane: `total` key tiles over `eff` CTAs.
+// The shares of a lane: `total` key tiles over `eff` CTAs, equal up to borders that
+// move to a unit's end within kSnap key tiles (a quarter of a share at most): a
+// cut costs two partial epilogues and a merge, as much as a few tiles.
+constexpr int kSnap = 3;
 struct Shares {
     long long total;
-    int eff;
-    __device__ long long begin(int j) const { return total * j / eff; }
-    // the CTA of the lane whose share holds tile x
-    __device__ int owner(long long x) const { return (int)(((x + 1) * eff - 1) / total); }
+    int eff, snap;
+    __device__ long long border(int j) const { return total * j / eff; }  // before it moves
+    // border x, which falls into the unit [u0, u0 + n), where it ends up
+    __device__ long long moved(long long x, long long u0, int n) const {
+        return x - u0 <= snap ? u0 : u0 + n - x <= snap ? u0 + n : x;
+    }
 };
 __device__ __forceinline__ Shares shares_of(const ChunkParams &p, const ChunkPlan &pl) {
     Shares s;
     s.total = (long long)(p.Hkv / p.lanes) * pl.tiles;
     const long long fit = s.total / kMinTiles;
     s.eff = (int)max(1LL, min((long long)p.per_lane, fit));
+    s.snap = (int)min((long long)kSnap, s.total / s.eff / 4);
     return s;
 }
 
@@ -341,6 +364,7 @@ __global__ void __launch_bounds__(kBound, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = Cfg<D>;
+    constexpr int kNumK = C::kNumK, kNumV = C::kNumV;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Meta &mt = *reinterpret_cast<Meta *>(smem + C::kMeta);
@@ -420,10 +444,24 @@ __global__ void __launch_bounds__(kBound, 1)
         if (pl.tiles > 0) {
             const Shares sh = shares_of(p, pl);
             if (j < sh.eff) {
-                long long x = sh.begin(j);
-                const long long x1 = sh.begin(j + 1);
+                // both borders of the share, moved; the unit the first one ends up in
+                long long x = sh.border(j), x1 = sh.border(j + 1);
                 int kvo = (int)(x / pl.tiles);
                 int u = find_unit(p.units, pl.units, x - kvo * pl.tiles, lane);
+                if (x1 < sh.total) {
+                    const long long base = x1 / pl.tiles * pl.tiles;
+                    const ChunkUnit e = p.units[find_unit(p.units, pl.units, x1 - base, lane)];
+                    x1 = sh.moved(x1, base + e.start, e.n_kt);
+                }
+                {
+                    const ChunkUnit e = p.units[u];
+                    const long long u0 = kvo * pl.tiles + e.start;
+                    x = sh.moved(x, u0, e.n_kt);
+                    if (x == u0 + e.n_kt && ++u == pl.units) {
+                        u = 0;
+                        ++kvo;
+                    }
+                }
                 while (x < x1 && alive) {
                     const ChunkUnit un = p.units[u];
                     const int a = (int)(x - kvo * pl.tiles - un.start);
@@ -441,7 +479,10 @@ __global__ void __launch_bounds__(kBound, 1)
                     const bool starts = a == 0, ends = a + n_tiles == un.n_kt;
                     sg.partial = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
                     if (starts && !ends) {
-                        head.n_parts = sh.owner(x + un.n_kt - 1) - j + 1;
+                        // the CTAs whose share begins inside the unit hold the other parts
+                        int k = j + 1;
+                        while (k < sh.eff && sh.moved(sh.border(k), x, un.n_kt) < x + un.n_kt) ++k;
+                        head.n_parts = k - j;
                         head.tok0 = un.tok0;
                         head.cnt = un.cnt;
                         head.kv = sg.kv;
@@ -517,9 +558,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             }
                             __syncwarp();
                             if (lane < n_box)
-                                for (int h = 0; h < C::kSub; ++h)
-                                    tma_load_3d(ks + h * (kRows * 128) + lane * box * 128, &tm_k, &mt.k_full[sk], 64 * h,
-                                                sg.kv, tok);
+                                tma_load_5d(ks + lane * box * D * 2, &tm_k, &mt.k_full[sk], 0, 0, 0, tok >> 3, sg.kv);
                             if (gi >= (uint32_t)kNumV &&
                                 !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, p.status)) {
                                 ++gk;
@@ -532,8 +571,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
                             __syncwarp();
                             if (lane < n_box)
-                                for (int h = 0; h < C::kSub; ++h)
-                                    tma_load_3d(vs + h * (kRows * 128) + lane * box * 128, &tm_v, full, 64 * h, sg.kv, tok);
+                                tma_load_5d(vs + lane * box * D * 2, &tm_v, full, 0, 0, 0, tok >> 3, sg.kv);
                             ++gv;
                         } else {
                             // page sizes without a copy box: the lanes gather the rows, 16 bytes at a time
@@ -553,7 +591,7 @@ __global__ void __launch_bounds__(kBound, 1)
                                     if (pg < 0 || pg >= p.num_pages) wrong = 1;
                                     else src = (((long long)pg * p.page_size + key % p.page_size) * p.Hkv + sg.kv) * D + 8 * c;
                                 }
-                                const uint32_t dk = smem_u32(ks + sw128(row, c)), dv = smem_u32(vs + sw128(row, c));
+                                const uint32_t dk = smem_u32(ks + kv_offset<D>(row, c)), dv = smem_u32(vs + kv_offset<D>(row, c));
                                 const uint32_t bytes = src >= 0 ? 16 : 0;  // 0: zero fill
                                 const __nv_bfloat16 *a = p.k + max(src, 0LL), *b2 = p.v + max(src, 0LL);
                                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk), "l"(a), "r"(bytes) : "memory");
@@ -606,13 +644,14 @@ __global__ void __launch_bounds__(kBound, 1)
             constexpr uint32_t kIdescO = idesc_f16(1, 1, 0, 1, kRows, D);      // bf16, V MN-major
             constexpr uint32_t kTileU = C::kTile >> 4;
             const uint64_t dq = desc_sw128(smem_u32(smem + C::kQ0), 16, 1024);
-            const uint64_t dk = desc_sw128(smem_u32(smem + C::kK0), 16, 1024);
-            const uint64_t dv = desc_sw128(smem_u32(smem + C::kV0), kKeys * 128, 1024);
+            const uint64_t dk = desc_sw128(smem_u32(smem + C::kK0), 16, D * 16);
+            const uint64_t dv = desc_sw128(smem_u32(smem + C::kV0), 1024, D * 16);
             auto issue_s = [&](int s, uint64_t qd, uint64_t kd) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
-                    mma_ss_if(el, tm + s * 128, qd + off, kd + off, kIdescS, ks > 0);
+                    const uint32_t qo = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+                    const uint32_t ko = ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4;
+                    mma_ss_if(el, tm + s * 128, qd + qo, kd + ko, kIdescS, ks > 0);
                 }
                 tc_commit_if(el, &mt.s_full[s]);
             };
@@ -621,7 +660,7 @@ __global__ void __launch_bounds__(kBound, 1)
 #pragma unroll
                 for (int k = 0; k < kKeys / 32; ++k) {
                     const int kk = h * (kKeys / 32) + k;
-                    mma_ts_if(el, tm + C::kTmemO + s * 128, tm + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                    mma_ts_if(el, tm + C::kTmemO + s * 128, tm + s * 128 + kk * 8, vd + (uint64_t)((kk * 16 * D * 2) >> 4),
                               kIdescO, kk > 0 ? 1u : acc0);
                 }
             };
@@ -737,7 +776,7 @@ __global__ void __launch_bounds__(kBound, 1)
         // ---------------- unseen value rows: a page that reaches past the unit's keys holds
         // anything there, and 0 * NaN is NaN ----------------
         uint32_t gk = 0;
-        uint32_t ne[kNumV] = {};  // such tiles handled per stage
+        uint32_t ne = 0;  // bit per stage: parity of such tiles handled
         bool ok = true;
         for (int i = 0; ok; ++i) {
             const int r = i % kSegRing;
@@ -751,13 +790,13 @@ __global__ void __launch_bounds__(kBound, 1)
                 int r0, r1;
                 if (!unseen_rows(sg, p.window, it, r0, r1)) continue;
                 const uint32_t sv = (gk + it) % kNumV;
-                if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (sv ? ne[1] : ne[0]) & 1, abort, p.status))) break;
-                if (sv) ++ne[1]; else ++ne[0];
+                if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (ne >> sv) & 1, abort, p.status))) break;
+                ne ^= 1u << sv;
                 uint8_t *vs = smem + C::kV0 + sv * C::kTile;
                 constexpr int kCh = D / 8;
                 for (int e = lane; e < (r0 + kKeys - r1) * kCh; e += 32) {
                     const int k = e / kCh, row = k < r0 ? k : r1 + k - r0;
-                    *reinterpret_cast<uint4 *>(vs + sw128(row, e % kCh)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(vs + kv_offset<D>(row, e % kCh)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -947,10 +986,18 @@ __global__ void __launch_bounds__(kBound, 1)
                         }
                         if (mine) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                reinterpret_cast<uint4 *>(dst + 32 * j)[e] =
-                                    make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                                               pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[16 * e + 2 * i], f[16 * e + 2 * i + 1]);
+                                if (p.o_aligned32) {
+                                    st_global_32b(dst + 32 * j + 16 * e, w);
+                                } else {
+                                    uint4 *to = reinterpret_cast<uint4 *>(dst + 32 * j + 16 * e);
+                                    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                }
+                            }
                         }
                     }
                     if (mine && p.lse) p.lse[tok * p.Hq + h] = m * p.scale + logf(l);
@@ -977,9 +1024,12 @@ __global__ void __launch_bounds__(kBound, 1)
                             }
                             if (mine) {
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    reinterpret_cast<float4 *>(dst + 32 * j)[e] =
-                                        make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                                for (int e = 0; e < 4; ++e) {
+                                    uint32_t w[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 * e + i]);
+                                    st_global_32b(dst + 32 * j + 8 * e, w);
+                                }
                             }
                         }
                     }
@@ -1093,10 +1143,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 
 template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
-    const long long tokens = (long long)p.num_pages * p.page_size;
-    const int box = p.box ? p.box : 8;  // (unused maps are valid ones)
+    const long long tokens = p.box ? (long long)p.num_pages * p.page_size : 8;  // (unused maps are valid ones)
+    const int box = p.box ? p.box : 8;
     if (!encode_rows_map_3d(&tq, p.q, p.n, p.Hq, D, p.Hq / p.Hkv, p.tile_tokens) ||
-        !encode_kv_map_3d(&tk, p.k, tokens, p.Hkv, D, box) || !encode_kv_map_3d(&tv, p.v, tokens, p.Hkv, D, box))
+        !encode_kv_groups_map(&tk, p.k, tokens, p.Hkv, D, box) || !encode_kv_groups_map(&tv, p.v, tokens, p.Hkv, D, box))
         return cudaErrorInvalidValue;
     static SmemLimit limit;
     if (cudaError_t e = limit.ensure((const void *)chunk_attn_kernel<D>, Cfg<D>::kSmem); e != cudaSuccess) return e;

@@ -362,6 +362,7 @@ struct ChunkParams {
     int rows_cap, slots_cap;         // rows and slots of a partial
     float scale, scale_log2;
     __nv_bfloat16 *o;                // [n, Hq, d]
+    bool o_aligned32;                // o is 32-byte aligned
     float *lse;                      // [n, Hq] or null
     uint32_t *status;
     int32_t *seq_units;              // [B] scratch of the plan
@@ -375,6 +376,11 @@ struct ChunkParams {
 // Units a call with these sizes can have at most (bound for the workspace).
 long long chunk_max_units(long long n, int B, int tile_tokens);
 cudaError_t launch_chunk_attention(const ChunkParams &p, int d, cudaStream_t stream);
+
+// prefill_tc.cu: 5-D tensor map (64 channels, 8 tokens, halves of a head, groups of 8
+// tokens, Hkv) over bf16 [tokens, Hkv, d] rows (tokens a multiple of 8), box of
+// box_tokens whole rows of one head, 128-byte swizzle, zero fill.
+bool encode_kv_groups_map(CUtensorMap *m, const void *base, long long tokens, int Hkv, int d, int box_tokens);
 
 // merge.cu: exact merge of normalised partials over disjoint key sets.
 cudaError_t launch_merge_partials(const float *o_parts, const float *lse_parts, int n_parts, int n_rows, int Hq, int d,

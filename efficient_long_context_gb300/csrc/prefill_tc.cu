@@ -1468,6 +1468,19 @@ bool encode_kv_map_3d(CUtensorMap *m, const void *base, long long tokens, int Hk
     return encode_rows_map_3d(m, base, tokens, Hkv, d, 1, box_tokens);
 }
 
+bool encode_kv_groups_map(CUtensorMap *m, const void *base, long long tokens, int Hkv, int d, int box_tokens) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)Hkv * d * 2;  // bytes of a token
+    cuuint64_t dims[5] = {64, 8, (cuuint64_t)(d / 64), (cuuint64_t)(tokens / 8), (cuuint64_t)Hkv};
+    cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)d * 2};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)(d / 64), (cuuint32_t)(box_tokens / 8), 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_units_per_kv(int nblk, int g) { return (g % 2 == 0) ? nblk * (g / 2) : g * ((nblk + 1) / 2); }
 
 cudaError_t launch_prefill_tc(const TcParams &p, const void *k16, const void *v, int d, cudaStream_t stream) {
