@@ -127,6 +127,7 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
     p.per_lane = L.ctas / p.lanes;
     p.rows_cap = L.rows_cap;
     p.slots_cap = L.slots_cap;
+    p.direct = (B <= 32 && p.max_new <= 2 * p.tile_tokens) || (B == 1 && n <= 32 * 2 * p.tile_tokens);
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o = static_cast<__nv_bfloat16 *>(o);

@@ -181,6 +181,30 @@ __device__ __forceinline__ void key_tiles(int first, int last, int window, int &
     hi = last / kKeys;
 }
 
+// New tokens of sequence b (first row of q, cached tokens), or 0 when there are
+// none or its lengths are impossible (wrong).
+__device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0, int &len, bool &wrong) {
+    tok0 = p.q_indptr[b];
+    const int nb = p.q_indptr[b + 1] - tok0;
+    len = p.kv_lens[b];
+    wrong = nb > 0 && (nb > p.max_new || len < nb || (long long)len > (long long)p.max_pages * p.page_size);
+    return wrong ? 0 : nb;
+}
+
+// The unit that begins at token i of a sequence's nb (i < nb).
+__device__ __forceinline__ ChunkUnit unit_at(const ChunkParams &p, int b, int tok0, int nb, int len, int i) {
+    ChunkUnit u;
+    u.b = b;
+    u.tok0 = tok0 + i;
+    u.cnt = min(2 * p.tile_tokens, nb - i);
+    u.pos0 = len - nb + i;
+    int hi;
+    key_tiles(u.pos0, u.pos0 + u.cnt - 1, p.window, u.kt_lo, hi);
+    u.n_kt = hi - u.kt_lo + 1;
+    u.start = 0;
+    return u;
+}
+
 // ---------------------------------------------------------------------------
 // Plan: one block. Checks the lengths, lists the units and their key tiles.
 // ---------------------------------------------------------------------------
@@ -208,45 +232,28 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        *p.status = 0;
+        p.plan->flags = 0;
         carry[0] = carry[1] = 0;
     }
     int bad = 0;
     for (int b = tid; b < p.B; b += kPlanThreads) bad |= p.q_indptr[b + 1] < p.q_indptr[b];
     if (tid == 0) bad |= p.q_indptr[0] != 0 || p.q_indptr[p.B] != p.n;
     if (__syncthreads_or(bad)) {  // no token's sequence is known
-        if (tid == 0) {
-            set_status(p.status, ORTHROS_DEV_BAD_LENGTH);
-            *p.plan = ChunkPlan{0, 0, 0};
-        }
+        if (tid == 0) *p.plan = ChunkPlan{0, ORTHROS_DEV_BAD_LENGTH, 0};
         fill_nan(p, 0, p.n, d, tid, kPlanThreads);
         return;
     }
     const int ut = 2 * p.tile_tokens;
-    // new tokens of sequence b, or 0 when there are none or its lengths are impossible
-    auto tokens_of = [&](int b, int &tok0, int &len, bool &wrong) -> int {
-        tok0 = p.q_indptr[b];
-        const int nb = p.q_indptr[b + 1] - tok0;
-        len = p.kv_lens[b];
-        wrong = nb > 0 && (nb > p.max_new || len < nb || (long long)len > (long long)p.max_pages * p.page_size);
-        return wrong ? 0 : nb;
-    };
-    // key tiles of the unit that begins at token i of nb, whose first position is t0
-    auto unit_tiles = [&](int i, int nb, int t0, int &lo) -> int {
-        int hi;
-        key_tiles(t0 + i, t0 + min(nb, i + ut) - 1, p.window, lo, hi);
-        return hi - lo + 1;
-    };
     for (int b = warp; b < p.B; b += kPlanThreads / 32) {
-        int tok0, len, lo;
+        int tok0, len;
         bool wrong;
-        const int nb = tokens_of(b, tok0, len, wrong);
+        const int nb = new_tokens(p, b, tok0, len, wrong);
         if (wrong) {
-            if (lane == 0) set_status(p.status, ORTHROS_DEV_BAD_LENGTH);
+            if (lane == 0) set_status(&p.plan->flags, ORTHROS_DEV_BAD_LENGTH);
             fill_nan(p, tok0, p.q_indptr[b + 1], d, lane, 32);
         }
         long long tiles = 0;
-        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_tiles(i, nb, len - nb, lo);
+        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_at(p, b, tok0, nb, len, i).n_kt;
         tiles = warp_scan(tiles, lane);
         if (lane == 31) {
             p.seq_units[b] = (nb + ut - 1) / ut;
@@ -282,29 +289,23 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         }
         __syncthreads();
     }
-    if (tid == 0) *p.plan = ChunkPlan{(int)carry[0], 0, carry[1]};
+    if (tid == 0) {
+        p.plan->units = (int)carry[0];
+        p.plan->tiles = carry[1];
+    }
     for (int b = warp; b < p.B; b += kPlanThreads / 32) {
         int tok0, len;
         bool wrong;
-        const int nb = tokens_of(b, tok0, len, wrong);
+        const int nb = new_tokens(p, b, tok0, len, wrong);
         const int u0 = p.seq_units[b];
         long long at = p.seq_tiles[b];
         for (int i0 = 0; i0 < nb; i0 += 32 * ut) {
             const int i = i0 + lane * ut;
-            int lo = 0;
-            const int w = i < nb ? unit_tiles(i, nb, len - nb, lo) : 0;
-            const long long sum = warp_scan(w, lane);
-            if (i < nb) {
-                ChunkUnit u;
-                u.b = b;
-                u.tok0 = tok0 + i;
-                u.cnt = min(ut, nb - i);
-                u.pos0 = len - nb + i;
-                u.kt_lo = lo;
-                u.n_kt = w;
-                u.start = at + sum - w;
-                p.units[u0 + i / ut] = u;
-            }
+            ChunkUnit u{};
+            if (i < nb) u = unit_at(p, b, tok0, nb, len, i);
+            const long long sum = warp_scan(u.n_kt, lane);
+            u.start = at + sum - u.n_kt;
+            if (i < nb) p.units[u0 + i / ut] = u;
             at += __shfl_sync(0xffffffffu, sum, 31);
         }
     }
@@ -372,8 +373,10 @@ __global__ void __launch_bounds__(kBound, 1)
     volatile int *abort = &mt.abort;
     const int g = p.Hq / p.Hkv;
     const int tt = p.tile_tokens;
+    uint32_t *status = &p.heads[blockIdx.x].flags;  // this CTA's; the merge collects them
 
     if (tid == 0) {
+        *status = 0;
         for (int i = 0; i < kNumK; ++i) {
             mbar_init(&mt.k_full[i], 1);
             mbar_init(&mt.k_empty[i], 1);
@@ -416,22 +419,72 @@ __global__ void __launch_bounds__(kBound, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = mt.tmem_base;
-    // the plan's kernel must have finished; the merge may start its set-up
+    // the merge may be launched; the plan's kernel, where there is one, must have finished
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == kCopyWarp) {
         // ---------------- segments and copies ----------------
-        const ChunkPlan pl = *p.plan;
+        // The batch's units: from the plan, or, when there are at most 32 (one per
+        // sequence, or those of a single sequence), one per lane of this warp.
+        ChunkPlan pl;
+        ChunkUnit own{};
+        if (p.direct) {
+            const int ut = 2 * tt;
+            const bool one = p.B == 1;  // lane = unit of the sequence, else lane = sequence
+            const int b = one ? 0 : lane;
+            int tok0 = 0, len = 0, nb = 0;
+            bool wrong = false, order = true;
+            if (b < p.B) {
+                nb = new_tokens(p, b, tok0, len, wrong);
+                order = p.q_indptr[b + 1] >= tok0;
+            }
+            if (lane == 0) order = order && p.q_indptr[0] == 0 && p.q_indptr[p.B] == p.n;
+            order = __all_sync(0xffffffffu, order);
+            if (!order || __any_sync(0xffffffffu, wrong)) {
+                // impossible lengths: NaN for their rows, or for all rows when no token's sequence is known
+                if (lane == 0 && blockIdx.x == 0) set_status(status, ORTHROS_DEV_BAD_LENGTH);
+                for (int k = 0; k < (one || !order ? 1 : p.B); ++k) {
+                    if (order && !__shfl_sync(0xffffffffu, (int)wrong, k)) continue;
+                    fill_nan(p, order ? p.q_indptr[k] : 0, order ? p.q_indptr[k + 1] : p.n, D,
+                             (int)blockIdx.x * 32 + lane, (int)gridDim.x * 32);
+                }
+            }
+            const int i = one ? lane * ut : 0;
+            if (order && i < nb) own = unit_at(p, b, tok0, nb, len, i);
+            const long long sum = warp_scan(own.n_kt, lane);
+            own.start = sum - own.n_kt;
+            pl.units = 32;
+            pl.tiles = __shfl_sync(0xffffffffu, sum, 31);
+        } else {
+            pl = *p.plan;
+        }
+        auto get_unit = [&](int u) -> ChunkUnit {
+            if (!p.direct) return p.units[u];
+            ChunkUnit r;
+            r.b = __shfl_sync(0xffffffffu, own.b, u);
+            r.tok0 = __shfl_sync(0xffffffffu, own.tok0, u);
+            r.cnt = __shfl_sync(0xffffffffu, own.cnt, u);
+            r.pos0 = __shfl_sync(0xffffffffu, own.pos0, u);
+            r.kt_lo = __shfl_sync(0xffffffffu, own.kt_lo, u);
+            r.n_kt = __shfl_sync(0xffffffffu, own.n_kt, u);
+            r.start = __shfl_sync(0xffffffffu, own.start, u);
+            return r;
+        };
+        // unit that holds key tile x of the list
+        auto find = [&](long long x) -> int {
+            if (!p.direct) return find_unit(p.units, pl.units, x, lane);
+            return 31 - __clz(__ballot_sync(0xffffffffu, own.n_kt > 0 && own.start <= x));
+        };
         const int ln = blockIdx.x % p.lanes, j = blockIdx.x / p.lanes;
-        ChunkHead head{0, 0, 0, 0};
+        ChunkHead head{};
         uint32_t gk = 0, gv = 0;  // key and value copies issued
         uint32_t nq[2] = {0, 0};  // query tiles issued per slot
         int ring = 0;
         bool alive = true;
         auto publish = [&](const Segment &sg) -> bool {
             const int r = ring % kSegRing;
-            if (ring >= kSegRing && !mbar_wait_warp(&mt.g_empty[r], ((ring / kSegRing) - 1) & 1, abort, p.status))
+            if (ring >= kSegRing && !mbar_wait_warp(&mt.g_empty[r], ((ring / kSegRing) - 1) & 1, abort, status))
                 return false;
             if (lane == 0) {
                 mt.seg[r] = sg;
@@ -447,23 +500,28 @@ __global__ void __launch_bounds__(kBound, 1)
                 // both borders of the share, moved; the unit the first one ends up in
                 long long x = sh.border(j), x1 = sh.border(j + 1);
                 int kvo = (int)(x / pl.tiles);
-                int u = find_unit(p.units, pl.units, x - kvo * pl.tiles, lane);
+                int u = find(x - kvo * pl.tiles);
+                auto next_unit = [&]() {  // (a lane without a unit is passed over)
+                    do {
+                        if (++u == pl.units) {
+                            u = 0;
+                            ++kvo;
+                        }
+                    } while (p.direct && __shfl_sync(0xffffffffu, own.n_kt, u) == 0);
+                };
                 if (x1 < sh.total) {
                     const long long base = x1 / pl.tiles * pl.tiles;
-                    const ChunkUnit e = p.units[find_unit(p.units, pl.units, x1 - base, lane)];
+                    const ChunkUnit e = get_unit(find(x1 - base));
                     x1 = sh.moved(x1, base + e.start, e.n_kt);
                 }
                 {
-                    const ChunkUnit e = p.units[u];
+                    const ChunkUnit e = get_unit(u);
                     const long long u0 = kvo * pl.tiles + e.start;
                     x = sh.moved(x, u0, e.n_kt);
-                    if (x == u0 + e.n_kt && ++u == pl.units) {
-                        u = 0;
-                        ++kvo;
-                    }
+                    if (x == u0 + e.n_kt) next_unit();
                 }
                 while (x < x1 && alive) {
-                    const ChunkUnit un = p.units[u];
+                    const ChunkUnit un = get_unit(u);
                     const int a = (int)(x - kvo * pl.tiles - un.start);
                     const int n_tiles = (int)min((long long)(un.n_kt - a), x1 - x);
                     Segment sg;
@@ -503,7 +561,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     if (!(alive = publish(sg))) break;
                     // query tiles (rows past the tile's tokens keep whatever was there: their results are dropped)
                     for (int s = 0; alive && s < (sg.pair ? 2 : 1); ++s) {
-                        if (nq[s] > 0 && !mbar_wait_warp(&mt.q_empty[s], (nq[s] - 1) & 1, abort, p.status)) {
+                        if (nq[s] > 0 && !mbar_wait_warp(&mt.q_empty[s], (nq[s] - 1) & 1, abort, status)) {
                             alive = false;
                             break;
                         }
@@ -544,14 +602,14 @@ __global__ void __launch_bounds__(kBound, 1)
                         const int tok = tok_next, bad = bad_next;
                         if (it + 1 < sg.nkt) tok_next = look(sg.kt0 + it + 1, bad_next);
                         if (gi >= (uint32_t)kNumK &&
-                            !mbar_wait_warp(&mt.k_empty[sk], ((gi / kNumK) - 1) & 1, abort, p.status)) {
+                            !mbar_wait_warp(&mt.k_empty[sk], ((gi / kNumK) - 1) & 1, abort, status)) {
                             alive = false;
                             break;
                         }
                         uint8_t *ks = smem + C::kK0 + sk * C::kTile, *vs = smem + C::kV0 + sv * C::kTile;
                         if (box) {
                             const bool any_bad = __any_sync(0xffffffffu, bad);
-                            if (any_bad && lane == 0) set_status(p.status, ORTHROS_DEV_BAD_PAGE);
+                            if (any_bad && lane == 0) set_status(status, ORTHROS_DEV_BAD_PAGE);
                             if (lane == 0) {
                                 mt.bad[gi % kFlagRing] = any_bad;
                                 mbar_arrive_expect_tx(&mt.k_full[sk], C::kTile);
@@ -560,7 +618,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             if (lane < n_box)
                                 tma_load_5d(ks + lane * box * D * 2, &tm_k, &mt.k_full[sk], 0, 0, 0, tok >> 3, sg.kv);
                             if (gi >= (uint32_t)kNumV &&
-                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, p.status)) {
+                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, status)) {
                                 ++gk;
                                 alive = false;
                                 break;
@@ -576,7 +634,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         } else {
                             // page sizes without a copy box: the lanes gather the rows, 16 bytes at a time
                             if (gi >= (uint32_t)kNumV &&
-                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, p.status)) {
+                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, status)) {
                                 alive = false;
                                 break;
                             }
@@ -601,7 +659,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             fence_proxy_async_smem();
                             wrong = __any_sync(0xffffffffu, wrong);
                             if (lane == 0) {
-                                if (wrong) set_status(p.status, ORTHROS_DEV_BAD_PAGE);
+                                if (wrong) set_status(status, ORTHROS_DEV_BAD_PAGE);
                                 mt.bad[gi % kFlagRing] = wrong;
                                 mbar_arrive(&mt.k_full[sk]);
                                 mbar_arrive(&mt.v_full[sv]);
@@ -611,10 +669,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         ++gk;
                     }
                     x += n_tiles;
-                    if (++u == pl.units) {
-                        u = 0;
-                        ++kvo;
-                    }
+                    next_unit();
                 }
             }
         }
@@ -624,16 +679,20 @@ __global__ void __launch_bounds__(kBound, 1)
             publish(sg);
         }
         if (lane == 0) {
-            p.heads[blockIdx.x] = head;
+            ChunkHead &to = p.heads[blockIdx.x];
+            to.n_parts = head.n_parts;
+            to.tok0 = head.tok0;
+            to.cnt = head.cnt;
+            to.kv = head.kv;
             // nothing may be in flight when the CTA leaves
             if (p.box) {
                 for (uint32_t i = gk > (uint32_t)kNumK ? gk - kNumK : 0; i < gk; ++i)
-                    mbar_wait_drain(&mt.k_full[i % kNumK], (i / kNumK) & 1, p.status);
+                    mbar_wait_drain(&mt.k_full[i % kNumK], (i / kNumK) & 1, status);
                 for (uint32_t i = gv > (uint32_t)kNumV ? gv - kNumV : 0; i < gv; ++i)
-                    mbar_wait_drain(&mt.v_full[i % kNumV], (i / kNumV) & 1, p.status);
+                    mbar_wait_drain(&mt.v_full[i % kNumV], (i / kNumV) & 1, status);
             }
             for (int s = 0; s < 2; ++s)
-                if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, p.status);
+                if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, status);
         }
     } else if (warp == kMmaWarp) {
         // ---------------- tcgen05.mma issuer ----------------
@@ -671,7 +730,7 @@ __global__ void __launch_bounds__(kBound, 1)
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 const int r = i % kSegRing;
-                if (!(ok = mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status))) break;
+                if (!(ok = mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status))) break;
                 // (broadcast: known to be the same in every lane, as everything that follows from them)
                 const Segment &sr = mt.seg[r];
                 const bool end = uniform(sr.end) != 0, pair = uniform(sr.pair) != 0;
@@ -682,11 +741,11 @@ __global__ void __launch_bounds__(kBound, 1)
                 if (end) break;
                 auto value_tile = [&](int it) -> bool {
                     const uint32_t gi = gk + it;
-                    return mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, p.status);
+                    return mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, status);
                 };
                 auto key_tile = [&](int it) -> bool {
                     const uint32_t gi = gk + it;
-                    return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, p.status);
+                    return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, status);
                 };
                 auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
                 auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
@@ -694,13 +753,13 @@ __global__ void __launch_bounds__(kBound, 1)
                 // before the slot's first product of the segment, its O is free
                 auto pv_tile = [&](int s, int it, bool first) -> bool {
                     if (first) {
-                        if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, p.status)) return false;
+                        if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, status)) return false;
                         ++oc[s];
                     }
-                    if (!mbar_wait_warp(&mt.p_half[s], pc[s] & 1, abort, p.status)) return false;
+                    if (!mbar_wait_warp(&mt.p_half[s], pc[s] & 1, abort, status)) return false;
                     tc_fence_after();
                     issue_pv(s, 0, vdesc(it), !first);
-                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, p.status)) return false;
+                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, status)) return false;
                     tc_fence_after();
                     issue_pv(s, 1, vdesc(it), 1);
                     ++pc[s];
@@ -708,11 +767,11 @@ __global__ void __launch_bounds__(kBound, 1)
                 };
                 if (pair) {
                     // first tile's S of both slots
-                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status) && key_tile(0))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, status) && key_tile(0))) break;
                     tc_fence_after();
                     if (lo0 <= 0 && hi0 >= 0) issue_s(0, dq, kdesc(0));
                     if (n == 1) tc_commit_if(el, &mt.q_empty[0]);
-                    if (!(ok = mbar_wait_warp(&mt.q_full[1], nq[1] & 1, abort, p.status))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[1], nq[1] & 1, abort, status))) break;
                     tc_fence_after();
                     if (lo1 <= 0 && hi1 >= 0) issue_s(1, dq + kTileU, kdesc(0));
                     if (n == 1) tc_commit_if(el, &mt.q_empty[1]);
@@ -745,7 +804,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     ++nq[0];
                     ++nq[1];
                 } else {
-                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, p.status))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, status))) break;
                     ++nq[0];
                     // S of tile it into slot it & 1
                     auto s_tile = [&](int it) -> bool {
@@ -769,7 +828,7 @@ __global__ void __launch_bounds__(kBound, 1)
             }
             // every product issued must be complete before tensor memory is freed
             tc_commit_if(el, &mt.mma_done);
-            if (lane == 0) mbar_wait_drain(&mt.mma_done, 0, p.status);
+            if (lane == 0) mbar_wait_drain(&mt.mma_done, 0, status);
         }
         __syncwarp();
     } else if (warp == kClearWarp) {
@@ -780,7 +839,7 @@ __global__ void __launch_bounds__(kBound, 1)
         bool ok = true;
         for (int i = 0; ok; ++i) {
             const int r = i % kSegRing;
-            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status)) break;
+            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status)) break;
             const Segment sg = mt.seg[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&mt.g_empty[r]);
@@ -790,7 +849,7 @@ __global__ void __launch_bounds__(kBound, 1)
                 int r0, r1;
                 if (!unseen_rows(sg, p.window, it, r0, r1)) continue;
                 const uint32_t sv = (gk + it) % kNumV;
-                if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (ne >> sv) & 1, abort, p.status))) break;
+                if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (ne >> sv) & 1, abort, status))) break;
                 ne ^= 1u << sv;
                 uint8_t *vs = smem + C::kV0 + sv * C::kTile;
                 constexpr int kCh = D / 8;
@@ -818,7 +877,7 @@ __global__ void __launch_bounds__(kBound, 1)
         uint32_t gk = 0;               // key tiles of earlier segments
         for (int i = 0;; ++i) {
             const int r = i % kSegRing;
-            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, p.status)) break;
+            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status)) break;
             const Segment sg = mt.seg[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&mt.g_empty[r]);
@@ -836,7 +895,7 @@ __global__ void __launch_bounds__(kBound, 1)
             float m_ref = -INFINITY, l = 0.f;
             bool ok = true, bad = false;
             for (int it = it0; it <= it1; it += step) {
-                if (!(ok = mbar_wait_warp(&mt.s_full[s], cnt & 1, abort, p.status))) break;
+                if (!(ok = mbar_wait_warp(&mt.s_full[s], cnt & 1, abort, status))) break;
                 ++cnt;
                 if (idle) {
                     mbar_arrive(&mt.p_half[s]);
@@ -933,7 +992,7 @@ __global__ void __launch_bounds__(kBound, 1)
             gk += sg.nkt;
             if (!sg.pair && s == 1) {
                 // slot 0 finishes the shared rows
-                if (shared > 0 && !mbar_wait_warp(&mt.ml_free, (shared - 1) & 1, abort, p.status)) break;
+                if (shared > 0 && !mbar_wait_warp(&mt.ml_free, (shared - 1) & 1, abort, status)) break;
                 mt.ml[row] = make_float2(m_ref, l);
                 mbar_arrive(&mt.ml_full);
                 ++shared;
@@ -942,11 +1001,11 @@ __global__ void __launch_bounds__(kBound, 1)
             // weights of the two accumulators (a slot with its own row tile: 1 and 0)
             float w0 = 1.f, w1 = 0.f, m = m_ref;
             bool two = false;
-            if (n0 + n1 > 0 && !mbar_wait_warp(&mt.o_full[s], oc++ & 1, abort, p.status)) break;
+            if (n0 + n1 > 0 && !mbar_wait_warp(&mt.o_full[s], oc++ & 1, abort, status)) break;
             if (!sg.pair) {
                 two = n1 > 0;
-                if (two && !mbar_wait_warp(&mt.ox_full, ox++ & 1, abort, p.status)) break;
-                if (!mbar_wait_warp(&mt.ml_full, shared & 1, abort, p.status)) break;
+                if (two && !mbar_wait_warp(&mt.ox_full, ox++ & 1, abort, status)) break;
+                if (!mbar_wait_warp(&mt.ml_full, shared & 1, abort, status)) break;
                 ++shared;
                 const float2 o = mt.ml[row];
                 mbar_arrive(&mt.ml_free);
@@ -1064,6 +1123,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
     const int g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ChunkHead hd = p.heads[blockIdx.x];
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        // the call's status word, from the CTAs' (and the plan's)
+        __shared__ uint32_t all;
+        if (threadIdx.x == 0) all = p.direct ? 0u : p.plan->flags;
+        __syncthreads();
+        uint32_t f = 0;
+        for (int i = threadIdx.x; i < (int)gridDim.x; i += kMergeWarps * 32) f |= p.heads[i].flags;
+        if (f) atomicOr(&all, f);
+        __syncthreads();
+        if (threadIdx.x == 0) *p.status = all;
+    }
     if (hd.n_parts == 0) return;
     const float c2 = p.scale_log2;
     // rows of the unit, slot-major: the blocks of a unit stride over them
@@ -1150,7 +1220,7 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
         return cudaErrorInvalidValue;
     static SmemLimit limit;
     if (cudaError_t e = limit.ensure((const void *)chunk_attn_kernel<D>, Cfg<D>::kSmem); e != cudaSuccess) return e;
-    {
+    if (!p.direct) {
         ProfScope ps("chunk_plan", stream);
         chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, D);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
@@ -1165,7 +1235,7 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
     cfg.dynamicSmemBytes = Cfg<D>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.direct ? 0 : 1;
     {
         ProfScope ps("chunk_attn", stream);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;

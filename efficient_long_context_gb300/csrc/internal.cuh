@@ -341,13 +341,15 @@ struct ChunkUnit {
 };
 struct ChunkPlan {
     int units;
-    int pad;
+    uint32_t flags;   // status bits of the plan's checks
     long long tiles;  // key tiles of all units (of one kv head)
 };
 // The unit that a CTA begins but does not finish: its output is the merge of
 // n_parts CTAs' partials (0: none).
 struct ChunkHead {
     int n_parts, tok0, cnt, kv;
+    uint32_t flags;  // the CTA's status bits
+    uint32_t pad[3];
 };
 struct ChunkParams {
     const __nv_bfloat16 *q;          // [n, Hq, d]
@@ -360,6 +362,7 @@ struct ChunkParams {
     int box;                         // tokens of a K/V copy box, a divisor of page_size (0: rows are gathered)
     int lanes, per_lane;             // CTAs: lanes x per_lane; a lane serves Hkv / lanes kv heads
     int rows_cap, slots_cap;         // rows and slots of a partial
+    bool direct;                     // at most 32 units: each CTA lists them itself, there is no plan
     float scale, scale_log2;
     __nv_bfloat16 *o;                // [n, Hq, d]
     bool o_aligned32;                // o is 32-byte aligned
