@@ -668,10 +668,12 @@ def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=N
     dev, here = _here()
     shape = x.shape
     n, H, d = shape
+    xa, xs = _rows("x", x, dev, x.dtype, shape)
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    xa, xs = _rows("x", x, dev, x.dtype, shape)
-    ya, ys = _rows("out", out, dev, x.dtype, shape)
+        ya, ys = out.data_ptr(), H * d
+    else:
+        ya, ys = _rows("out", out, dev, x.dtype, shape)
     st, rot = _steps(steps, dev)
     rc = lib.orthros_rotate(xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)),
                             _block("beta", beta, dev, torch.float32, (H, d)), st, rot, _rope_layout(layout), amplitude, n, H,
@@ -697,16 +699,18 @@ def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude
     shape, dtype = dy.shape, dy.dtype
     n, H, d = shape
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=dy.device),
-               torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None,
-               torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None)
-    dx, da, db = out
+        dx = torch.empty(shape, dtype=dtype, device=dy.device)
+        da = torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None
+        db = torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None
+        oa, os_ = dx.data_ptr(), H * d
+    else:
+        dx, da, db = out
+        oa, os_ = _rows("dx", dx, dev, dtype, shape)
     if workspace is None and da is not None:
         workspace = torch.empty(max(orthros_rotate_backward_workspace_size(n, H, d, dtype), 256),
                                 dtype=torch.uint8, device=dy.device)
     ga, gs = _rows("dy", dy, dev, dtype, shape)
     xa, xs = _rows("x", x, dev, dtype, shape)
-    oa, os_ = _rows("dx", dx, dev, dtype, shape)
     st, rot = _steps(steps, dev)
     rc = lib.orthros_rotate_backward(
         ga, gs, xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)), st, rot,

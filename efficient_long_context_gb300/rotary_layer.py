@@ -1,0 +1,99 @@
+"""One Orthros attention layer with rotary positions, made of the library's calls.
+
+The pages leave the positional encoding aside; a model with rotary positions
+turns queries and keys between the stream affines and the attention (Alg. 1
+lines 5 and 7). `RotaryLayer` shows where those calls stand:
+
+serving   step(): projection -> rotated paged append -> attention of the new
+          tokens over the cache, base stream (window) and output stream (all
+          keys). One token per sequence, chunks of prompts, or both mixed; no
+          length is read on the host, so a step can be captured in a CUDA graph.
+training  forward() / backward(): rotation of affined queries and of keys ->
+          orthros_prefill with identity affines, and the gradients back through
+          both, those of the four affines included.
+"""
+from __future__ import annotations
+
+import dataclasses
+
+import torch
+
+from . import _binding as ops
+
+
+@dataclasses.dataclass
+class RotaryLayer:
+    """Weights and shape of the layer. `affines` are alpha_base, beta_base, alpha_out,
+    beta_out [Hq, d]; `freq` [rot_dim/2] the rotary frequencies (orthros_rotary_frequencies)."""
+
+    w_qkv: torch.Tensor  # [(Hq + 2 Hkv) d, d_model] bf16
+    affines: list
+    freq: torch.Tensor
+    Hq: int
+    Hkv: int
+    d: int
+    window: int
+    layout: str = "half"
+    amplitude: float = 1.0
+
+    def __post_init__(self):
+        dev = self.w_qkv.device
+        self.steps = ops.orthros_rotary_steps(self.freq).to(dev)
+        self.identity = (torch.ones(self.Hq, self.d, device=dev), torch.zeros(self.Hq, self.d, device=dev))
+
+    def _rope(self):
+        return dict(layout=self.layout, amplitude=self.amplitude)
+
+    # ---- serving -------------------------------------------------------------
+    def step(self, x, n_new, k_cache, v_cache, block_table, token_seq, token_pos, new_indptr, kv_lens, out_indptr,
+             out_positions, max_new):
+        """One serving step.
+
+        x [n_new + n_out, d_model]: the new tokens of the batch (rows new_indptr[b] ..
+        new_indptr[b+1] belong to sequence b), then at most one output-stream token per
+        sequence, at its last position (out_indptr, out_positions). kv_lens counts the
+        cached tokens with the new ones. Returns (o_base [n_new, Hq, d], o_out [n_out, Hq, d]).
+        """
+        q, q_out, k, v = ops.orthros_qkv_project(x, n_new, self.w_qkv, self.Hq, self.Hkv, self.d, *self.affines,
+                                                 kv_out=True)
+        q, q_out = ops.orthros_rotate_append(q, k, v, k_cache, v_cache, block_table, token_seq, token_pos, self.steps,
+                                             q_out=q_out, out_positions=out_positions, **self._rope())
+        o_base, _ = ops.orthros_chunk_attention(q, new_indptr, kv_lens, k_cache, v_cache, block_table, self.window,
+                                                max_new=max_new)
+        o_out, _ = ops.orthros_chunk_attention(q_out, out_indptr, kv_lens, k_cache, v_cache, block_table, 2 ** 31 - 1,
+                                               max_new=1)
+        return o_base, o_out
+
+    # ---- training ------------------------------------------------------------
+    def forward(self, q, k, v, out_indptr, out_positions):
+        """q [B, T, Hq, d] (before the affines), k, v [B, T, Hkv, d]; output rows as in
+        orthros_prefill (their raw queries are q at their positions). Returns
+        ((o_base, o_out), saved for backward)."""
+        B, T = q.shape[:2]
+        ab, bb, ao, bo = self.affines
+        pos = torch.arange(T, dtype=torch.int32, device=q.device).repeat(B)
+        counts = torch.as_tensor(out_indptr, dtype=torch.int64).diff()
+        rows = torch.repeat_interleave(torch.arange(B), counts).to(q.device) * T + out_positions
+        qf, kf = q.flatten(0, 1), k.flatten(0, 1)
+        q_sel = qf[rows]
+        qr = ops.orthros_rotate(qf, pos, self.steps, alpha=ab, beta=bb, **self._rope()).view_as(q)
+        kr = ops.orthros_rotate(kf, pos, self.steps, **self._rope()).view_as(k)
+        qo = ops.orthros_rotate(q_sel, out_positions, self.steps, alpha=ao, beta=bo, **self._rope())
+        out = ops.orthros_prefill(qr, kr, v, *self.identity, *self.identity, out_indptr, out_positions, self.window,
+                                  q_out=qo)
+        return (out[0], out[2]), (qf, q_sel, rows, pos, qr, kr, v, qo, out_indptr, out_positions, out)
+
+    def backward(self, saved, do_base, do_out):
+        """Gradients of q, k, v and of the four affines, in a dict."""
+        qf, q_sel, rows, pos, qr, kr, v, qo, out_indptr, out_positions, out = saved
+        ab, _, ao, _ = self.affines
+        g = ops.orthros_prefill_backward(qr, kr, v, *self.identity, *self.identity, out_indptr, out_positions,
+                                         self.window, None, *out, do_base, do_out, q_out=qo)
+        dq, da, db = ops.orthros_rotate_backward(g["dq"].flatten(0, 1), qf, pos, self.steps, alpha=ab, **self._rope())
+        dk, _, _ = ops.orthros_rotate_backward(g["dk"].flatten(0, 1), None, pos, self.steps, affine_grads=False,
+                                               **self._rope())
+        dq_sel, da_out, db_out = ops.orthros_rotate_backward(g["dq_out"], q_sel, out_positions, self.steps, alpha=ao,
+                                                             **self._rope())
+        dq = dq.float().index_add_(0, rows, dq_sel.float()).to(qf.dtype)
+        return {"dq": dq.view_as(qr), "dk": dk.view_as(kr), "dv": g["dv"], "d_alpha_base": da, "d_beta_base": db,
+                "d_alpha_out": da_out, "d_beta_out": db_out}

@@ -1,0 +1,114 @@
+"""The rotary layer (projection, rotated append, attention over the cache; rotation around
+prefill and its backward): serving a prompt in chunks and then token by token agrees with
+the training forward over the whole sequence, and the gradients with autograd in fp64.
+
+Outputs: both paths read the same bf16 queries, keys and values and each lies within the
+attention contract (2e-2 absolute for N(0, 1) inputs) of the exact value. Gradients: the
+prefill backward's own bound (5e-2 of rms(ref) + |ref| + floor), whose terms the orthogonal
+rotation does not enlarge; the floor is rms(dO), times sqrt(rows summed) for the affines.
+"""
+import numpy as np
+import pytest
+import torch
+
+import efficient_long_context_gb300 as ola
+from efficient_long_context_gb300.rotary_layer import RotaryLayer
+
+pytestmark = pytest.mark.gpu
+
+
+def make_layer(Hq, Hkv, d, window, layout, seed, d_model=256, rot=None):
+    g = torch.Generator().manual_seed(seed)
+    w = (torch.randn((Hq + 2 * Hkv) * d, d_model, generator=g) / d_model ** 0.5).bfloat16().cuda()
+    aff = []
+    for _ in range(2):
+        aff += [(1 + 0.1 * torch.randn(Hq, d, generator=g)).cuda(), (0.1 * torch.randn(Hq, d, generator=g)).cuda()]
+    freq, amp = ola.orthros_rotary_frequencies(rot or d, 10000.0, "bands_tempered", factor=4.0, original_length=4096.0)
+    return RotaryLayer(w, aff, freq, Hq, Hkv, d, window, layout, amp), g
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,layout,page", [(8, 2, 128, 100, "half", 16), (32, 8, 128, 300, "interleaved", 64),
+                                                         (4, 4, 64, 64, "half", 24)])
+def test_serving_in_chunks_and_steps_matches_one_prefill(Hq, Hkv, d, window, layout, page):
+    layer, g = make_layer(Hq, Hkv, d, window, layout, seed=Hq)
+    B, T = 3, 330
+    x = torch.randn(B, T, 256, generator=g).bfloat16().cuda()
+    mp = (T + page - 1) // page
+    bt = torch.randperm(B * mp, generator=g).to(torch.int32).view(B, mp).cuda()
+    kc = torch.full((B * mp, page, Hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vc = torch.full_like(kc, float("nan"))
+    # sequences advance by chunks of their own, then by single tokens; sequence 2 sits one step out
+    plan = [(200, 70, 130), (100, 129, 0), (1, 1, 1), (1, 1, 64), (1, 1, 1)]
+    at = [0] * B
+    base = torch.zeros(B, T, Hq, d, device="cuda")
+    outs = []
+    for new in plan:
+        seq = [b for b in range(B) for _ in range(new[b])]
+        pos = [at[b] + i for b in range(B) for i in range(new[b])]
+        at = [a + n for a, n in zip(at, new)]
+        live = [b for b in range(B) if new[b]]
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+        rows = torch.cat([x[seq, pos], x[live, [at[b] - 1 for b in live]]])
+        ob, oo = layer.step(rows, len(seq), kc, vc, bt, i32(seq), i32(pos), i32(np.concatenate([[0], np.cumsum(new)])),
+                            i32(at), i32(np.concatenate([[0], np.cumsum([int(n > 0) for n in new])])),
+                            i32([at[b] - 1 for b in live]), max(new))
+        base[seq, pos] = ob.float()
+        outs += [(b, at[b] - 1, oo[i].float()) for i, b in enumerate(live)]
+    # the same tokens in one training forward: raw projections, output rows at the served positions
+    one = [torch.ones(Hq, d, device="cuda"), torch.zeros(Hq, d, device="cuda")] * 2
+    q, _, k, v = ola.orthros_qkv_project(x.flatten(0, 1), B * T, layer.w_qkv, Hq, Hkv, d, *one, kv_out=True)
+    outs.sort(key=lambda o: (o[0], o[1]))
+    indptr = np.concatenate([[0], np.cumsum([sum(o[0] == b for o in outs) for b in range(B)])]).astype(np.int32)
+    (ob, oo), _ = layer.forward(q.view(B, T, Hq, d), k.view(B, T, Hkv, d), v.view(B, T, Hkv, d), indptr,
+                                torch.tensor([o[1] for o in outs], dtype=torch.int32, device="cuda"))
+    for b in range(B):
+        # the raw projection is rounded before its affine here and after it in step(): one bf16
+        # rounding of q apart (2^-8 per logit of a few units), besides the two contracts
+        assert float((base[b, :at[b]] - ob[b, :at[b]].float()).abs().max()) <= 6e-2
+    assert float((torch.stack([o[2] for o in outs]) - oo.float()).abs().max()) <= 6e-2
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_training_gradients_against_autograd(layout):
+    Hq, Hkv, d, T, B, window, rot = 4, 2, 64, 90, 2, 30, 48
+    layer, g = make_layer(Hq, Hkv, d, window, layout, seed=3, rot=rot)
+    q, k, v = (torch.randn(B, T, h, d, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv))
+    indptr = np.array([0, 3, 5], dtype=np.int32)
+    opos = torch.tensor([10, 89, 10, 0, 50], dtype=torch.int32, device="cuda")
+    (ob, oo), saved = layer.forward(q, k, v, indptr, opos)
+    db, do = torch.randn(ob.shape, generator=g).bfloat16().cuda(), torch.randn(oo.shape, generator=g).bfloat16().cuda()
+    got = layer.backward(saved, db, do)
+
+    leaves = {n: t.double().detach().clone().requires_grad_() for n, t in
+              zip(("q", "k", "v", "alpha_base", "beta_base", "alpha_out", "beta_out"), (q, k, v, *layer.affines))}
+    th = torch.arange(T, device="cuda").double()[:, None] * layer.freq.cuda()
+    ia, ib = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+
+    def rot_(u, c, s):  # u [..., n, H, d], c, s [n, pairs]
+        y = u.clone()
+        y[..., ia] = layer.amplitude * (u[..., ia] * c[:, None] - u[..., ib] * s[:, None])
+        y[..., ib] = layer.amplitude * (u[..., ia] * s[:, None] + u[..., ib] * c[:, None])
+        return y
+
+    c, s = torch.cos(th), torch.sin(th)
+    kr = rot_(leaves["k"], c, s).repeat_interleave(Hq // Hkv, 2)
+    vv = leaves["v"].repeat_interleave(Hq // Hkv, 2)
+    t = torch.arange(T, device="cuda")
+    band = (t[None, :] <= t[:, None]) & (t[None, :] > t[:, None] - window)
+    qr = rot_(leaves["q"] * leaves["alpha_base"] + leaves["beta_base"], c, s)
+    z = torch.einsum("bthd,bjhd->bhtj", qr, kr) * d ** -0.5
+    o = torch.einsum("bhtj,bjhd->bthd", torch.softmax(z.masked_fill(~band, float("-inf")), -1), vv)
+    seq = torch.tensor([0, 0, 0, 1, 1], device="cuda")
+    p = opos.long()
+    qo = rot_((leaves["q"][seq, p] * leaves["alpha_out"] + leaves["beta_out"]), c[p], s[p])
+    z = torch.einsum("nhd,njhd->nhj", qo, kr[seq]) * d ** -0.5
+    z = z.masked_fill(t[None, None, :] > p[:, None, None], float("-inf"))
+    oo64 = torch.einsum("nhj,njhd->nhd", torch.softmax(z, -1), vv[seq])
+    assert float((ob.double() - o.detach()).abs().max()) <= 3e-2 and float((oo.double() - oo64.detach()).abs().max()) <= 3e-2
+    ((o * db.double()).sum() + (oo64 * do.double()).sum()).backward()
+    rms = float(db.float().pow(2).mean().sqrt())
+    for n, leaf in leaves.items():
+        ref, a = leaf.grad, got["d" + n if n in "qkv" else "d_" + n].double()
+        floor = rms if n in "qkv" else rms * (B * T if n.endswith("base") else 5) ** 0.5
+        err = float(((a - ref).abs() / (ref.pow(2).mean().sqrt() + ref.abs() + floor)).max())
+        assert err <= 5e-2, (n, err)
