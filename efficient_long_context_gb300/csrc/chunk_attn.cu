@@ -321,7 +321,11 @@ constexpr int kSnap = 3;
 struct Shares {
     long long total;
     int eff, snap;
-    __device__ long long border(int j) const { return total * j / eff; }  // before it moves
+    __device__ long long border(int j) const {  // before it moves
+        // (a 64-bit division takes the copy warp, which starts with two, half a microsecond)
+        if (total * eff <= 0xffffffffLL) return (uint32_t)total * (uint32_t)j / (uint32_t)eff;
+        return total * j / eff;
+    }
     // border x, which falls into the unit [u0, u0 + n), where it ends up
     __device__ long long moved(long long x, long long u0, int n) const {
         return x - u0 <= snap ? u0 : u0 + n - x <= snap ? u0 + n : x;
@@ -330,9 +334,9 @@ struct Shares {
 __device__ __forceinline__ Shares shares_of(const ChunkParams &p, const ChunkPlan &pl) {
     Shares s;
     s.total = (long long)(p.Hkv / p.lanes) * pl.tiles;
-    const long long fit = s.total / kMinTiles;
-    s.eff = (int)max(1LL, min((long long)p.per_lane, fit));
-    s.snap = (int)min((long long)kSnap, s.total / s.eff / 4);
+    s.eff = (int)max(1LL, min((long long)p.per_lane, s.total / kMinTiles));
+    s.snap = 0;  // the largest with 4 snap eff <= total, up to kSnap
+    while (s.snap < kSnap && 4LL * (s.snap + 1) * s.eff <= s.total) ++s.snap;
     return s;
 }
 
@@ -478,6 +482,8 @@ __global__ void __launch_bounds__(kBound, 1)
         };
         const int ln = blockIdx.x % p.lanes, j = blockIdx.x / p.lanes;
         ChunkHead head{};
+        long long head_u0 = 0;  // first key tile and key tiles of the unit it names
+        int head_n = 0;
         uint32_t gk = 0, gv = 0;  // key and value copies issued
         uint32_t nq[2] = {0, 0};  // query tiles issued per slot
         int ring = 0;
@@ -499,7 +505,8 @@ __global__ void __launch_bounds__(kBound, 1)
             if (j < sh.eff) {
                 // both borders of the share, moved; the unit the first one ends up in
                 long long x = sh.border(j), x1 = sh.border(j + 1);
-                int kvo = (int)(x / pl.tiles);
+                int kvo = 0;  // which of the lane's kv heads (few: counted, not divided)
+                while (x >= (kvo + 1) * pl.tiles) ++kvo;
                 int u = find(x - kvo * pl.tiles);
                 auto next_unit = [&]() {  // (a lane without a unit is passed over)
                     do {
@@ -510,7 +517,8 @@ __global__ void __launch_bounds__(kBound, 1)
                     } while (p.direct && __shfl_sync(0xffffffffu, own.n_kt, u) == 0);
                 };
                 if (x1 < sh.total) {
-                    const long long base = x1 / pl.tiles * pl.tiles;
+                    long long base = kvo * pl.tiles;
+                    while (x1 >= base + pl.tiles) base += pl.tiles;
                     const ChunkUnit e = get_unit(find(x1 - base));
                     x1 = sh.moved(x1, base + e.start, e.n_kt);
                 }
@@ -537,10 +545,8 @@ __global__ void __launch_bounds__(kBound, 1)
                     const bool starts = a == 0, ends = a + n_tiles == un.n_kt;
                     sg.partial = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
                     if (starts && !ends) {
-                        // the CTAs whose share begins inside the unit hold the other parts
-                        int k = j + 1;
-                        while (k < sh.eff && sh.moved(sh.border(k), x, un.n_kt) < x + un.n_kt) ++k;
-                        head.n_parts = k - j;
+                        head_u0 = x;
+                        head_n = un.n_kt;
                         head.tok0 = un.tok0;
                         head.cnt = un.cnt;
                         head.kv = sg.kv;
@@ -677,6 +683,13 @@ __global__ void __launch_bounds__(kBound, 1)
             Segment sg{};
             sg.end = 1;
             publish(sg);
+        }
+        if (head_n > 0) {
+            // the CTAs whose share begins inside the unit hold its other parts
+            const Shares sh = shares_of(p, pl);
+            int k = j + 1;
+            while (k < sh.eff && sh.moved(sh.border(k), head_u0, head_n) < head_u0 + head_n) ++k;
+            head.n_parts = k - j;
         }
         if (lane == 0) {
             ChunkHead &to = p.heads[blockIdx.x];
@@ -1022,12 +1035,21 @@ __global__ void __launch_bounds__(kBound, 1)
                 const long long tok = sg.tok0 + c0 + row / g;
                 const int h = sg.kv * g + row % g;
                 const uint32_t t_a = t_o + (sg.pair ? s * 128 : 0);
-                if (sg.partial < 0) {
+                const bool fin = sg.partial < 0;
+                const long long out = tok * p.Hq + h;  // row of o, or of the partials
+                const long long at = ((long long)sg.partial * p.slots_cap + (sg.pair ? s : 0)) * p.rows_cap + row;
+                if (fin) {
                     const float inv = l > 0.f ? 1.f / l : l;  // a NaN sum stays
                     w0 *= inv;
                     w1 *= inv;
-                    __nv_bfloat16 *dst = p.o + (tok * p.Hq + h) * D;
-#pragma unroll
+                    if (mine && p.lse) p.lse[out] = m * p.scale + logf(l);
+                } else if (mine) {
+                    p.part_ml[at] = make_float2(m, l);
+                }
+                // 32 channels a turn, not unrolled: this code runs once per segment, mostly from a cold
+                // instruction cache
+                if (n0 + n1 > 0)
+#pragma unroll 1
                     for (int j = 0; j < D / 32; ++j) {
                         uint32_t o[32];
                         tmem_ld32(t_a + 32 * j, o);
@@ -1043,56 +1065,33 @@ __global__ void __launch_bounds__(kBound, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
                         }
-                        if (mine) {
+                        if (!mine) continue;
+                        if (fin) {
+                            __nv_bfloat16 *dst = p.o + out * D + 32 * j;
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 uint32_t w[8];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[16 * e + 2 * i], f[16 * e + 2 * i + 1]);
                                 if (p.o_aligned32) {
-                                    st_global_32b(dst + 32 * j + 16 * e, w);
+                                    st_global_32b(dst + 16 * e, w);
                                 } else {
-                                    uint4 *to = reinterpret_cast<uint4 *>(dst + 32 * j + 16 * e);
+                                    uint4 *to = reinterpret_cast<uint4 *>(dst + 16 * e);
                                     to[0] = make_uint4(w[0], w[1], w[2], w[3]);
                                     to[1] = make_uint4(w[4], w[5], w[6], w[7]);
                                 }
                             }
-                        }
-                    }
-                    if (mine && p.lse) p.lse[tok * p.Hq + h] = m * p.scale + logf(l);
-                } else {
-                    const long long at = ((long long)sg.partial * p.slots_cap + (sg.pair ? s : 0)) * p.rows_cap + row;
-                    if (mine) p.part_ml[at] = make_float2(m, l);
-                    float *dst = p.part_o + at * D;
-                    if (n0 + n1 > 0) {
+                        } else {
+                            float *dst = p.part_o + at * D + 32 * j;
 #pragma unroll
-                        for (int j = 0; j < D / 32; ++j) {
-                            uint32_t o[32];
-                            tmem_ld32(t_a + 32 * j, o);
-                            tmem_ld_wait();
-                            reg_fence(o);
-                            float f[32];
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
-                            if (two) {
-                                tmem_ld32(t_a + 128 + 32 * j, o);
-                                tmem_ld_wait();
-                                reg_fence(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
-                            }
-                            if (mine) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    uint32_t w[8];
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 * e + i]);
-                                    st_global_32b(dst + 32 * j + 8 * e, w);
-                                }
+                                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 * e + i]);
+                                st_global_32b(dst + 8 * e, w);
                             }
                         }
                     }
-                }
                 tc_fence_before();
             }
             if (n0) mbar_arrive(&mt.o_free[0]);
