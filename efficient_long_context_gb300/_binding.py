@@ -572,13 +572,17 @@ def _here():
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _elsewhere(t):
+    return OrthrosError(1, f"tensor on {t.device}: every tensor argument must be on the current CUDA device")
+
+
 def _addr(t, dev):
     """_ptr for a known current device: the address as an integer (None for no or no elements)."""
     if t is None:
         return None
     if t.get_device() != dev:
-        raise OrthrosError(1, f"tensor on {t.device}: every tensor argument must be on the current CUDA device")
-    return t.data_ptr() or None
+        raise _elsewhere(t)
+    return t.data_ptr()
 
 
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -601,7 +605,9 @@ def _rows(name, t, dev, dtype, shape):
     st = t.stride()
     if (st[2] != 1 or (H > 1 and st[1] != d)) and t.numel():
         raise OrthrosError(1, f"{name}: the heads of a token must be contiguous")
-    return _addr(t, dev), st[0] if n > 1 else H * d
+    if t.get_device() != dev:
+        raise _elsewhere(t)
+    return t.data_ptr(), st[0] if n > 1 else H * d
 
 
 def _index(name, t, dev, n):
@@ -610,7 +616,9 @@ def _index(name, t, dev, n):
         return None
     if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
         raise OrthrosError(1, f"{name} must be a contiguous int32 tensor of {n} entries")
-    return _addr(t, dev)
+    if t.get_device() != dev:
+        raise _elsewhere(t)
+    return t.data_ptr()
 
 
 def _block(name, t, dev, dtype, shape):
@@ -619,7 +627,9 @@ def _block(name, t, dev, dtype, shape):
         return None
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise OrthrosError(1, f"{name} must be a contiguous {dtype} {list(shape)} tensor")
-    return _addr(t, dev)
+    if t.get_device() != dev:
+        raise _elsewhere(t)
+    return t.data_ptr()
 
 
 def _steps(t, dev):
@@ -739,9 +749,12 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     num_pages, page_size = k_cache.shape[:2]
     B, max_pages = block_table.shape
     if out is None:
-        out = (torch.empty((n, Hq, d), dtype=dtype, device=k_new.device) if q is not None else None,
-               torch.empty((n_out, Hq, d), dtype=dtype, device=k_new.device) if q_out is not None else None)
-    q_rot, q_out_rot = out
+        q_rot = torch.empty((n, Hq, d), dtype=dtype, device=k_new.device) if q is not None else None
+        q_out_rot = torch.empty((n_out, Hq, d), dtype=dtype, device=k_new.device) if q_out is not None else None
+    else:
+        q_rot, q_out_rot = out
+        _block("q_rot", q_rot, dev, dtype, (n, Hq, d))
+        _block("q_out_rot", q_out_rot, dev, dtype, (n_out, Hq, d))
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=k_new.device)
     qa, qs = _rows("q", q, dev, dtype, (n, Hq, d))
@@ -756,7 +769,7 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
         qa, qs, qoa, qos, ka, ks, va, vs, *aff, st, rot, _rope_layout(layout), amplitude,
         _index("token_seq", token_seq, dev, n), _index("token_pos", token_pos, dev, n),
         _index("out_positions", out_positions, dev, n_out), n, n_out, Hq, Hkv, d, _dtype(k_new),
-        _block("q_rot", q_rot, dev, dtype, (n, Hq, d)), _block("q_out_rot", q_out_rot, dev, dtype, (n_out, Hq, d)),
+        _addr(q_rot, dev), _addr(q_out_rot, dev),
         _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
         _index("block_table", block_table, dev, B * max_pages), B, max_pages, page_size, num_pages, _addr(workspace, dev),
         workspace.numel(), here if stream is None else _stream(stream))
@@ -787,9 +800,12 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     if max_new is None:
         max_new = n
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=q.device),
-               torch.empty((n, Hq), dtype=torch.float32, device=q.device))
-    o, lse = out
+        o = torch.empty(shape, dtype=dtype, device=q.device)
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        oa, la = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        oa, la = _block("o", o, dev, dtype, shape), _block("lse", lse, dev, torch.float32, (n, Hq))
     if workspace is None:
         ws = orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype)
         workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=q.device)
@@ -799,7 +815,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
         _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
         _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq, Hkv, d, window,
         d ** -0.5 if scale is None else scale, _dtype(q), max_pages, page_size, num_pages,
-        _block("o", o, dev, dtype, shape), _block("lse", lse, dev, torch.float32, (n, Hq)), _addr(workspace, dev),
+        oa, la, _addr(workspace, dev),
         workspace.numel(), here if stream is None else _stream(stream))
     _raise_if(rc, lib)
     return o, lse
