@@ -306,7 +306,6 @@ struct RotateParams {
     void *k_cache, *v_cache;
     int Hkv, B, max_pages, page_size, num_pages;
     uint32_t *status;
-    bool status_here;  // one block writes the whole status word (short calls), else a launch resets it
     int blocks;        // set by the launcher: blocks along the new tokens
 };
 struct RotateBwdParams {

@@ -143,7 +143,7 @@ __device__ __forceinline__ void load_affine(const float *p, int ca, int cb, floa
 // heads: entry (token, j / 2, item) holds angles j and j + 1 of the item, so the
 // lanes of a row read consecutive 16-byte words.
 constexpr int kTabTokens = 16;  // at most
-constexpr int kRunTokens = 64;  // positions (and page slots) a block looks up at a time
+constexpr int kRunTokens = 128;  // positions (and page slots) a block looks up at a time
 // Tokens of a table (a divisor of kRunTokens): two batches' worth of loads of one
 // token a thread; more when tokens go side by side. A longer table delays its
 // first rows (16 and 32 tokens: 1 and 5 % at 32 heads).
@@ -186,40 +186,46 @@ template <typename T, int D> struct Table {
 //
 // The virtual heads of a token are its Hq query heads, then (append) its Hkv key
 // heads and Hkv value heads. Blocks from p.blocks on (along x) move the output
-// stream's rows.
+// stream's rows; an append's last one writes the status word.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 512;  // at most
 constexpr int kBatch = 4;
 
-// Token slot of new token i in the page pool; wrong: its status bit when it has none.
-__device__ __forceinline__ long long page_slot(const RotateParams &p, long long i, uint32_t &wrong) {
+// Token slot of new token i in the page pool, or -1 when it has none.
+__device__ __forceinline__ long long page_slot(const RotateParams &p, long long i) {
     const int b = p.token_seq[i], t = p.positions[i];
-    if (b < 0 || b >= p.B || t < 0 || t / p.page_size >= p.max_pages) {
-        wrong |= ORTHROS_DEV_BAD_POSITION;
-        return 0;
-    }
+    if (b < 0 || b >= p.B || t < 0 || t / p.page_size >= p.max_pages) return -1;
     const int pg = p.block_table[(long long)b * p.max_pages + t / p.page_size];
-    if (pg < 0 || pg >= p.num_pages) {
-        wrong |= ORTHROS_DEV_BAD_PAGE;
-        return 0;
-    }
+    if (pg < 0 || pg >= p.num_pages) return -1;
     return (long long)pg * p.page_size + t % p.page_size;
 }
 
-// The status word of an append: one block checks every new token and writes the
-// word, with no reset before it and no atomics.
+// The status word of an append, written by a block of its own that checks every new
+// token beside the moving ones: no reset launch before the kernel, no atomics.
 __device__ __forceinline__ void write_status(const RotateParams &p) {
+    constexpr int kBatchS = 8;  // tokens a thread looks up at once
     uint32_t wrong = 0;
-    for (long long i = threadIdx.x; i < p.n; i += blockDim.x) page_slot(p, i, wrong);
+    for (long long i0 = threadIdx.x; i0 < p.n; i0 += (long long)kBatchS * blockDim.x) {
+        int b[kBatchS], t[kBatchS];
+#pragma unroll
+        for (int u = 0; u < kBatchS; ++u) {
+            const long long i = i0 + (long long)u * blockDim.x;
+            b[u] = i < p.n ? p.token_seq[i] : 0;
+            t[u] = i < p.n ? p.positions[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatchS; ++u) {
+            if (i0 + (long long)u * blockDim.x >= p.n) break;
+            if (b[u] < 0 || b[u] >= p.B || t[u] < 0 || t[u] / p.page_size >= p.max_pages) {
+                wrong |= ORTHROS_DEV_BAD_POSITION;
+            } else {
+                const int pg = p.block_table[(long long)b[u] * p.max_pages + t[u] / p.page_size];
+                if (pg < 0 || pg >= p.num_pages) wrong |= ORTHROS_DEV_BAD_PAGE;
+            }
+        }
+    }
     const int pos = __syncthreads_or(wrong & ORTHROS_DEV_BAD_POSITION), pg = __syncthreads_or(wrong & ORTHROS_DEV_BAD_PAGE);
     if (threadIdx.x == 0) *p.status = (pos ? ORTHROS_DEV_BAD_POSITION : 0u) | (pg ? ORTHROS_DEV_BAD_PAGE : 0u);
-}
-
-// The reset of a long append's status word, which the moving kernel starts beside;
-// only a block that found something wrong waits for it before it adds its bit.
-__global__ void rotate_status_reset_kernel(uint32_t *status) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) *status = 0;
 }
 
 template <typename T, int D, bool kAppend>
@@ -228,6 +234,10 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
     __shared__ Table<T, D> tab[2];
     __shared__ int pos[kRunTokens];
     __shared__ long long slot[kRunTokens];  // append: first element of the token's page slot, or -1
+    if (kAppend && blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0) write_status(p);
+        return;
+    }
     const int tid = threadIdx.x;
     const int hb = p.heads_per_block;
     const int lanes = blockDim.x / (hb * IPR);  // tokens handled side by side
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
     const int h = blockIdx.y * hb + (tid / IPR) % hb;
     const int item = tid % IPR;
     const bool out = kAppend && (int)blockIdx.x >= p.blocks;
-    const int bx = out ? blockIdx.x - p.blocks : blockIdx.x, nbx = out ? gridDim.x - p.blocks : p.blocks;
+    const int bx = out ? blockIdx.x - p.blocks : blockIdx.x, nbx = out ? gridDim.x - 1 - p.blocks : p.blocks;
     const long long n = out ? p.n_out : p.n;
     const int32_t *positions = out ? p.out_positions : p.positions;
     // what this thread's virtual head moves
@@ -266,7 +276,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
         load_affine<VEC>(alpha + hh * D, it.ca, it.cb, al[0], al[1]);
         load_affine<VEC>(beta + hh * D, it.ca, it.cb, be[0], be[1]);
     }
-    if (kAppend && p.status_here && blockIdx.x == 0 && blockIdx.y == 0) write_status(p);  // a short call's
     const long long n0 = n * bx / nbx, n1 = n * (bx + 1) / nbx;
     const int step = table_tokens(lanes);
     int buf = 0;
@@ -291,13 +300,8 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
             for (int k = tid; k < kRunTokens && base + k < n1; k += blockDim.x) {
                 pos[k] = positions[base + k];
                 if (kAppend && !out) {
-                    uint32_t wrong = 0;
-                    const long long at = page_slot(p, base + k, wrong);
-                    slot[k] = wrong ? -1 : at * p.Hkv * D;
-                    if (wrong && !p.status_here) {
-                        asm volatile("griddepcontrol.wait;" ::: "memory");
-                        set_status(p.status, wrong);
-                    }
+                    const long long at = page_slot(p, base + k);
+                    slot[k] = at < 0 ? -1 : at * p.Hkv * D;
                 }
             }
             __syncthreads();
@@ -335,8 +339,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
             }
         }
     }
-    // (append) the call is complete when the status word's reset is, too
-    if (kAppend) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -520,29 +522,19 @@ template <typename T, int D, bool kAppend> cudaError_t move_t(RotateParams p, in
     }
     p.heads_per_block = hb;
     const int lanes = threads / (hb * IPR);  // (the kernel's)
-    const long long rows = p.n > 0 ? p.n : p.n_out;
-    long long blocks = (long long)device_sm_count() * (per_sm / threads < 32 ? per_sm / threads : 32) / groups;
-    if (blocks > (rows + lanes - 1) / lanes) blocks = (rows + lanes - 1) / lanes;
-    if (blocks < 1) blocks = 1;
-    p.blocks = p.n > 0 ? (int)blocks : 0;
-    const long long out_blocks = (p.n_out + lanes - 1) / lanes;
-    const dim3 grid((unsigned)(p.blocks + (out_blocks < blocks ? out_blocks : blocks)), groups);
-    if (!kAppend || p.status_here) {
-        rotate_move_kernel<T, D, kAppend><<<grid, threads, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    rotate_status_reset_kernel<<<1, 32, 0, s>>>(p.status);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rotate_move_kernel<T, D, kAppend>, p);
+    // blocks that run at once (append: one of them, in each group's row, for the status
+    // word), shared between the new tokens and the output stream's rows by their
+    // number: a second wave of a few short blocks cost 3 us
+    const int fit = device_sm_count() * (per_sm / threads < 32 ? per_sm / threads : 32) / groups - (kAppend ? 1 : 0);
+    const long long most = (p.n + lanes - 1) / lanes, most_out = (p.n_out + lanes - 1) / lanes;
+    long long out = p.n_out == 0 ? 0 : fit * (long long)p.n_out / (p.n + p.n_out);
+    out = out > most_out ? most_out : out < 1 && p.n_out > 0 ? 1 : out;
+    long long blocks = fit - out;
+    blocks = blocks > most ? most : blocks < 1 && p.n > 0 ? 1 : blocks < 0 ? 0 : blocks;
+    p.blocks = (int)blocks;
+    const dim3 grid((unsigned)(blocks + out + (kAppend ? 1 : 0)), groups);
+    rotate_move_kernel<T, D, kAppend><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int D> cudaError_t rotate_t(const RotateParams &p, cudaStream_t s) {

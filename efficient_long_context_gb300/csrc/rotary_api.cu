@@ -256,11 +256,6 @@ orthros_status orthros_rotate_append(
         const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(uint32_t), stream);
         return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "status reset");
     }
-    // Up to kStatusHere new tokens, a block of the moving kernel checks them all and
-    // writes the status word besides its rows (a decoding step: one launch, 3.9 us;
-    // with a reset launch 6.2 us); that block would outlast the others on long
-    // inputs, which take a reset launch that the moving kernel starts beside.
-    constexpr int kStatusHere = 1024;
     RotateParams p{};
     p.x = q;
     p.y = q_rot;
@@ -296,7 +291,6 @@ orthros_status orthros_rotate_append(
     p.page_size = page_size;
     p.num_pages = num_pages;
     p.status = status;
-    p.status_here = n_new <= kStatusHere;
     ProfScope ps("rotate_append", stream);
     const cudaError_t e = launch_rotate_append(p, d, dtype, stream);
     return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "rotated append launch");
