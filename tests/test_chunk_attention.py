@@ -213,6 +213,16 @@ def test_long_history_and_large_logits():
 
 
 @pytest.mark.gpu
+def test_largest_window():
+    """A window of INT_MAX is every key (no index of the window's start may wrap)."""
+    for new, total, Hq, Hkv in (([200, 1], [200, 130], 1, 1), ([70], [900], 8, 2)):
+        w = make(new, total, Hq, Hkv, 64, 16, 1 << 20, seed=13)
+        got = call(dict(w, window=2 ** 31 - 1))
+        want = call(w)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
 def test_pool_past_32_bit_offsets():
     """Pages whose elements lie past 2^31 of the pool."""
     page, Hkv, d = 64, 8, 128
