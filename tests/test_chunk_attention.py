@@ -239,18 +239,20 @@ def test_pool_past_32_bit_offsets():
 
 
 @pytest.mark.gpu
-def test_bad_lengths_and_pages():
+@pytest.mark.parametrize("m", [70, 40])  # with and without a plan kernel (64 tokens are one unit here)
+def test_bad_lengths_and_pages(m):
     """Impossible data set their status bit and give NaN for the rows they concern, no others."""
-    new, total = [2, 70, 1], [300, 400, 90]
+    new, total = [2, m, 1], [300, 400, 90]
     w = make(new, total, 8, 2, 64, 16, 1 << 20, seed=10)
     ref = plain(w, 0.125)
-    rows = [slice(0, 2), slice(2, 72), slice(72, 73)]
-    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(3, 73, 73, 8, 2, 64, w["bt"].shape[1], 16),
+    rows = [slice(0, 2), slice(2, 2 + m), slice(2 + m, 3 + m)]
+    bound = m if m <= 64 else 3 + m
+    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(3, 3 + m, 3 + m, 8, 2, 64, w["bt"].shape[1], 16),
                      dtype=torch.uint8, device="cuda")
 
     def expect(bad, bits, **kw):
         v = dict(w, **kw)
-        o, lse = call(v, workspace=ws, max_new=kw.get("max_new", 73))
+        o, lse = call(v, workspace=ws, max_new=kw.get("max_new", bound))
         assert ola.orthros_check(ws) == (5, bits)
         for b in range(3):
             if b in bad:
@@ -262,12 +264,22 @@ def test_bad_lengths_and_pages():
     expect([0], 4, lens=lens(1, 400, 90))                           # fewer cached tokens than new ones
     expect([2], 4, lens=lens(300, 400, -5))
     expect([1], 4, lens=lens(300, w["bt"].shape[1] * 16 + 1, 90))   # past the block table
-    expect([1], 4, max_new=69)
+    expect([1], 4, max_new=m - 1)
+    expect([0, 2], 4, lens=lens(1, 400, 0))
+    expect([0, 1, 2], 4, lens=lens(1, 5, 0))
     bt = w["bt"].clone()
     bt[2, 0] = -1
     expect([2], 2, bt=bt)
-    for indptr in ([0, 2, 72, 72], [1, 2, 72, 73], [0, 72, 2, 73], [0, 2, 72, 74]):
+    for indptr in ([0, 2, 2 + m, 2 + m], [1, 2, 2 + m, 3 + m], [0, 2 + m, 2, 3 + m], [0, 2, 2 + m, 4 + m]):
         expect([0, 1, 2], 4, indptr=lens(*indptr))
+    # a single sequence, its units listed by the CTAs
+    v = make([50], [60], 8, 2, 64, 16, 1 << 20, seed=14)
+    for bad in (dict(lens=lens(49)), dict(indptr=lens(0, 49)), dict(lens=lens(1 << 20))):
+        o, lse = call(dict(v, **bad), workspace=ws)
+        assert ola.orthros_check(ws) == (5, 4)
+        assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+    check(call(v, workspace=ws), plain(v, 0.125))
+    assert ola.orthros_check(ws) == (0, 0)
     # a bad page in the middle of a chunk's keys: rows whose keys stop before its tile are untouched
     v = make([256], [256], 1, 1, 64, 16, 1 << 20, seed=11)
     ref = plain(v, 0.125)
