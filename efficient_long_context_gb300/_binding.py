@@ -560,16 +560,19 @@ def orthros_decode_static(q, k_new, v_new, k_cache, v_cache, block_table, cache_
 # The calls below are also made once per layer and decoding step on tensors of a
 # few hundred KB, where the marshalling is what takes the time: one look-up of
 # the current device and stream per call, plain integers for addresses.
-def _here():
-    """(current CUDA device, its current stream's handle); without a driver a
-    device that no tensor is on, so that every tensor is refused."""
-    if not torch.cuda.is_initialized():
-        try:
-            torch.cuda.init()
-        except RuntimeError:
-            return -2, None
-    dev = torch.cuda.current_device()
+def _here(t):
+    """(device that every tensor of the call has to be on, its current stream's handle):
+    the current CUDA device, for a call whose main tensor is t. For a t elsewhere a
+    device that no tensor is on, so that the call is refused while it is marshalled."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        return -2, None
     return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _new(t, shape):
+    """An uninitialised contiguous tensor of t's type on its device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(shape, dtype=t.dtype, device=t.device)
 
 
 def _elsewhere(t):
@@ -675,20 +678,23 @@ def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=N
     orthros_rotary_steps on the GPU. Returns y [n, H, d] (`out` may be x).
     """
     lib = _lib or load_library()
-    dev, here = _here()
-    shape = x.shape
+    dev, here = _here(x)
+    shape, dtype = x.shape, x.dtype
     n, H, d = shape
-    xa, xs = _rows("x", x, dev, x.dtype, shape)
+    xa, xs = _rows("x", x, dev, dtype, shape)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _new(x, shape)
         ya, ys = out.data_ptr(), H * d
     else:
-        ya, ys = _rows("out", out, dev, x.dtype, shape)
+        ya, ys = _rows("out", out, dev, dtype, shape)
     st, rot = _steps(steps, dev)
-    rc = lib.orthros_rotate(xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)),
-                            _block("beta", beta, dev, torch.float32, (H, d)), st, rot, _rope_layout(layout), amplitude, n, H,
-                            d, _dtype(x), ya, ys, here if stream is None else _stream(stream))
-    _raise_if(rc, lib)
+    pos = _index("positions", positions, dev, n)
+    al = _block("alpha", alpha, dev, torch.float32, (H, d))
+    be = _block("beta", beta, dev, torch.float32, (H, d))
+    rc = lib.orthros_rotate(xa, xs, pos, al, be, st, rot, _rope_layout(layout), amplitude, n, H, d, _dtype(x), ya, ys,
+                            here if stream is None else _stream(stream))
+    if rc:
+        _raise_if(rc, lib)
     return out
 
 
@@ -705,13 +711,14 @@ def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude
     affine_grads; `out` gives the three tensors.
     """
     lib = _lib or load_library()
-    dev, here = _here()
+    dev, here = _here(dy)
     shape, dtype = dy.shape, dy.dtype
     n, H, d = shape
     if out is None:
-        dx = torch.empty(shape, dtype=dtype, device=dy.device)
-        da = torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None
-        db = torch.empty((H, d), dtype=torch.float32, device=dy.device) if affine_grads else None
+        dx, da, db = _new(dy, shape), None, None
+        if affine_grads:
+            da = torch.empty((H, d), dtype=torch.float32, device=dy.device)
+            db = torch.empty_like(da)
         oa, os_ = dx.data_ptr(), H * d
     else:
         dx, da, db = out
@@ -741,7 +748,7 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     q_out_rot or None); k_cache / v_cache are updated in place.
     """
     lib = _lib or load_library()
-    dev, here = _here()
+    dev, here = _here(k_cache)
     dtype = k_new.dtype
     n, Hkv, d = k_new.shape
     n_out = q_out.shape[0] if q_out is not None else 0
@@ -749,8 +756,8 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     num_pages, page_size = k_cache.shape[:2]
     B, max_pages = block_table.shape
     if out is None:
-        q_rot = torch.empty((n, Hq, d), dtype=dtype, device=k_new.device) if q is not None else None
-        q_out_rot = torch.empty((n_out, Hq, d), dtype=dtype, device=k_new.device) if q_out is not None else None
+        q_rot = _new(q, (n, Hq, d)) if q is not None else None
+        q_out_rot = _new(q_out, (n_out, Hq, d)) if q_out is not None else None
     else:
         q_rot, q_out_rot = out
         _block("q_rot", q_rot, dev, dtype, (n, Hq, d))
@@ -792,7 +799,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     tokens of a sequence (default n). Returns (o [n, Hq, d], lse [n, Hq]).
     """
     lib = _lib or load_library()
-    dev, here = _here()
+    dev, here = _here(q)
     shape, dtype = q.shape, q.dtype
     n, Hq, d = shape
     num_pages, page_size, Hkv = k_cache.shape[:3]
@@ -800,7 +807,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     if max_new is None:
         max_new = n
     if out is None:
-        o = torch.empty(shape, dtype=dtype, device=q.device)
+        o = torch.empty_like(q)
         lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
         oa, la = o.data_ptr(), lse.data_ptr()
     else:
