@@ -742,10 +742,18 @@ __global__ void __launch_bounds__(kBound, 1)
                               kIdescO, kk > 0 ? 1u : acc0);
                 }
             };
-            uint32_t gk = 0;                   // key tiles consumed
-            uint32_t nq[2] = {0, 0};           // query tiles consumed per slot
-            uint32_t pc[2] = {0, 0};           // P tiles consumed per slot
-            uint32_t oc[2] = {0, 0};           // segments in which the slot had tiles
+            // stage and phase of the next key tile, the next value tile (counted, not divided: this
+            // warp's instructions are on the critical path)
+            uint32_t ks = 0, kph = 0, vs = 0, vph = 0;
+            auto next_k = [&]() {
+                if (++ks == kNumK) ks = 0, kph ^= 1;
+            };
+            auto next_v = [&]() {
+                if (++vs == kNumV) vs = 0, vph ^= 1;
+            };
+            uint32_t nq0 = 0, nq1 = 0;         // phase of the next query tile per slot
+            uint32_t pc0 = 0, pc1 = 0;         // of the next P tile
+            uint32_t oc0 = 0, oc1 = 0;         // segments in which the slot had tiles
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 const int r = i % kSegRing;
@@ -758,92 +766,102 @@ __global__ void __launch_bounds__(kBound, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mt.g_empty[r]);
                 if (end) break;
-                auto value_tile = [&](int it) -> bool {
-                    const uint32_t gi = gk + it;
-                    return mbar_wait_warp(&mt.v_full[gi % kNumV], (gi / kNumV) & 1, abort, status);
+                auto key_tile = [&]() -> bool {
+                    if (!mbar_wait_warp(&mt.k_full[ks], kph, abort, status)) return false;
+                    tc_fence_after();
+                    return true;
                 };
-                auto key_tile = [&](int it) -> bool {
-                    const uint32_t gi = gk + it;
-                    return mbar_wait_warp(&mt.k_full[gi % kNumK], (gi / kNumK) & 1, abort, status);
-                };
-                auto kdesc = [&](int it) { return dk + (uint64_t)(((gk + it) % kNumK) * kTileU); };
-                auto vdesc = [&](int it) { return dv + (uint64_t)(((gk + it) % kNumV) * kTileU); };
+                auto value_tile = [&]() -> bool { return mbar_wait_warp(&mt.v_full[vs], vph, abort, status); };
                 // the slot's next P V: the first half of the keys goes while the softmax finishes the second;
                 // before the slot's first product of the segment, its O is free
-                auto pv_tile = [&](int s, int it, bool first) -> bool {
+                auto pv_tile = [&](int s, uint32_t &pc, uint32_t &oc, bool first) -> bool {
+                    const uint64_t vd = dv + (uint64_t)(vs * kTileU);
                     if (first) {
-                        if (oc[s] > 0 && !mbar_wait_warp(&mt.o_free[s], (oc[s] - 1) & 1, abort, status)) return false;
-                        ++oc[s];
+                        if (oc > 0 && !mbar_wait_warp(&mt.o_free[s], (oc - 1) & 1, abort, status)) return false;
+                        ++oc;
                     }
-                    if (!mbar_wait_warp(&mt.p_half[s], pc[s] & 1, abort, status)) return false;
+                    if (!mbar_wait_warp(&mt.p_half[s], pc, abort, status)) return false;
                     tc_fence_after();
-                    issue_pv(s, 0, vdesc(it), !first);
-                    if (!mbar_wait_warp(&mt.p_full[s], pc[s] & 1, abort, status)) return false;
+                    issue_pv(s, 0, vd, !first);
+                    if (!mbar_wait_warp(&mt.p_full[s], pc, abort, status)) return false;
                     tc_fence_after();
-                    issue_pv(s, 1, vdesc(it), 1);
-                    ++pc[s];
+                    issue_pv(s, 1, vd, 1);
+                    pc ^= 1;
                     return true;
                 };
                 if (pair) {
                     // first tile's S of both slots
-                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, status) && key_tile(0))) break;
-                    tc_fence_after();
-                    if (lo0 <= 0 && hi0 >= 0) issue_s(0, dq, kdesc(0));
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq0, abort, status) && key_tile())) break;
+                    if (lo0 <= 0 && hi0 >= 0) issue_s(0, dq, dk + (uint64_t)(ks * kTileU));
                     if (n == 1) tc_commit_if(el, &mt.q_empty[0]);
-                    if (!(ok = mbar_wait_warp(&mt.q_full[1], nq[1] & 1, abort, status))) break;
+                    if (!(ok = mbar_wait_warp(&mt.q_full[1], nq1, abort, status))) break;
                     tc_fence_after();
-                    if (lo1 <= 0 && hi1 >= 0) issue_s(1, dq + kTileU, kdesc(0));
+                    if (lo1 <= 0 && hi1 >= 0) issue_s(1, dq + kTileU, dk + (uint64_t)(ks * kTileU));
                     if (n == 1) tc_commit_if(el, &mt.q_empty[1]);
-                    tc_commit_if(el, &mt.k_empty[gk % kNumK]);
+                    tc_commit_if(el, &mt.k_empty[ks]);
+                    next_k();
                     // per tile and slot: P V, then the next tile's S into the columns that held P
-                    for (int it = 0; it < n; ++it) {
-                        const bool more = it + 1 < n;
-                        if (!(ok = value_tile(it))) break;
-                        if (it >= lo0 && it <= hi0) {
-                            if (!(ok = pv_tile(0, it, it == lo0))) break;
-                            if (it == hi0) tc_commit_if(el, &mt.o_full[0]);
+                    int it = 0;
+                    // both: both slots work on tiles it and it + 1, neither for the first or the last time
+                    auto tile = [&](bool both) -> bool {
+                        const bool more = both || it + 1 < n;
+                        if (!value_tile()) return false;
+                        if (both || (it >= lo0 && it <= hi0)) {
+                            if (!pv_tile(0, pc0, oc0, !both && it == lo0)) return false;
+                            if (!both && it == hi0) tc_commit_if(el, &mt.o_full[0]);
                         }
                         if (more) {
-                            if (!(ok = key_tile(it + 1))) break;
-                            tc_fence_after();
-                            if (it + 1 >= lo0 && it + 1 <= hi0) issue_s(0, dq, kdesc(it + 1));
+                            if (!key_tile()) return false;
+                            if (both || (it + 1 >= lo0 && it + 1 <= hi0)) issue_s(0, dq, dk + (uint64_t)(ks * kTileU));
                             if (it + 2 == n) tc_commit_if(el, &mt.q_empty[0]);
                         }
-                        if (it >= lo1 && it <= hi1) {
-                            if (!(ok = pv_tile(1, it, it == lo1))) break;
-                            if (it == hi1) tc_commit_if(el, &mt.o_full[1]);
+                        if (both || (it >= lo1 && it <= hi1)) {
+                            if (!pv_tile(1, pc1, oc1, !both && it == lo1)) return false;
+                            if (!both && it == hi1) tc_commit_if(el, &mt.o_full[1]);
                         }
-                        tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
+                        tc_commit_if(el, &mt.v_empty[vs]);
+                        next_v();
                         if (more) {
-                            if (it + 1 >= lo1 && it + 1 <= hi1) issue_s(1, dq + kTileU, kdesc(it + 1));
+                            if (both || (it + 1 >= lo1 && it + 1 <= hi1)) issue_s(1, dq + kTileU, dk + (uint64_t)(ks * kTileU));
                             if (it + 2 == n) tc_commit_if(el, &mt.q_empty[1]);
-                            tc_commit_if(el, &mt.k_empty[(gk + it + 1) % kNumK]);
+                            tc_commit_if(el, &mt.k_empty[ks]);
+                            next_k();
                         }
-                    }
-                    ++nq[0];
-                    ++nq[1];
-                } else {
-                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq[0] & 1, abort, status))) break;
-                    ++nq[0];
-                    // S of tile it into slot it & 1
-                    auto s_tile = [&](int it) -> bool {
-                        if (!key_tile(it)) return false;
-                        tc_fence_after();
-                        issue_s(it & 1, dq, kdesc(it));
-                        if (it + 1 == n) tc_commit_if(el, &mt.q_empty[0]);
-                        tc_commit_if(el, &mt.k_empty[(gk + it) % kNumK]);
+                        ++it;
                         return true;
                     };
-                    ok = s_tile(0) && (n < 2 || s_tile(1));
+                    const int mid0 = max(lo0, lo1) + 1, mid1 = min(hi0, hi1);  // tiles mid0 .. mid1 - 1 in full
+                    while (ok && it < n) {
+                        while (ok && it >= mid0 && it < mid1) ok = tile(true);
+                        if (ok && it < n) ok = tile(false);
+                    }
+                    nq0 ^= 1;
+                    nq1 ^= 1;
+                } else {
+                    if (!(ok = mbar_wait_warp(&mt.q_full[0], nq0, abort, status))) break;
+                    nq0 ^= 1;
+                    // tile it's S into slot s
+                    auto s_tile = [&](int it, int s) -> bool {
+                        if (!key_tile()) return false;
+                        issue_s(s, dq, dk + (uint64_t)(ks * kTileU));
+                        if (it + 1 == n) tc_commit_if(el, &mt.q_empty[0]);
+                        tc_commit_if(el, &mt.k_empty[ks]);
+                        next_k();
+                        return true;
+                    };
+                    ok = s_tile(0, 0) && (n < 2 || s_tile(1, 1));
+                    // (one body for both slots: these segments are short, their code mostly cold)
+                    uint32_t pc[2] = {pc0, pc1}, oc[2] = {oc0, oc1};
                     for (int it = 0; ok && it < n; ++it) {
                         const int s = it & 1;
-                        if (!(ok = value_tile(it) && pv_tile(s, it, it < 2))) break;
+                        if (!(ok = value_tile() && pv_tile(s, pc[s], oc[s], it < 2))) break;
                         if (it + 2 >= n) tc_commit_if(el, s ? &mt.ox_full : &mt.o_full[0]);
-                        tc_commit_if(el, &mt.v_empty[(gk + it) % kNumV]);
-                        if (it + 2 < n) ok = s_tile(it + 2);
+                        tc_commit_if(el, &mt.v_empty[vs]);
+                        next_v();
+                        if (it + 2 < n) ok = s_tile(it + 2, s);
                     }
+                    pc0 = pc[0], pc1 = pc[1], oc0 = oc[0], oc1 = oc[1];
                 }
-                gk += n;
             }
             // every product issued must be complete before tensor memory is freed
             tc_commit_if(el, &mt.mma_done);
