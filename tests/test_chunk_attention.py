@@ -164,6 +164,10 @@ CASES = [
     ([9, 1], [500, 300], 40, 1, 128, 64, 1 << 20),
     ([3, 2], [130, 5], 128, 1, 64, 8, 1 << 20),
     ([5, 1], [400, 40], 3, 1, 64, 8, 77),
+    # kv heads that share no or a small factor with the number of SMs
+    ([40, 1, 300], [900, 2000, 300], 10, 5, 128, 64, 1 << 20),
+    ([7, 129], [300, 700], 24, 12, 64, 16, 200),
+    ([1, 1], [777, 3000], 7, 7, 128, 64, 1 << 20),
     # page sizes without a copy box
     ([1, 1], [300, 7], 8, 2, 128, 1, 1 << 20),
     ([60, 1], [300, 129], 8, 2, 128, 5, 1 << 20),
@@ -288,6 +292,35 @@ def test_bad_lengths_and_pages(m):
     o, lse = call(dict(v, bt=bt))
     check((o[:128], lse[:128]), [r[:128] for r in ref])
     assert bool(torch.isnan(o[128:]).all()) and bool(torch.isnan(lse[128:]).all())
+
+
+@pytest.mark.gpu
+def test_outputs_on_16_byte_boundaries():
+    """o may start at any 16-byte boundary (32-byte stores only where they fit), and nothing beside it is touched."""
+    for new, total in (([1, 40], [400, 500]), ([200], [300])):
+        w = make(new, total, 8, 2, 128, 16, 1 << 20, seed=15)
+        n = sum(new)
+        flat = torch.full((n * 8 * 128 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        o = flat[8:8 + n * 8 * 128].view(n, 8, 128)
+        lse = torch.empty((n, 8), device="cuda")
+        call(w, out=(o, lse))
+        want = call(w)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert bool((flat[:8] == 7).all()) and bool((flat[-8:] == 7).all())
+
+
+@pytest.mark.gpu
+def test_non_finite_query_stays_in_its_row():
+    w = make([40, 3], [200, 50], 8, 2, 64, 16, 1 << 20, seed=16)
+    want = call(w)
+    q = w["q"].clone()
+    q[5, 3] = float("nan")
+    q[41, 0, 7] = float("inf")
+    o, lse = call(dict(w, q=q))
+    keep = torch.ones(43, 8, dtype=torch.bool)
+    keep[5, 3] = keep[41, 0] = False
+    assert torch.equal(o[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
+    assert bool(torch.isnan(o[5, 3]).all()) and not bool(torch.isfinite(o[41, 0]).any())
 
 
 @pytest.mark.gpu
