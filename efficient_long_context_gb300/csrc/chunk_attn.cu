@@ -1213,7 +1213,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
             for (int e = 0; e < E; ++e) acc[i][e] *= w0;
 #pragma unroll
             for (int k = 0; k < kParts; ++k) {
-                if (ml[k][i].x == -INFINITY) continue;  // a part without keys for this row wrote no output
+                if (ml[k][i].x == -INFINITY) {  // no finite logit: no output, and a sum of 0 or NaN
+                    L[i] += ml[k][i].y;
+                    continue;
+                }
                 const float w = ex2(ml[k][i].x * c2 - mb);
                 L[i] = fmaf(w, ml[k][i].y, L[i]);
 #pragma unroll
