@@ -110,7 +110,7 @@ struct Meta {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    volatile int bad[kFlagRing];  // per key tile (running count): a page id of its keys was outside the pool
+    volatile int bad[kFlagRing];  // per key tile (running count): its keys [bad >> 8, bad & 255) had page ids outside the pool
     Segment seg[kSegRing];
     float2 ml[kRows];             // slot 1's running max and sum, for slot 0 (shared row tile)
 };
@@ -620,10 +620,10 @@ __global__ void __launch_bounds__(kBound, 1)
                         }
                         uint8_t *ks = smem + C::kK0 + sk * C::kTile, *vs = smem + C::kV0 + sv * C::kTile;
                         if (box) {
-                            const bool any_bad = __any_sync(0xffffffffu, bad);
-                            if (any_bad && lane == 0) set_status(status, ORTHROS_DEV_BAD_PAGE);
+                            const unsigned wrong = __ballot_sync(0xffffffffu, bad);
                             if (lane == 0) {
-                                mt.bad[gi % kFlagRing] = any_bad;
+                                if (wrong) set_status(status, ORTHROS_DEV_BAD_PAGE);
+                                mt.bad[gi % kFlagRing] = wrong ? (__ffs(wrong) - 1) * box << 8 | (32 - __clz(wrong)) * box : 0;
                                 mbar_arrive_expect_tx(&mt.k_full[sk], C::kTile);
                             }
                             __syncwarp();
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kBound, 1)
                                 alive = false;
                                 break;
                             }
-                            int wrong = 0;
+                            unsigned bad0 = kKeys, bad1 = 0;  // first and past the last key without a page
                             constexpr int kCh = D / 8;
                             for (int e = lane; e < kRows * kCh; e += 32) {
                                 const int row = e / kCh, c = e % kCh;
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kBound, 1)
                                 long long src = -1;
                                 if (key >= key_lo && key <= key_hi) {
                                     const int pg = bt[key / p.page_size];
-                                    if (pg < 0 || pg >= p.num_pages) wrong = 1;
+                                    if (pg < 0 || pg >= p.num_pages) bad0 = min(bad0, (unsigned)row), bad1 = max(bad1, (unsigned)row + 1);
                                     else src = (((long long)pg * p.page_size + key % p.page_size) * p.Hkv + sg.kv) * D + 8 * c;
                                 }
                                 const uint32_t dk = smem_u32(ks + kv_offset<D>(row, c)), dv = smem_u32(vs + kv_offset<D>(row, c));
@@ -669,10 +669,11 @@ __global__ void __launch_bounds__(kBound, 1)
                             }
                             asm volatile("cp.async.wait_all;" ::: "memory");
                             fence_proxy_async_smem();
-                            wrong = __any_sync(0xffffffffu, wrong);
+                            bad0 = __reduce_min_sync(0xffffffffu, bad0);
+                            bad1 = __reduce_max_sync(0xffffffffu, bad1);
                             if (lane == 0) {
-                                if (wrong) set_status(status, ORTHROS_DEV_BAD_PAGE);
-                                mt.bad[gi % kFlagRing] = wrong;
+                                if (bad1) set_status(status, ORTHROS_DEV_BAD_PAGE);
+                                mt.bad[gi % kFlagRing] = bad1 ? (int)(bad0 << 8 | bad1) : 0;
                                 mbar_arrive(&mt.k_full[sk]);
                                 mbar_arrive(&mt.v_full[sv]);
                             }
@@ -941,7 +942,8 @@ __global__ void __launch_bounds__(kBound, 1)
                 }
                 tc_fence_after();
                 const int key0 = (sg.kt0 + it) * kKeys;
-                if (mt.bad[(gk + it) % kFlagRing] && key0 <= t_row && key0 + kKeys - 1 >= lo_row) bad = true;
+                const int no_page = mt.bad[(gk + it) % kFlagRing];
+                if (no_page && key0 + (no_page >> 8) <= t_row && key0 + (no_page & 255) > lo_row) bad = true;
                 uint32_t xr[kKeys];
                 using Cols = uint32_t[32];
                 const float *x = reinterpret_cast<const float *>(xr);

@@ -284,14 +284,25 @@ def test_bad_lengths_and_pages(m):
         assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
     check(call(v, workspace=ws), plain(v, 0.125))
     assert ola.orthros_check(ws) == (0, 0)
-    # a bad page in the middle of a chunk's keys: rows whose keys stop before its tile are untouched
+    # a bad page (keys 144 .. 159) in the middle of a chunk's keys: rows that stop before them are untouched
     v = make([256], [256], 1, 1, 64, 16, 1 << 20, seed=11)
     ref = plain(v, 0.125)
     bt = v["bt"].clone()
     bt[0, 9] = 1 << 20
     o, lse = call(dict(v, bt=bt))
-    check((o[:128], lse[:128]), [r[:128] for r in ref])
-    assert bool(torch.isnan(o[128:]).all()) and bool(torch.isnan(lse[128:]).all())
+    check((o[:144], lse[:144]), [r[:144] for r in ref])
+    assert bool(torch.isnan(o[144:]).all()) and bool(torch.isnan(lse[144:]).all())
+    # with a window, rows past it too; the same on pages that are gathered row by row
+    for page, entry in ((16, 9), (12, 12)):
+        v = make([256], [256], 1, 1, 128, page, 50, seed=17)
+        ref = plain(v, 128 ** -0.5)
+        bt = v["bt"].clone()
+        bt[0, entry] = -7
+        o, lse = call(dict(v, bt=bt))
+        last = entry * page + page - 1 + 49  # the last row whose window holds one of its keys
+        for rows in (slice(0, 144), slice(last + 1, 256)):
+            check((o[rows], lse[rows]), [r[rows] for r in ref])
+        assert bool(torch.isnan(o[144:last + 1]).all()) and bool(torch.isnan(lse[144:last + 1]).all())
 
 
 @pytest.mark.gpu
