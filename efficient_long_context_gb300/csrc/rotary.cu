@@ -64,6 +64,11 @@ template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float (&f
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes from global to shared memory, not through registers.
+__device__ __forceinline__ void copy16(uint4 *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
 // cos and sin of position t's angle for one frequency step, times the amplitude.
 __device__ __forceinline__ void angle(int t, uint64_t step, float amp, float &c, float &s) {
     const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(t)) * step;  // modulo one turn
@@ -147,7 +152,7 @@ constexpr int kRunTokens = 128;  // positions (and page slots) a block looks up 
 // Tokens of a table (a divisor of kRunTokens): two batches' worth of loads of one
 // token a thread; more when tokens go side by side. A longer table delays its
 // first rows (16 and 32 tokens: 1 and 5 % at 32 heads).
-__device__ __forceinline__ int table_tokens(int lanes) { return lanes > 1 ? kTabTokens : kTabTokens / 2; }
+__host__ __device__ __forceinline__ int table_tokens(int lanes) { return lanes > 1 ? kTabTokens : kTabTokens / 2; }
 template <typename T, int D> struct Table {
     static constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kQ = VEC / 2;
     float4 e[kTabTokens][kQ][IPR];
@@ -352,16 +357,16 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
 // it). One block of 256 threads with four tokens in flight fills the SM's
 // registers; two blocks with two in flight spill (143 us), with one, 153 us.
 // ---------------------------------------------------------------------------
-constexpr int kBwdThreads = 256;
-constexpr int kBwdBatch = 4;   // tokens whose loads a thread has in flight
+constexpr int kBwdThreads = 512;
 constexpr int kBwdBlocks = 1;  // blocks per SM
+constexpr int kBwdDepth = 6;   // tokens a thread has in flight
 
 template <typename T, int D, bool kGrads>
 __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kernel(const RotateBwdParams p) {
-    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
+    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kV = kGrads ? 4 : 2;
+    extern __shared__ uint4 fifo[];  // [kBwdDepth][kV][thread]
     __shared__ Table<T, D> tab[2];
     __shared__ int pos[kRunTokens];
-    __shared__ float red[kBwdThreads * 2];
     const int tid = threadIdx.x;
     const int hb = p.heads_per_block;            // heads of this block
     const int lanes = kBwdThreads / (hb * IPR);  // tokens handled side by side
@@ -372,6 +377,29 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
     const Item<VEC, D> it(item, p.rot, p.interleaved);
     const int ca = it.ca, cb = it.cb;
     const long long n0 = p.n * blockIdx.x / gridDim.x, n1 = p.n * (blockIdx.x + 1) / gridDim.x;
+    const int step = table_tokens(lanes);
+    const int n = (int)(n1 - n0);
+    // this thread's tokens, kBwdDepth of them ahead
+    int ahead = 0, ahead_k = tl, wr = 0;
+    auto fetch = [&]() {
+        if (active && ahead_k < step && ahead + ahead_k < n) {
+            uint4 *to = fifo + wr * kV * kBwdThreads + tid;
+            const long long i = n0 + ahead + ahead_k;
+            const T *dy = static_cast<const T *>(p.dy) + i * p.dy_stride + h * D;
+            copy16(to, dy + ca);
+            copy16(to + kBwdThreads, dy + cb);
+            if constexpr (kGrads) {
+                const T *x = static_cast<const T *>(p.x) + i * p.x_stride + h * D;
+                copy16(to + 2 * kBwdThreads, x + ca);
+                copy16(to + 3 * kBwdThreads, x + cb);
+            }
+            ahead_k += lanes;
+            if (ahead_k >= step) ahead += step, ahead_k = tl;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        wr = wr + 1 == kBwdDepth ? 0 : wr + 1;
+    };
+    for (int i = 0; i < kBwdDepth; ++i) fetch();
     float al[2][VEC], da[2][VEC], db[2][VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -379,90 +407,73 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
         da[0][j] = da[1][j] = db[0][j] = db[1][j] = 0.f;
     }
     if (active && p.alpha) load_affine<VEC>(p.alpha + h * D, ca, cb, al[0], al[1]);
-    const int step = table_tokens(lanes);
-    int buf = 0;
-    for (long long base = n0; base < n1; base += step, buf ^= 1) {
-        const int cnt = (int)min((long long)step, n1 - base);
-        uint4 ra[kBwdBatch], rb[kBwdBatch], xa[kBwdBatch], xb[kBwdBatch];
-        auto load = [&](int k0) {
-#pragma unroll
-            for (int u = 0; u < kBwdBatch; ++u) {
-                const int k = k0 + u * lanes;
-                if (k >= cnt) break;
-                const T *dy = static_cast<const T *>(p.dy) + (base + k) * p.dy_stride + h * D;
-                ra[u] = __ldcs(reinterpret_cast<const uint4 *>(dy + ca));
-                rb[u] = __ldcs(reinterpret_cast<const uint4 *>(dy + cb));
-                if constexpr (kGrads) {
-                    const T *x = static_cast<const T *>(p.x) + (base + k) * p.x_stride + h * D;
-                    xa[u] = __ldcs(reinterpret_cast<const uint4 *>(x + ca));
-                    xb[u] = __ldcs(reinterpret_cast<const uint4 *>(x + cb));
-                }
-            }
-        };
-        if (active) load(tl);
-        const int run = (int)((base - n0) % kRunTokens);
+    int buf = 0, rd = 0;
+    for (int base = 0; base < n; base += step, buf ^= 1) {
+        const int cnt = min(step, n - base);
+        const int run = base % kRunTokens;  // first entry of these tokens in pos
         if (run == 0) {
             __syncthreads();
-            for (int k = tid; k < kRunTokens && base + k < n1; k += kBwdThreads) pos[k] = p.positions[base + k];
+            for (int k = tid; k < kRunTokens && base + k < n; k += kBwdThreads) pos[k] = p.positions[n0 + base + k];
             __syncthreads();
         }
         tab[buf].fill(pos + run, cnt, p.steps, p.rot, p.interleaved, p.amplitude, -1.f);  // the opposite angle
         __syncthreads();
         if (!active) continue;
-        for (int k0 = tl; k0 < cnt; k0 += kBwdBatch * lanes) {
-            if (k0 != tl) load(k0);
-#pragma unroll
-            for (int u = 0; u < kBwdBatch; ++u) {
-                const int k = k0 + u * lanes;
-                if (k >= cnt) break;
-                float a[VEC], b[VEC], c[VEC], s[VEC];
-                unpack<T>(ra[u], a);
-                unpack<T>(rb[u], b);
-                tab[buf].read(k, item, c, s);
-                turn<VEC, D>(a, b, c, s, it, p.interleaved);
-                if constexpr (kGrads) {
-                    float x0[VEC], x1[VEC];
-                    unpack<T>(xa[u], x0);
-                    unpack<T>(xb[u], x1);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        da[0][j] = fmaf(a[j], x0[j], da[0][j]);
-                        da[1][j] = fmaf(b[j], x1[j], da[1][j]);
-                        db[0][j] += a[j];
-                        db[1][j] += b[j];
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) a[j] *= al[0][j], b[j] *= al[1][j];
-                T *dx = static_cast<T *>(p.dx) + (base + k) * p.dx_stride + h * D;
-                *reinterpret_cast<uint4 *>(dx + ca) = pack<T>(a);
-                *reinterpret_cast<uint4 *>(dx + cb) = pack<T>(b);
+        for (int k = tl; k < cnt; k += lanes) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kBwdDepth - 1) : "memory");
+            const uint4 *from = fifo + rd * kV * kBwdThreads + tid;
+            rd = rd + 1 == kBwdDepth ? 0 : rd + 1;
+            float a[VEC], b[VEC], c[VEC], s[VEC];
+            float x0[VEC], x1[VEC];
+            unpack<T>(from[0], a);
+            unpack<T>(from[kBwdThreads], b);
+            if constexpr (kGrads) {
+                unpack<T>(from[2 * kBwdThreads], x0);
+                unpack<T>(from[3 * kBwdThreads], x1);
             }
+            tab[buf].read(k, item, c, s);
+            turn<VEC, D>(a, b, c, s, it, p.interleaved);
+            if constexpr (kGrads) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    da[0][j] = fmaf(a[j], x0[j], da[0][j]);
+                    da[1][j] = fmaf(b[j], x1[j], da[1][j]);
+                    db[0][j] += a[j];
+                    db[1][j] += b[j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a[j] *= al[0][j], b[j] *= al[1][j];
+            T *dx = static_cast<T *>(p.dx) + (n0 + base + k) * p.dx_stride + h * D;
+            *reinterpret_cast<uint4 *>(dx + ca) = pack<T>(a);
+            *reinterpret_cast<uint4 *>(dx + cb) = pack<T>(b);
+            fetch();  // into the slot this thread has just read
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (kGrads) {
-        // sum over the token lanes of the block, one channel of every thread at a time
-        float *part = p.partial + (long long)blockIdx.x * 2 * p.H * D;
+        // sums over the token lanes of the block, through the shared memory that the loads have left:
+        // [value of a thread][thread]
+        float *red = reinterpret_cast<float *>(fifo);
+        __syncthreads();
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                __syncthreads();
-                red[tid] = da[v][j];
-                red[kBwdThreads + tid] = db[v][j];
-                __syncthreads();
-                if (tl == 0 && active) {
-                    float sa = 0.f, sb = 0.f;
-                    for (int l = 0; l < lanes; ++l) {
-                        sa += red[l * hb * IPR + tid];
-                        sb += red[kBwdThreads + l * hb * IPR + tid];
-                    }
-                    const int ch = h * D + (v ? cb : ca) + j;
-                    part[ch] = sa;
-                    part[p.H * D + ch] = sb;
-                }
+                red[(v * VEC + j) * kBwdThreads + tid] = da[v][j];
+                red[((2 + v) * VEC + j) * kBwdThreads + tid] = db[v][j];
             }
+        }
+        __syncthreads();
+        float *part = p.partial + (long long)blockIdx.x * 2 * p.H * D;
+        const int row = hb * IPR;  // threads of a token lane
+        if (!active) return;
+        for (int v = tl; v < 4 * VEC; v += lanes) {  // this thread's channels, shared with its fellows of other lanes
+            const float *from = red + v * kBwdThreads + tid - tl * row;
+            float sum = 0.f;
+            for (int l = 0; l < lanes; ++l) sum += from[l * row];
+            const int j = v % VEC, ch = h * D + (v / VEC & 1 ? cb : ca) + j;
+            part[(v < 2 * VEC ? 0 : p.H * D) + ch] = sum;
         }
     }
 }
@@ -548,8 +559,17 @@ template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStrea
     constexpr int IPR = D / (2 * Vec<T>::kN);
     p.heads_per_block = p.H < kBwdThreads / IPR ? p.H : kBwdThreads / IPR;
     const dim3 grid(p.n_part, (p.H + p.heads_per_block - 1) / p.heads_per_block);
-    if (p.d_alpha) rotate_backward_kernel<T, D, true><<<grid, kBwdThreads, 0, s>>>(p);
-    else rotate_backward_kernel<T, D, false><<<grid, kBwdThreads, 0, s>>>(p);
+    const bool grads = p.d_alpha != nullptr;
+    const auto kernel = grads ? rotate_backward_kernel<T, D, true> : rotate_backward_kernel<T, D, false>;
+    constexpr int kSlot = kBwdThreads * 16;
+    static SmemLimit limit[2];
+    if (cudaError_t e = limit[grads].ensure((const void *)kernel, kBwdDepth * (grads ? 4 : 2) * kSlot); e != cudaSuccess) return e;
+    // slots for the tokens of a thread, where those are few
+    const int lanes = kBwdThreads / (p.heads_per_block * IPR), step = table_tokens(lanes);
+    const long long m = (p.n + p.n_part - 1) / p.n_part, most = (m + step - 1) / step * ((step + lanes - 1) / lanes);
+    int fifo = (int)(most < kBwdDepth ? most : kBwdDepth) * (grads ? 4 : 2) * kSlot;
+    if (grads && fifo < Vec<T>::kN * kSlot) fifo = Vec<T>::kN * kSlot;  // the sums' exchange
+    kernel<<<grid, kBwdThreads, fifo, s>>>(p);
     return cudaGetLastError();
 }
 
