@@ -149,10 +149,12 @@ __device__ __forceinline__ void load_affine(const float *p, int ca, int cb, floa
 // lanes of a row read consecutive 16-byte words.
 constexpr int kTabTokens = 16;  // at most
 constexpr int kRunTokens = 128;  // positions (and page slots) a block looks up at a time
-// Tokens of a table (a divisor of kRunTokens): two batches' worth of loads of one
-// token a thread; more when tokens go side by side. A longer table delays its
-// first rows (16 and 32 tokens: 1 and 5 % at 32 heads).
-__host__ __device__ __forceinline__ int table_tokens(int lanes) { return lanes > 1 ? kTabTokens : kTabTokens / 2; }
+constexpr int kBatch = 4;        // tokens whose loads a thread of the moving kernel has in flight
+// Tokens of a table (a divisor of kRunTokens), for so many handled side by side: one
+// batch of loads a thread, which are under way while the angles are computed. Two
+// batches leave the second one's trip to memory bare: 16384 x 32 x 128 fp32 96 us
+// instead of 86, 32768 x 8 x 128 53 instead of 46.
+__device__ __forceinline__ int table_tokens(int lanes) { return lanes > 2 ? kTabTokens : kBatch * lanes; }
 template <typename T, int D> struct Table {
     static constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kQ = VEC / 2;
     float4 e[kTabTokens][kQ][IPR];
@@ -194,7 +196,6 @@ template <typename T, int D> struct Table {
 // stream's rows; an append's last one writes the status word.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 512;  // at most
-constexpr int kBatch = 4;
 
 // Token slot of new token i in the page pool, or -1 when it has none.
 __device__ __forceinline__ long long page_slot(const RotateParams &p, long long i) {
@@ -352,10 +353,14 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
 // registers, so d_alpha and d_beta cost no traffic per token. The block's sums go
 // to the workspace as one partial each, and rotate_grad_sum_kernel adds the
 // partials in a fixed order (no atomics: the same call gives the same bits).
-// Bound by HBM: dy and x read once, dx written. 32768 x 32 x 128 bf16: 139 us,
-// 5.8 TB/s (85 % of the measured copy rate; the sum of the partials is 5 us of
-// it). One block of 256 threads with four tokens in flight fills the SM's
-// registers; two blocks with two in flight spill (143 us), with one, 153 us.
+// Rows reach a thread through slots of its own in shared memory, kBwdDepth tokens
+// ahead: no other thread touches them, so they need no barrier.
+// Bound by HBM: dy and x read once, dx written. 32768 x 32 x 128 bf16: 133 us,
+// 6.0 TB/s (89 % of the measured copy rate; the sum of the partials is 5 us of
+// it). 138 us with four tokens in flight in registers (which they filled with 256
+// threads), 138 with three ahead instead of six, 143 as two blocks of 256
+// threads. The moving kernel above keeps its loads in registers: through
+// shared memory it took 84 to 110 us by the depth, and its append 38 to 46.
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
 constexpr int kBwdBlocks = 1;  // blocks per SM
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
     const Item<VEC, D> it(item, p.rot, p.interleaved);
     const int ca = it.ca, cb = it.cb;
     const long long n0 = p.n * blockIdx.x / gridDim.x, n1 = p.n * (blockIdx.x + 1) / gridDim.x;
-    const int step = table_tokens(lanes);
+    constexpr int step = kTabTokens;
     const int n = (int)(n1 - n0);
     // this thread's tokens, kBwdDepth of them ahead
     int ahead = 0, ahead_k = tl, wr = 0;
@@ -565,7 +570,7 @@ template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStrea
     static SmemLimit limit[2];
     if (cudaError_t e = limit[grads].ensure((const void *)kernel, kBwdDepth * (grads ? 4 : 2) * kSlot); e != cudaSuccess) return e;
     // slots for the tokens of a thread, where those are few
-    const int lanes = kBwdThreads / (p.heads_per_block * IPR), step = table_tokens(lanes);
+    const int lanes = kBwdThreads / (p.heads_per_block * IPR), step = kTabTokens;
     const long long m = (p.n + p.n_part - 1) / p.n_part, most = (m + step - 1) / step * ((step + lanes - 1) / lanes);
     int fifo = (int)(most < kBwdDepth ? most : kBwdDepth) * (grads ? 4 : 2) * kSlot;
     if (grads && fifo < Vec<T>::kN * kSlot) fifo = Vec<T>::kN * kSlot;  // the sums' exchange
@@ -575,7 +580,7 @@ template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStrea
 
 }  // namespace
 
-// Partials of the affine's gradient (blocks along the tokens): two blocks per
+// Partials of the affine's gradient (blocks along the tokens): kBwdBlocks per
 // SM over all head groups, but no fewer than 16 tokens a block.
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes) {
     const int per = kBwdThreads / (d * elem_bytes / 32);  // heads of a block
