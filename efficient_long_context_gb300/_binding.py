@@ -570,6 +570,14 @@ def _here(t):
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _on(stream):
+    """Context in which the caller's stream is the current one: what a call allocates
+    then belongs to the stream that writes it, and is not handed on before that is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _new(t, shape):
     """An uninitialised contiguous tensor of t's type on its device."""
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(shape, dtype=t.dtype, device=t.device)
@@ -677,6 +685,9 @@ def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=N
     x [n, H, d] (any token stride), positions [n] int32, steps from
     orthros_rotary_steps on the GPU. Returns y [n, H, d] (`out` may be x).
     """
+    if stream is not None:
+        with _on(stream):
+            return orthros_rotate(x, positions, steps, layout=layout, amplitude=amplitude, alpha=alpha, beta=beta, out=out)
     lib = _lib or load_library()
     dev, here = _here(x)
     shape, dtype = x.shape, x.dtype
@@ -692,7 +703,7 @@ def orthros_rotate(x, positions, steps, *, layout="half", amplitude=1.0, alpha=N
     al = _block("alpha", alpha, dev, torch.float32, (H, d))
     be = _block("beta", beta, dev, torch.float32, (H, d))
     rc = lib.orthros_rotate(xa, xs, pos, al, be, st, rot, _rope_layout(layout), amplitude, n, H, d, _dtype(x), ya, ys,
-                            here if stream is None else _stream(stream))
+                            here)
     if rc:
         _raise_if(rc, lib)
     return out
@@ -710,6 +721,10 @@ def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude
     Returns (dx, d_alpha, d_beta), the last two float [H, d], or None without
     affine_grads; `out` gives the three tensors.
     """
+    if stream is not None:
+        with _on(stream):
+            return orthros_rotate_backward(dy, x, positions, steps, layout=layout, amplitude=amplitude, alpha=alpha,
+                                           affine_grads=affine_grads, out=out, workspace=workspace)
     lib = _lib or load_library()
     dev, here = _here(dy)
     shape, dtype = dy.shape, dy.dtype
@@ -733,7 +748,7 @@ def orthros_rotate_backward(dy, x, positions, steps, *, layout="half", amplitude
         ga, gs, xa, xs, _index("positions", positions, dev, n), _block("alpha", alpha, dev, torch.float32, (H, d)), st, rot,
         _rope_layout(layout), amplitude, n, H, d, _dtype(dy), oa, os_, _block("d_alpha", da, dev, torch.float32, (H, d)),
         _block("d_beta", db, dev, torch.float32, (H, d)), _addr(workspace, dev),
-        workspace.numel() if workspace is not None else 0, here if stream is None else _stream(stream))
+        workspace.numel() if workspace is not None else 0, here)
     _raise_if(rc, lib)
     return dx, da, db
 
@@ -747,6 +762,12 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     d] (or None) and q_out [n_out, Hq, d] are rotated. Returns (q_rot or None,
     q_out_rot or None); k_cache / v_cache are updated in place.
     """
+    if stream is not None:
+        with _on(stream):
+            return orthros_rotate_append(
+                q, k_new, v_new, k_cache, v_cache, block_table, token_seq, token_pos, steps, layout=layout,
+                amplitude=amplitude, q_out=q_out, out_positions=out_positions, alpha_base=alpha_base, beta_base=beta_base,
+                alpha_out=alpha_out, beta_out=beta_out, out=out, workspace=workspace)
     lib = _lib or load_library()
     dev, here = _here(k_cache)
     dtype = k_new.dtype
@@ -779,7 +800,7 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
         _addr(q_rot, dev), _addr(q_out_rot, dev),
         _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
         _index("block_table", block_table, dev, B * max_pages), B, max_pages, page_size, num_pages, _addr(workspace, dev),
-        workspace.numel(), here if stream is None else _stream(stream))
+        workspace.numel(), here)
     _raise_if(rc, lib)
     return q_rot, q_out_rot
 
@@ -798,6 +819,10 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     q_indptr and kv_lens are int32 tensors on the GPU. max_new bounds the new
     tokens of a sequence (default n). Returns (o [n, Hq, d], lse [n, Hq]).
     """
+    if stream is not None:
+        with _on(stream):
+            return orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table, window, scale,
+                                           max_new=max_new, out=out, workspace=workspace)
     lib = _lib or load_library()
     dev, here = _here(q)
     shape, dtype = q.shape, q.dtype
@@ -823,7 +848,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
         _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq, Hkv, d, window,
         d ** -0.5 if scale is None else scale, _dtype(q), max_pages, page_size, num_pages,
         oa, la, _addr(workspace, dev),
-        workspace.numel(), here if stream is None else _stream(stream))
+        workspace.numel(), here)
     _raise_if(rc, lib)
     return o, lse
 

@@ -43,10 +43,10 @@
 // of o itself.
 //
 // Bound and measured (GQA 32/8, d = 128): decoding by HBM, 32 sequences over 16K-32K
-// keys in 486 us, 6.5 TB/s, 96 % of the measured copy rate; chunks by the softmax that
+// keys in 482 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that
 // has to run beside the products, 2 x 4000 tokens over 24K keys at 1484 TFLOP/s (76 %
 // of the measured bf16 rate; 1375 once the power limit lowers the clock), 2048
-// tokens at window 4096 in 120 us, 11 of them the merge.
+// tokens at window 4096 in 117 us, 11 of them the merge.
 //
 // Keys outside the sequence's length or before every row's window are never
 // read into a result: their copy boxes are skipped (zero fill), their logits

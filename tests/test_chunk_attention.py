@@ -370,3 +370,21 @@ def test_graph_replays_growing_lengths_and_side_stream():
         side = step()
     s.synchronize()
     assert torch.equal(side[0], out[0]) and torch.equal(side[1], out[1])
+
+
+@pytest.mark.gpu
+def test_stream_argument_owns_what_the_call_allocates():
+    """Outputs of a call on another stream are not taken from memory that the current stream still writes."""
+    w = make([1, 30], [1000, 700], 8, 2, 128, 64, 1 << 20, seed=12)
+    t = [w[k].cuda() for k in ("q", "indptr", "lens", "kc", "vc", "bt")]
+    want = [x.clone() for x in ola.orthros_chunk_attention(*t, 1 << 20, max_new=30)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # the current stream is behind, with writes to what it has freed
+    stale = [torch.empty_like(x) for x in want for _ in range(3)]
+    for x in stale:
+        x.fill_(float("nan"))
+    del x, stale
+    got = ola.orthros_chunk_attention(*t, 1 << 20, max_new=30, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

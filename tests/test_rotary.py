@@ -453,3 +453,34 @@ def test_graph_and_side_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(list(out) + [kg, vg], want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_argument_owns_what_the_call_allocates(handle):
+    """Outputs of a call on another stream are not taken from memory that the current stream still writes."""
+    bt, kc, vc, seq, pos, packed = make_append(torch.bfloat16, 2, [4, 9], [2, 60], 8, 2, 128, 16, seed=2)
+    _, al, be, _ = make(1, 8, 128, torch.float32, seed=1)
+    steps = ola.orthros_rotary_steps(frequencies(128)).cuda()
+    dev, al, be, bt, seq, pos = packed.cuda(), al.cuda(), be.cuda(), bt.cuda(), seq.cuda(), pos.cuda()
+    kg, vg = kc.cuda(), vc.cuda()
+    q = dev[:, :8]
+    dy = torch.ones_like(q)
+
+    def step(**kw):
+        return (ola.orthros_rotate(q, pos, steps, alpha=al, beta=be, **kw),
+                *ola.orthros_rotate_backward(dy, q, pos, steps, alpha=al, **kw),
+                ola.orthros_rotate_append(q, dev[:, 8:10], dev[:, 10:], kg, vg, bt, seq, pos, steps, alpha_base=al,
+                                          beta_base=be, **kw)[0])
+
+    want = [t.clone() for t in step()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # the current stream is behind, with writes to what it has freed
+    stale = [torch.empty_like(t) for t in want for _ in range(3)]
+    for t in stale:
+        t.fill_(float("nan"))
+    del t, stale
+    got = step(stream=s.cuda_stream if handle else s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
