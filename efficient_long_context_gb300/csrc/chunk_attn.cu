@@ -46,7 +46,7 @@
 // keys in 482 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that
 // has to run beside the products, 2 x 4000 tokens over 24K keys at 1484 TFLOP/s (76 %
 // of the measured bf16 rate; 1375 once the power limit lowers the clock), 2048
-// tokens at window 4096 in 117 us, 11 of them the merge.
+// tokens at window 4096 in 112 us, 5 of them the merge.
 //
 // Keys outside the sequence's length or before every row's window are never
 // read into a result: their copy boxes are skipped (zero fill), their logits
@@ -1136,15 +1136,19 @@ __global__ void __launch_bounds__(kBound, 1)
 // ---------------------------------------------------------------------------
 // Merge of the units that a share's border cut: o = sum_k w_k o_k / sum_k w_k l_k with
 // w_k = exp(scale (m_k - max m)), the parts in their order with a running maximum.
-// A warp joins kRowsW rows; kParts parts of each are loaded at once, outputs beside
-// their maxima and sums, so that a row costs one trip to L2 rather than two.
+// kLanes lanes join a row, kParts parts of it loaded at once, outputs beside their
+// maxima and sums, so that a row costs one trip to L2 rather than two. Many rows take
+// few lanes each (addresses and weights cost every lane the same, and a warp per row
+// was bound by its instructions: 11 us of the 2048-token call instead of 5), few rows
+// many: 8 parts of a row in flight.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8, kMergeBlocks = 8;  // blocks of a unit
+constexpr int kMergeBlocks = 16;  // blocks of a unit, at most
 
-template <int D, int kRowsW, int kParts>
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
+template <int D, int kLanes, int kParts, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+    constexpr int V = D / (4 * kLanes);  // a lane's channels: 4 kLanes i + 4 lane .. + 3, i < V
+    constexpr int kRowsW = 32 / kLanes;
+    const int lane = threadIdx.x % kLanes;
     const int g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ChunkHead hd = p.heads[blockIdx.x];
@@ -1154,89 +1158,83 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
         if (threadIdx.x == 0) all = p.direct ? 0u : p.plan->flags;
         __syncthreads();
         uint32_t f = 0;
-        for (int i = threadIdx.x; i < (int)gridDim.x; i += kMergeWarps * 32) f |= p.heads[i].flags;
+        for (int i = threadIdx.x; i < (int)gridDim.x; i += kWarps * 32) f |= p.heads[i].flags;
         if (f) atomicOr(&all, f);
         __syncthreads();
         if (threadIdx.x == 0) *p.status = all;
     }
     if (hd.n_parts == 0) return;
     const float c2 = p.scale_log2;
-    // rows of the unit, slot-major: the blocks of a unit stride over them
-    for (int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kRowsW; r0 < p.slots_cap * p.rows_cap;
-         r0 += gridDim.y * kMergeWarps * kRowsW) {
-    int slot[kRowsW], row[kRowsW];
+    const int cap = p.slots_cap * p.rows_cap;  // rows of a partial, slot-major
+    for (int r = blockIdx.y * kWarps * kRowsW + threadIdx.x / kLanes; r < cap; r += gridDim.y * kWarps * kRowsW) {
+        const int slot = r / p.rows_cap, row = r % p.rows_cap;
+        if (row >= min(p.tile_tokens, hd.cnt - slot * p.tile_tokens) * g) continue;  // no token stands there
+        float M = -INFINITY, L = 0.f;
+        float4 acc[V];
 #pragma unroll
-    for (int i = 0; i < kRowsW; ++i) {
-        slot[i] = (r0 + i) / p.rows_cap;
-        row[i] = (r0 + i) % p.rows_cap;
-    }
-    bool live[kRowsW];  // a token stands there
-    float M[kRowsW], L[kRowsW], acc[kRowsW][E];
-#pragma unroll
-    for (int i = 0; i < kRowsW; ++i) {
-        live[i] = slot[i] < p.slots_cap && row[i] < min(p.tile_tokens, hd.cnt - slot[i] * p.tile_tokens) * g;
-        M[i] = -INFINITY;
-        L[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
-    }
-    for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
-        float2 ml[kParts][kRowsW];
-        float x[kParts][kRowsW][E];
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-#pragma unroll
-            for (int i = 0; i < kRowsW; ++i) {
-                ml[k][i] = make_float2(-INFINITY, 0.f);
-                if (!live[i] || k0 + k >= hd.n_parts) continue;
-                // part k: the head's own (second) partial, then the first partial of the lane's next CTAs
-                const long long id = k0 + k == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + (long long)(k0 + k) * p.lanes);
-                const long long at = (id * p.slots_cap + slot[i]) * p.rows_cap + row[i];
-                ml[k][i] = p.part_ml[at];
-                const float *src = p.part_o + at * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src);
-                    x[k][i][0] = f.x, x[k][i][1] = f.y, x[k][i][2] = f.z, x[k][i][3] = f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(src);
-                    x[k][i][0] = f.x, x[k][i][1] = f.y;
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < kRowsW; ++i) {
-            float m = M[i];
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k][i].x);
-            const float mb = m == -INFINITY ? 0.f : m * c2;
-            const float w0 = ex2(M[i] * c2 - mb);
-            M[i] = m;
-            L[i] *= w0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[i][e] *= w0;
+        for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
+            float2 ml[kParts];
+            float4 x[kParts][V];
 #pragma unroll
             for (int k = 0; k < kParts; ++k) {
-                if (ml[k][i].x == -INFINITY) {  // no finite logit: no output, and a sum of 0 or NaN
-                    L[i] += ml[k][i].y;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (k0 + k >= hd.n_parts) continue;
+                // part k: the head's own (second) partial, then the first partial of the lane's next CTAs
+                const int id = k0 + k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + (k0 + k) * p.lanes);
+                const long long at = (long long)id * cap + r;
+                ml[k] = p.part_ml[at];
+                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at * D) + lane;
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[k][i] = src[i * kLanes];
+            }
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k].x);
+            const float mb = m == -INFINITY ? 0.f : m * c2;
+            const float w0 = ex2(M * c2 - mb);
+            M = m;
+            L *= w0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i].x *= w0, acc[i].y *= w0, acc[i].z *= w0, acc[i].w *= w0;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (ml[k].x == -INFINITY) {  // no finite logit: no output, and a sum of 0 or NaN
+                    L += ml[k].y;
                     continue;
                 }
-                const float w = ex2(ml[k][i].x * c2 - mb);
-                L[i] = fmaf(w, ml[k][i].y, L[i]);
+                const float w = ex2(ml[k].x * c2 - mb);
+                L = fmaf(w, ml[k].y, L);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[i][e] = fmaf(w, x[k][i][e], acc[i][e]);
+                for (int i = 0; i < V; ++i) {
+                    acc[i].x = fmaf(w, x[k][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, x[k][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, x[k][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, x[k][i].w, acc[i].w);
+                }
             }
         }
-    }
+        const float inv = L > 0.f ? 1.f / L : L;  // a NaN sum stays
+        const long long out = ((long long)hd.tok0 + slot * p.tile_tokens + row / g) * p.Hq + hd.kv * g + row % g;
+        uint2 *dst = reinterpret_cast<uint2 *>(p.o + out * D) + lane;
 #pragma unroll
-    for (int i = 0; i < kRowsW; ++i) {
-        if (!live[i]) continue;
-        const float inv = L[i] > 0.f ? 1.f / L[i] : L[i];  // a NaN sum stays
-        const long long out = ((long long)hd.tok0 + slot[i] * p.tile_tokens + row[i] / g) * p.Hq + hd.kv * g + row[i] % g;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + out * D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[i][e] * inv, acc[i][e + 1] * inv);
-        if (lane == 0 && p.lse) p.lse[out] = M[i] * p.scale + logf(L[i]);
+        for (int i = 0; i < V; ++i)
+            dst[i * kLanes] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+        if (lane == 0 && p.lse) p.lse[out] = M * p.scale + logf(L);
     }
-    }
+}
+
+template <int D, int kLanes, int kParts, int kWarps>
+cudaError_t launch_merge(const ChunkParams &p, cudaLaunchAttribute *attr, cudaStream_t stream) {
+    constexpr int kRowsB = kWarps * (32 / kLanes);
+    const int blocks = (p.slots_cap * p.rows_cap + kRowsB - 1) / kRowsB;
+    cudaLaunchConfig_t mc = {};
+    mc.gridDim = dim3(p.lanes * p.per_lane, blocks < kMergeBlocks ? blocks : kMergeBlocks);
+    mc.blockDim = dim3(kWarps * 32);
+    mc.stream = stream;
+    mc.attrs = attr;
+    mc.numAttrs = 1;
+    return cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, kLanes, kParts, kWarps>, p);
 }
 
 template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
@@ -1268,18 +1266,9 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
         ProfScope ps("chunk_attn", stream);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;
     }
-    const int rows = p.slots_cap * p.rows_cap;
-    const int per_warp = rows <= kMergeWarps ? 1 : 2;
-    cudaLaunchConfig_t mc = {};
-    const int row_blocks = (rows + kMergeWarps * per_warp - 1) / (kMergeWarps * per_warp);
-    mc.gridDim = dim3(p.lanes * p.per_lane, row_blocks < kMergeBlocks ? row_blocks : kMergeBlocks);
-    mc.blockDim = dim3(kMergeWarps * 32);
-    mc.stream = stream;
-    mc.attrs = attr;
-    mc.numAttrs = 1;
     ProfScope ps("chunk_merge", stream);
-    if (cudaError_t e = per_warp == 1 ? cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, 1, 8>, p)
-                                      : cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, 2, 3>, p);
+    const int rows = p.slots_cap * p.rows_cap;
+    if (cudaError_t e = rows <= 8 ? launch_merge<D, D / 4, 8, 8>(p, attr, stream) : launch_merge<D, 8, 2, 4>(p, attr, stream);
         e != cudaSuccess)
         return e;
     return cudaGetLastError();
