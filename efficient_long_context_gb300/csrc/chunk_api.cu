@@ -119,6 +119,7 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
     p.page_size = page_size;
     p.num_pages = num_pages;
     p.tile_tokens = L.tile_tokens;
+    p.g_inv = 65536 / (Hq / Hkv) + 1;
     // the largest copy box of whole 8-row swizzle atoms that never crosses a page
     p.box = 128;
     while (page_size % p.box != 0) p.box /= 2;

@@ -43,10 +43,10 @@
 // of o itself.
 //
 // Bound and measured (GQA 32/8, d = 128): decoding by HBM, 32 sequences over 16K-32K
-// keys in 482 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that
+// keys in 480 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that
 // has to run beside the products, 2 x 4000 tokens over 24K keys at 1484 TFLOP/s (76 %
 // of the measured bf16 rate; 1375 once the power limit lowers the clock), 2048
-// tokens at window 4096 in 112 us, 5 of them the merge.
+// tokens at window 4096 in 110 us, 5 of them the merge.
 //
 // Keys outside the sequence's length or before every row's window are never
 // read into a result: their copy boxes are skipped (zero fill), their logits
@@ -181,20 +181,27 @@ template <int D> __device__ __forceinline__ uint32_t kv_offset(int row, int c) {
     return (row >> 3) * (D * 16) + (c >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
 
+// Token of a row within its tile: row / g for rows and groups up to 128.
+__device__ __forceinline__ int row_token(const ChunkParams &p, int row) { return row * p.g_inv >> 16; }
+
 // Key tiles a run of tokens at positions [first, last] sees.
 __device__ __forceinline__ void key_tiles(int first, int last, int window, int &lo, int &hi) {
     lo = max(0, first - window + 1) / kKeys;
     hi = last / kKeys;
 }
 
-// New tokens of sequence b (first row of q, cached tokens), or 0 when there are
-// none or its lengths are impossible (wrong).
-__device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0, int &len, bool &wrong) {
-    tok0 = p.q_indptr[b];
-    const int nb = p.q_indptr[b + 1] - tok0;
-    len = p.kv_lens[b];
+// New tokens of a sequence that has nb of them among len in the cache, or 0 when there
+// are none or its lengths are impossible (wrong).
+__device__ __forceinline__ int new_tokens(const ChunkParams &p, int nb, int len, bool &wrong) {
     wrong = nb > 0 && (nb > p.max_new || len < nb || (long long)len > (long long)p.max_pages * p.page_size);
     return wrong ? 0 : nb;
+}
+
+// The same for sequence b: its first row of q and cached tokens.
+__device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0, int &len, bool &wrong) {
+    tok0 = p.q_indptr[b];
+    len = p.kv_lens[b];
+    return new_tokens(p, p.q_indptr[b + 1] - tok0, len, wrong);
 }
 
 // The unit that begins at token i of a sequence's nb (i < nb).
@@ -425,6 +432,13 @@ __global__ void __launch_bounds__(kBound, 1)
         tmem_alloc(&mt.tmem_base, 512);
         tmem_relinquish();
     }
+    // lengths of the sequence that this lane of the copy warp lists (no plan: no launch to wait for)
+    int tok0 = 0, tok1 = 0, len = 0, tok_first = 0, tok_last = p.n;
+    if (warp == kCopyWarp && p.direct) {
+        const int b = p.B == 1 ? 0 : lane;
+        if (b < p.B) tok0 = p.q_indptr[b], tok1 = p.q_indptr[b + 1], len = p.kv_lens[b];
+        tok_first = p.q_indptr[0], tok_last = p.q_indptr[p.B];
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -443,14 +457,9 @@ __global__ void __launch_bounds__(kBound, 1)
             const int ut = 2 * tt;
             const bool one = p.B == 1;  // lane = unit of the sequence, else lane = sequence
             const int b = one ? 0 : lane;
-            int tok0 = 0, len = 0, nb = 0;
-            bool wrong = false, order = true;
-            if (b < p.B) {
-                nb = new_tokens(p, b, tok0, len, wrong);
-                order = p.q_indptr[b + 1] >= tok0;
-            }
-            if (lane == 0) order = order && p.q_indptr[0] == 0 && p.q_indptr[p.B] == p.n;
-            order = __all_sync(0xffffffffu, order);
+            bool wrong;
+            const int nb = new_tokens(p, tok1 - tok0, len, wrong);
+            const bool order = __all_sync(0xffffffffu, tok1 >= tok0 && tok_first == 0 && tok_last == p.n);
             if (!order || __any_sync(0xffffffffu, wrong)) {
                 // impossible lengths: NaN for their rows, or for all rows when no token's sequence is known
                 if (lane == 0 && blockIdx.x == 0) set_status(status, ORTHROS_DEV_BAD_LENGTH);
@@ -509,11 +518,24 @@ __global__ void __launch_bounds__(kBound, 1)
         if (pl.tiles > 0) {
             const Shares sh = shares_of(p, pl);
             if (j < sh.eff) {
-                // both borders of the share, moved; the unit the first one ends up in
-                long long x = sh.border(j), x1 = sh.border(j + 1);
-                int kvo = 0;  // which of the lane's kv heads (few: counted, not divided)
-                while (x >= (kvo + 1) * pl.tiles) ++kvo;
-                int u = find(x - kvo * pl.tiles);
+                // both borders of the share, moved, the end first (one body for both: this code runs
+                // once, from a cold instruction cache); the unit that it begins with
+                long long x = 0, x1 = 0;
+                int kvo = 0, u = 0;  // which of the lane's kv heads (few: counted, not divided), unit
+                bool past = false;
+#pragma unroll 1
+                for (int k = 1; k >= 0; --k) {
+                    x1 = x;
+                    x = sh.border(j + k);
+                    if (x >= sh.total) continue;  // the lane's end stays
+                    kvo = 0;
+                    while (x >= (kvo + 1) * pl.tiles) ++kvo;
+                    u = find(x - kvo * pl.tiles);
+                    const ChunkUnit e = get_unit(u);
+                    const long long u0 = kvo * pl.tiles + e.start;
+                    x = sh.moved(x, u0, e.n_kt);
+                    past = x == u0 + e.n_kt;
+                }
                 auto next_unit = [&]() {  // (a lane without a unit is passed over)
                     do {
                         if (++u == pl.units) {
@@ -522,18 +544,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         }
                     } while (p.direct && __shfl_sync(0xffffffffu, own.n_kt, u) == 0);
                 };
-                if (x1 < sh.total) {
-                    long long base = kvo * pl.tiles;
-                    while (x1 >= base + pl.tiles) base += pl.tiles;
-                    const ChunkUnit e = get_unit(find(x1 - base));
-                    x1 = sh.moved(x1, base + e.start, e.n_kt);
-                }
-                {
-                    const ChunkUnit e = get_unit(u);
-                    const long long u0 = kvo * pl.tiles + e.start;
-                    x = sh.moved(x, u0, e.n_kt);
-                    if (x == u0 + e.n_kt) next_unit();
-                }
+                if (past) next_unit();
                 while (x < x1 && alive) {
                     const ChunkUnit un = get_unit(u);
                     const int a = (int)(x - kvo * pl.tiles - un.start);
@@ -595,6 +606,8 @@ __global__ void __launch_bounds__(kBound, 1)
                     const int box = p.box;
                     const int n_box = box ? kKeys / box : 0;
                     // first token row of this lane's box of a tile (TMA), or oob; bad: page id outside the pool
+                    // (The page is awaited here, a tile before its use: awaited at its use, decoding took 1 %
+                    // longer, its copies less in step with those of the other heads.)
                     auto look = [&](int kt, int &bad) -> int {
                         bad = 0;
                         if (lane >= n_box) return oob;
@@ -925,7 +938,7 @@ __global__ void __launch_bounds__(kBound, 1)
             const bool mine = row < n_tok * g;                       // a real row
             const bool idle = (warp & 3) * 32 >= n_tok * g;          // no real row in this warp
             const int t_first = sg.pos0 + c0, t_last = t_first + n_tok - 1;
-            const int t_row = mine ? t_first + row / g : t_last;
+            const int t_row = mine ? t_first + row_token(p, row) : t_last;
             const int lo_row = max(0, t_row - p.window + 1);
             const int lo_max = max(0, t_last - p.window + 1);
             const int it0 = sg.pair ? sg.lo[s] : s, step = sg.pair ? 1 : 2, it1 = sg.pair ? sg.hi[s] : sg.nkt - 1;
@@ -1058,8 +1071,9 @@ __global__ void __launch_bounds__(kBound, 1)
             }
             if (!idle) {
                 tc_fence_after();
-                const long long tok = sg.tok0 + c0 + row / g;
-                const int h = sg.kv * g + row % g;
+                const int rt = row_token(p, row);
+                const long long tok = sg.tok0 + c0 + rt;
+                const int h = sg.kv * g + row - rt * g;
                 const uint32_t t_a = t_o + (sg.pair ? s * 128 : 0);
                 const bool fin = sg.partial < 0;
                 const long long out = tok * p.Hq + h;  // row of o, or of the partials
@@ -1215,7 +1229,8 @@ __global__ void __launch_bounds__(kWarps * 32) chunk_merge_kernel(const ChunkPar
             }
         }
         const float inv = L > 0.f ? 1.f / L : L;  // a NaN sum stays
-        const long long out = ((long long)hd.tok0 + slot * p.tile_tokens + row / g) * p.Hq + hd.kv * g + row % g;
+        const int rt = row_token(p, row);
+        const long long out = ((long long)hd.tok0 + slot * p.tile_tokens + rt) * p.Hq + hd.kv * g + row - rt * g;
         uint2 *dst = reinterpret_cast<uint2 *>(p.o + out * D) + lane;
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -358,6 +358,7 @@ struct ChunkParams {
     const int32_t *block_table;      // [B, max_pages]
     int B, n, max_new, Hq, Hkv, window, max_pages, page_size, num_pages;
     int tile_tokens;                 // tokens of a 128-row tile: 128 / (Hq / Hkv)
+    int g_inv;                       // 65536 / (Hq / Hkv) + 1: row / g = row * g_inv >> 16
     int box;                         // tokens of a K/V copy box, a divisor of page_size (0: rows are gathered)
     int lanes, per_lane;             // CTAs: lanes x per_lane; a lane serves Hkv / lanes kv heads
     int rows_cap, slots_cap;         // rows and slots of a partial
