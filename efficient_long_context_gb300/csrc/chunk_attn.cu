@@ -707,9 +707,13 @@ __global__ void __launch_bounds__(kBound, 1)
         if (head_n > 0) {
             // the CTAs whose share begins inside the unit hold its other parts
             const Shares sh = shares_of(p, pl);
-            int k = j + 1;
-            while (k < sh.eff && sh.moved(sh.border(k), head_u0, head_n) < head_u0 + head_n) ++k;
-            head.n_parts = k - j;
+            head.n_parts = 1;
+            for (int k0 = j + 1; k0 < sh.eff; k0 += 32) {  // (a lane looks at one border)
+                const int k = k0 + lane;
+                const unsigned in = __ballot_sync(0xffffffffu, k < sh.eff && sh.moved(sh.border(k), head_u0, head_n) < head_u0 + head_n);
+                head.n_parts += __popc(in);
+                if (in != 0xffffffffu) break;
+            }
         }
         if (lane == 0) {
             ChunkHead &to = p.heads[blockIdx.x];
