@@ -1153,107 +1153,157 @@ __global__ void __launch_bounds__(kBound, 1)
 
 // ---------------------------------------------------------------------------
 // Merge of the units that a share's border cut: o = sum_k w_k o_k / sum_k w_k l_k with
-// w_k = exp(scale (m_k - max m)), the parts in their order with a running maximum.
-// kLanes lanes join a row, kParts parts of it loaded at once, outputs beside their
-// maxima and sums, so that a row costs one trip to L2 rather than two. Many rows take
-// few lanes each (addresses and weights cost every lane the same, and a warp per row
-// was bound by its instructions: 11 us of the 2048-token call instead of 5), few rows
-// many: 8 parts of a row in flight.
+// w_k = exp(scale (m_k - max m)), the parts in a fixed order with a running maximum.
+// Many rows: 8 lanes join a row (addresses and weights cost every lane the same, and a
+// warp per row was bound by its instructions: 11 us of the 2048-token call instead of
+// 5). Few rows may have many parts: a block joins a row, its warps every fourth part
+// each, and adds their results up (a warp that walked the parts alone took 7 us longer
+// for the 152 of one token over a single kv head).
 // ---------------------------------------------------------------------------
-constexpr int kMergeBlocks = 16;  // blocks of a unit, at most
+constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 32;    // a block per row up to so many rows of a partial
+constexpr int kMergeBlocks = 16;  // blocks of a unit beyond
 
-template <int D, int kLanes, int kParts, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32) chunk_merge_kernel(const ChunkParams p) {
-    constexpr int V = D / (4 * kLanes);  // a lane's channels: 4 kLanes i + 4 lane .. + 3, i < V
-    constexpr int kRowsW = 32 / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const int g = p.Hq / p.Hkv;
+// Running joint of parts of one row: kLanes lanes, lane l with channels 4 kLanes i + 4 l .. + 3, i < V.
+template <int V> struct Joint {
+    float M, L;
+    float4 acc[V];
+    __device__ __forceinline__ void clear() {
+        M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    template <int kParts> __device__ __forceinline__ void add(const float2 (&ml)[kParts], const float4 (&x)[kParts][V], float c2) {
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k].x);
+        const float mb = m == -INFINITY ? 0.f : m * c2;
+        const float w0 = ex2(M * c2 - mb);
+        M = m;
+        L *= w0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i].x *= w0, acc[i].y *= w0, acc[i].z *= w0, acc[i].w *= w0;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            if (ml[k].x == -INFINITY) {  // no finite logit: no output, and a sum of 0 or NaN
+                L += ml[k].y;
+                continue;
+            }
+            const float w = ex2(ml[k].x * c2 - mb);
+            L = fmaf(w, ml[k].y, L);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                acc[i].x = fmaf(w, x[k][i].x, acc[i].x);
+                acc[i].y = fmaf(w, x[k][i].y, acc[i].y);
+                acc[i].z = fmaf(w, x[k][i].z, acc[i].z);
+                acc[i].w = fmaf(w, x[k][i].w, acc[i].w);
+            }
+        }
+    }
+};
+
+template <int D, bool kRowBlocks>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+    const int tid = threadIdx.x, g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ChunkHead hd = p.heads[blockIdx.x];
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         // the call's status word, from the CTAs' (and the plan's)
         __shared__ uint32_t all;
-        if (threadIdx.x == 0) all = p.direct ? 0u : p.plan->flags;
+        if (tid == 0) all = p.direct ? 0u : p.plan->flags;
         __syncthreads();
         uint32_t f = 0;
-        for (int i = threadIdx.x; i < (int)gridDim.x; i += kWarps * 32) f |= p.heads[i].flags;
+        for (int i = tid; i < (int)gridDim.x; i += kMergeWarps * 32) f |= p.heads[i].flags;
         if (f) atomicOr(&all, f);
         __syncthreads();
-        if (threadIdx.x == 0) *p.status = all;
+        if (tid == 0) *p.status = all;
     }
     if (hd.n_parts == 0) return;
     const float c2 = p.scale_log2;
     const int cap = p.slots_cap * p.rows_cap;  // rows of a partial, slot-major
-    for (int r = blockIdx.y * kWarps * kRowsW + threadIdx.x / kLanes; r < cap; r += gridDim.y * kWarps * kRowsW) {
+    // row r's token and head: its row of o, or -1 when no token stands there
+    auto out_row = [&](int r) -> long long {
         const int slot = r / p.rows_cap, row = r % p.rows_cap;
-        if (row >= min(p.tile_tokens, hd.cnt - slot * p.tile_tokens) * g) continue;  // no token stands there
-        float M = -INFINITY, L = 0.f;
-        float4 acc[V];
+        if (row >= min(p.tile_tokens, hd.cnt - slot * p.tile_tokens) * g) return -1;
+        const int rt = row_token(p, row);
+        return ((long long)hd.tok0 + slot * p.tile_tokens + rt) * p.Hq + hd.kv * g + row - rt * g;
+    };
+    // row r of part k: the head's own (second) partial, then the first partial of the lane's next CTAs
+    auto part_row = [&](int k, int r) -> long long {
+        const int id = k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k * p.lanes);
+        return (long long)id * cap + r;
+    };
+    auto store = [&](long long out, int chunk, const float4 &a, float inv) {
+        reinterpret_cast<uint2 *>(p.o + out * D)[chunk] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    };
+    if constexpr (!kRowBlocks) {
+        constexpr int kLanes = 8, V = D / (4 * kLanes), kParts = 2;
+        const int lane = tid % kLanes;
+        for (int r = (blockIdx.y * kMergeWarps * 32 + tid) / kLanes; r < cap; r += gridDim.y * kMergeWarps * (32 / kLanes)) {
+            const long long out = out_row(r);
+            if (out < 0) continue;
+            Joint<V> jt;
+            jt.clear();
+            for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
+                float2 ml[kParts];
+                float4 x[kParts][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
-            float2 ml[kParts];
-            float4 x[kParts][V];
+                for (int k = 0; k < kParts; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    if (k0 + k >= hd.n_parts) continue;
+                    const long long at = part_row(k0 + k, r);
+                    ml[k] = p.part_ml[at];
+                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at * D) + lane;
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
-                if (k0 + k >= hd.n_parts) continue;
-                // part k: the head's own (second) partial, then the first partial of the lane's next CTAs
-                const int id = k0 + k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + (k0 + k) * p.lanes);
-                const long long at = (long long)id * cap + r;
-                ml[k] = p.part_ml[at];
-                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at * D) + lane;
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[k][i] = src[i * kLanes];
+                    for (int i = 0; i < V; ++i) x[k][i] = src[i * kLanes];
+                }
+                jt.add(ml, x, c2);
             }
-            float m = M;
+            const float inv = jt.L > 0.f ? 1.f / jt.L : jt.L;  // a NaN sum stays
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k].x);
-            const float mb = m == -INFINITY ? 0.f : m * c2;
-            const float w0 = ex2(M * c2 - mb);
-            M = m;
-            L *= w0;
+            for (int i = 0; i < V; ++i) store(out, lane + i * kLanes, jt.acc[i], inv);
+            if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
+        }
+    } else {
+        // a block per row: kLanes threads hold a row, kSub parts are walked side by side
+        constexpr int kLanes = D / 4, kSub = kMergeWarps * 32 / kLanes, kParts = 8;
+        __shared__ float2 sub_ml[kSub];
+        __shared__ float4 sub_x[kSub][kLanes];
+        const int lane = tid % kLanes, sub = tid / kLanes;
+        const int r = blockIdx.y;
+        const long long out = out_row(r);
+        if (out >= 0) {
+            Joint<1> jt;
+            jt.clear();
+            for (int k0 = sub; k0 < hd.n_parts; k0 += kSub * kParts) {
+                float2 ml[kParts];
+                float4 x[kParts][1];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i].x *= w0, acc[i].y *= w0, acc[i].z *= w0, acc[i].w *= w0;
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-                if (ml[k].x == -INFINITY) {  // no finite logit: no output, and a sum of 0 or NaN
-                    L += ml[k].y;
-                    continue;
+                for (int k = 0; k < kParts; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    if (k0 + k * kSub >= hd.n_parts) continue;
+                    const long long at = part_row(k0 + k * kSub, r);
+                    ml[k] = p.part_ml[at];
+                    x[k][0] = reinterpret_cast<const float4 *>(p.part_o + at * D)[lane];
                 }
-                const float w = ex2(ml[k].x * c2 - mb);
-                L = fmaf(w, ml[k].y, L);
+                jt.add(ml, x, c2);
+            }
+            if (lane == 0) sub_ml[sub] = make_float2(jt.M, jt.L);
+            sub_x[sub][lane] = jt.acc[0];
+            __syncthreads();
+            if (sub == 0) {
+                float2 ml[kSub];
+                float4 x[kSub][1];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    acc[i].x = fmaf(w, x[k][i].x, acc[i].x);
-                    acc[i].y = fmaf(w, x[k][i].y, acc[i].y);
-                    acc[i].z = fmaf(w, x[k][i].z, acc[i].z);
-                    acc[i].w = fmaf(w, x[k][i].w, acc[i].w);
-                }
+                for (int k = 0; k < kSub; ++k) ml[k] = sub_ml[k], x[k][0] = sub_x[k][lane];
+                jt.clear();
+                jt.add(ml, x, c2);
+                const float inv = jt.L > 0.f ? 1.f / jt.L : jt.L;
+                store(out, lane, jt.acc[0], inv);
+                if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
             }
         }
-        const float inv = L > 0.f ? 1.f / L : L;  // a NaN sum stays
-        const int rt = row_token(p, row);
-        const long long out = ((long long)hd.tok0 + slot * p.tile_tokens + rt) * p.Hq + hd.kv * g + row - rt * g;
-        uint2 *dst = reinterpret_cast<uint2 *>(p.o + out * D) + lane;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            dst[i * kLanes] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-        if (lane == 0 && p.lse) p.lse[out] = M * p.scale + logf(L);
     }
-}
-
-template <int D, int kLanes, int kParts, int kWarps>
-cudaError_t launch_merge(const ChunkParams &p, cudaLaunchAttribute *attr, cudaStream_t stream) {
-    constexpr int kRowsB = kWarps * (32 / kLanes);
-    const int blocks = (p.slots_cap * p.rows_cap + kRowsB - 1) / kRowsB;
-    cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3(p.lanes * p.per_lane, blocks < kMergeBlocks ? blocks : kMergeBlocks);
-    mc.blockDim = dim3(kWarps * 32);
-    mc.stream = stream;
-    mc.attrs = attr;
-    mc.numAttrs = 1;
-    return cudaLaunchKernelEx(&mc, chunk_merge_kernel<D, kLanes, kParts, kWarps>, p);
 }
 
 template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
@@ -1285,11 +1335,15 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
         ProfScope ps("chunk_attn", stream);
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;
     }
-    ProfScope ps("chunk_merge", stream);
     const int rows = p.slots_cap * p.rows_cap;
-    if (cudaError_t e = rows <= 8 ? launch_merge<D, D / 4, 8, 8>(p, attr, stream) : launch_merge<D, 8, 2, 4>(p, attr, stream);
-        e != cudaSuccess)
-        return e;
+    cudaLaunchConfig_t mc = {};
+    mc.gridDim = dim3(p.lanes * p.per_lane, rows <= kMergeRows ? rows : kMergeBlocks);
+    mc.blockDim = dim3(kMergeWarps * 32);
+    mc.stream = stream;
+    mc.attrs = attr;
+    mc.numAttrs = 1;
+    ProfScope ps("chunk_merge", stream);
+    if (cudaError_t e = cudaLaunchKernelEx(&mc, rows <= kMergeRows ? chunk_merge_kernel<D, true> : chunk_merge_kernel<D, false>, p); e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
