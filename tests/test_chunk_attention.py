@@ -388,3 +388,20 @@ def test_stream_argument_owns_what_the_call_allocates():
     got = ola.orthros_chunk_attention(*t, 1 << 20, max_new=30, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,new", [(8, 1, 128, 1), (8, 1, 64, 3), (32, 2, 128, 2), (6, 3, 64, 9), (16, 1, 128, 5),
+                                          (16, 1, 64, 40), (5, 5, 128, 1)])
+def test_long_units_of_few_heads(Hq, Hkv, d, new):
+    """One sequence whose keys many CTAs share: up to one part per SM to join for a row, NaN rows among them."""
+    w = make([new], [40003], Hq, Hkv, d, 64, 1 << 20, seed=18)
+    want = call(w)
+    check(want, plain(w, d ** -0.5))
+    q = w["q"].clone()
+    q[new - 1, 2] = float("nan")
+    o, lse = call(dict(w, q=q))
+    keep = torch.ones(new, Hq, dtype=torch.bool)
+    keep[new - 1, 2] = False
+    assert torch.equal(o[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
+    assert bool(torch.isnan(o[new - 1, 2]).all()) and bool(torch.isnan(lse[new - 1, 2]))
