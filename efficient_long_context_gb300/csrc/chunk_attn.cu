@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(kBound, 1)
                             fence_proxy_async_smem();
                             bad0 = __reduce_min_sync(0xffffffffu, bad0);
                             bad1 = __reduce_max_sync(0xffffffffu, bad1);
+                            __syncwarp();  // (the reductions order no memory: lane 0 arrives for every lane's rows)
                             if (lane == 0) {
                                 if (bad1) set_status(status, ORTHROS_DEV_BAD_PAGE);
                                 mt.bad[gi % kFlagRing] = bad1 ? (int)(bad0 << 8 | bad1) : 0;
