@@ -67,13 +67,15 @@ class RotaryLayer:
     # ---- training ------------------------------------------------------------
     def forward(self, q, k, v, out_indptr, out_positions):
         """q [B, T, Hq, d] (before the affines), k, v [B, T, Hkv, d]; output rows as in
-        orthros_prefill (their raw queries are q at their positions). Returns
-        ((o_base, o_out), saved for backward)."""
+        orthros_prefill (their raw queries are q at their positions). A position outside
+        [0, T) makes its output row NaN and has no gradient. Returns ((o_base, o_out), saved
+        for backward)."""
         B, T = q.shape[:2]
         ab, bb, ao, bo = self.affines
         pos = torch.arange(T, dtype=torch.int32, device=q.device).repeat(B)
         counts = torch.as_tensor(out_indptr, dtype=torch.int64).diff()
-        rows = torch.repeat_interleave(torch.arange(B), counts).to(q.device) * T + out_positions
+        # (the prefill judges the positions; here they only have to stay within their sequence)
+        rows = torch.repeat_interleave(torch.arange(B), counts).to(q.device) * T + out_positions.clamp(0, T - 1)
         qf, kf = q.flatten(0, 1), k.flatten(0, 1)
         q_sel = qf[rows]
         qr = ops.orthros_rotate(qf, pos, self.steps, alpha=ab, beta=bb, **self._rope()).view_as(q)
@@ -92,7 +94,9 @@ class RotaryLayer:
         dq, da, db = ops.orthros_rotate_backward(g["dq"].flatten(0, 1), qf, pos, self.steps, alpha=ab, **self._rope())
         dk, _, _ = ops.orthros_rotate_backward(g["dk"].flatten(0, 1), None, pos, self.steps, affine_grads=False,
                                                **self._rope())
-        dq_sel, da_out, db_out = ops.orthros_rotate_backward(g["dq_out"], q_sel, out_positions, self.steps, alpha=ao,
+        outside = (out_positions < 0) | (out_positions >= qr.shape[1])  # rows that read nothing
+        dq_out = g["dq_out"].masked_fill_(outside[:, None, None], 0)
+        dq_sel, da_out, db_out = ops.orthros_rotate_backward(dq_out, q_sel, out_positions, self.steps, alpha=ao,
                                                              **self._rope())
         dq = dq.float().index_add_(0, rows, dq_sel.float()).to(qf.dtype)
         return {"dq": dq.view_as(qr), "dk": dk.view_as(kr), "dv": g["dv"], "d_alpha_base": da, "d_beta_base": db,

@@ -112,3 +112,33 @@ def test_training_gradients_against_autograd(layout):
         floor = rms if n in "qkv" else rms * (B * T if n.endswith("base") else 5) ** 0.5
         err = float(((a - ref).abs() / (ref.pow(2).mean().sqrt() + ref.abs() + floor)).max())
         assert err <= 5e-2, (n, err)
+
+
+def test_output_positions_outside_their_sequence():
+    """A position outside [0, T) gives a NaN row and no gradient: the gradients are those of the other
+    rows alone, in its neighbours' sequences too."""
+    Hq, Hkv, d, T, B, window = 4, 2, 64, 90, 3, 30
+    layer, g = make_layer(Hq, Hkv, d, window, "half", seed=5)
+    q, k, v = (torch.randn(B, T, h, d, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv))
+    db = torch.randn(B, T, Hq, d, generator=g).bfloat16().cuda()
+    good = [(0, 10), (0, 89), (1, 10), (2, 50)]
+    do = torch.randn(len(good), Hq, d, generator=g).bfloat16().cuda()
+
+    def run(rows, do_rows):
+        indptr = np.concatenate([[0], np.cumsum([sum(r[0] == b for r in rows) for b in range(B)])]).astype(np.int32)
+        (ob, oo), saved = layer.forward(q, k, v, indptr, torch.tensor([r[1] for r in rows], dtype=torch.int32, device="cuda"))
+        return ob, oo, layer.backward(saved, db, do_rows)
+
+    ob, oo, want = run(good, do)
+    for where, bad in ((0, (0, -1)), (2, (0, T)), (4, (2, 1 << 30)), (2, (1, -(2 ** 31))), (3, (2, 2 ** 31 - 1))):
+        rows = good[:where] + [bad] + good[where:]
+        keep = [i for i in range(len(rows)) if i != where]
+        do_rows = torch.cat([do[:where], torch.full_like(do[:1], 100.0), do[where:]])
+        ob2, oo2, got = run(rows, do_rows)
+        assert torch.equal(ob2, ob) and float((oo2[keep].float() - oo.float()).abs().max()) <= 2e-2
+        assert bool(torch.isnan(oo2[where]).all())
+        for n in want:
+            # the same terms, each rounded to bf16 at most three times (2^-8 each) before the fp32 sums;
+            # the bad row's 100s would move every sum they enter by more than this
+            a, b = got[n].double(), want[n].double()
+            assert bool(((a - b).abs() <= 2.0 ** -6 * (b.abs() + b.abs().max())).all()), (bad, n)
