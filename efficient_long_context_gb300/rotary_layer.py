@@ -73,7 +73,7 @@ class RotaryLayer:
         B, T = q.shape[:2]
         ab, bb, ao, bo = self.affines
         pos = torch.arange(T, dtype=torch.int32, device=q.device).repeat(B)
-        counts = torch.as_tensor(out_indptr, dtype=torch.int64).diff()
+        counts = torch.as_tensor(out_indptr, dtype=torch.int64, device="cpu").diff()
         # (the prefill judges the positions; here they only have to stay within their sequence)
         rows = torch.repeat_interleave(torch.arange(B), counts).to(q.device) * T + out_positions.clamp(0, T - 1)
         qf, kf = q.flatten(0, 1), k.flatten(0, 1)

@@ -142,3 +142,16 @@ def test_output_positions_outside_their_sequence():
             # the bad row's 100s would move every sum they enter by more than this
             a, b = got[n].double(), want[n].double()
             assert bool(((a - b).abs() <= 2.0 ** -6 * (b.abs() + b.abs().max())).all()), (bad, n)
+
+
+def test_output_rows_counted_on_the_gpu():
+    """out_indptr may be a GPU tensor, as orthros_prefill takes it."""
+    layer, g = make_layer(4, 2, 64, 30, "half", seed=7)
+    q, k, v = (torch.randn(2, 50, h, 64, generator=g).bfloat16().cuda() for h in (4, 2, 2))
+    opos = torch.tensor([10, 49, 0], dtype=torch.int32, device="cuda")
+    host = layer.forward(q, k, v, np.array([0, 2, 3], dtype=np.int32), opos)
+    dev = layer.forward(q, k, v, torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda"), opos)
+    for a, b in zip(host[0], dev[0]):
+        assert torch.equal(a, b)
+    grads = [layer.backward(s, torch.ones_like(q), torch.ones_like(o[1])) for o, s in (host, dev)]
+    assert torch.equal(grads[0]["dv"], grads[1]["dv"])
