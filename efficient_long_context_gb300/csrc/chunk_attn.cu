@@ -190,6 +190,10 @@ __device__ __forceinline__ void key_tiles(int first, int last, int window, int &
     hi = last / kKeys;
 }
 
+// What a row's output is scaled by. Every row sees a key (its own), so a sum that is 0 had
+// only logits of -inf: such a row has no softmax and is NaN, as is one whose sum is.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.f / l : __int_as_float(0x7fc00000); }
+
 // New tokens of a sequence that has nb of them among len in the cache, or 0 when there
 // are none or its lengths are impossible (wrong).
 __device__ __forceinline__ int new_tokens(const ChunkParams &p, int nb, int len, bool &wrong) {
@@ -1084,7 +1088,7 @@ __global__ void __launch_bounds__(kBound, 1)
                 const long long out = tok * p.Hq + h;  // row of o, or of the partials
                 const long long at = ((long long)sg.partial * p.slots_cap + (sg.pair ? s : 0)) * p.rows_cap + row;
                 if (fin) {
-                    const float inv = l > 0.f ? 1.f / l : l;  // a NaN sum stays
+                    const float inv = inverse_sum(l);
                     w0 *= inv;
                     w1 *= inv;
                     if (mine && p.lse) p.lse[out] = m * p.scale + logf(l);
@@ -1260,7 +1264,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
                 }
                 jt.add(ml, x, c2);
             }
-            const float inv = jt.L > 0.f ? 1.f / jt.L : jt.L;  // a NaN sum stays
+            const float inv = inverse_sum(jt.L);
 #pragma unroll
             for (int i = 0; i < V; ++i) store(out, lane + i * kLanes, jt.acc[i], inv);
             if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
@@ -1299,7 +1303,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
                 for (int k = 0; k < kSub; ++k) ml[k] = sub_ml[k], x[k][0] = sub_x[k][lane];
                 jt.clear();
                 jt.add(ml, x, c2);
-                const float inv = jt.L > 0.f ? 1.f / jt.L : jt.L;
+                const float inv = inverse_sum(jt.L);
                 store(out, lane, jt.acc[0], inv);
                 if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
             }

@@ -599,7 +599,8 @@ ORTHROS_API size_t orthros_chunk_attention_workspace_size(int B, int n, int max_
  * every row is NaN; n_b > max_new, kv_lens[b] < n_b or past the block table
  * sets it for that sequence's rows. A page id outside [0, num_pages) sets
  * ORTHROS_DEV_BAD_PAGE and the rows that see its keys are NaN (as are those that
- * see only keys between two such pages closer than 128 tokens).
+ * see only keys between two such pages closer than 128 tokens). A row whose
+ * logits are all -inf (an infinite query) has no softmax: o is NaN, lse -inf.
  */
 ORTHROS_API orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, const int32_t *kv_lens,
                                                    const void *k_cache, const void *v_cache,

@@ -442,3 +442,31 @@ def test_gathered_rows_of_long_histories(page):
     for _ in range(5):
         again = call(w, max_new=70)
         assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,total,Hq,Hkv,d,page", [
+    ([1, 1, 1], [1, 5, 130], 8, 2, 128, 16),  # whole units
+    ([1], [40003], 8, 1, 128, 64),            # a cut unit of few rows: a block per row joins its parts
+    ([300], [5000], 32, 8, 64, 64),           # cut units of many rows
+    ([40, 200], [40, 900], 4, 4, 128, 12)])   # gathered pages
+def test_row_without_a_finite_logit_is_nan(new, total, Hq, Hkv, d, page):
+    """A query whose logits are all -inf (an infinite channel against keys of the other sign) has no
+    softmax: o is NaN, lse = log 0 = -inf, and no other row is touched."""
+    w = make(new, total, Hq, Hkv, d, page, 1 << 20, seed=20)
+    w["kc"][..., 7] = -w["kc"][..., 7].abs() - 0.125
+    for k in w["K"]:
+        k[..., 7] = -k[..., 7].abs() - 0.125
+    want = call(w, max_new=max(new))
+    check(want, plain(w, d ** -0.5))
+    n = sum(new)
+    q = w["q"].clone()
+    bad = [(0, 0), (n // 2, Hq - 1), (n - 1, 1)]
+    for i, h in bad:
+        q[i, h, 7] = float("inf")
+    o, lse = call(dict(w, q=q), max_new=max(new))
+    keep = torch.ones(n, Hq, dtype=torch.bool)
+    for i, h in bad:
+        keep[i, h] = False
+        assert bool(torch.isnan(o[i, h]).all()) and float(lse[i, h]) == -float("inf"), (i, h)
+    assert torch.equal(o[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
