@@ -21,6 +21,20 @@ import torch
 from . import _binding as ops
 
 
+def _add_rows(x, rows, y):
+    """x[rows[i]] += y[i] in place, in fp32 and rounded once per row of x. Rows may repeat: the y of a
+    row are summed in the order they stand in (an indexed add with atomics would take any order, and
+    through an fp32 copy of x it would move all of x for a few rows)."""
+    if rows.numel() == 0:
+        return
+    rows, order = torch.sort(rows, stable=True)
+    run = torch.zeros_like(rows)  # which run of equal rows an entry belongs to
+    run[1:] = (rows[1:] != rows[:-1]).cumsum(0)
+    total = torch.zeros(y.shape, dtype=torch.float32, device=y.device)
+    total.index_put_((run,), y[order].float(), accumulate=True)  # (sorts its indices, no atomics)
+    x[rows] = (x[rows].float() + total[run]).to(x.dtype)  # entries of a run write the same value
+
+
 @dataclasses.dataclass
 class RotaryLayer:
     """Weights and shape of the layer. `affines` are alpha_base, beta_base, alpha_out,
@@ -98,6 +112,6 @@ class RotaryLayer:
         dq_out = g["dq_out"].masked_fill_(outside[:, None, None], 0)
         dq_sel, da_out, db_out = ops.orthros_rotate_backward(dq_out, q_sel, out_positions, self.steps, alpha=ao,
                                                              **self._rope())
-        dq = dq.float().index_add_(0, rows, dq_sel.float()).to(qf.dtype)
+        _add_rows(dq, rows, dq_sel)
         return {"dq": dq.view_as(qr), "dk": dk.view_as(kr), "dv": g["dv"], "d_alpha_base": da, "d_beta_base": db,
                 "d_alpha_out": da_out, "d_beta_out": db_out}

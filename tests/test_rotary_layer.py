@@ -155,3 +155,28 @@ def test_output_rows_counted_on_the_gpu():
         assert torch.equal(a, b)
     grads = [layer.backward(s, torch.ones_like(q), torch.ones_like(o[1])) for o, s in (host, dev)]
     assert torch.equal(grads[0]["dv"], grads[1]["dv"])
+
+
+def test_repeated_output_positions_add_in_a_fixed_order():
+    """fp32, hundreds of output rows at one position: the same backward gives the same bits of dq, which
+    holds the sum of the rows' gradients (at most 500 fp32 additions of 2^-24 each)."""
+    Hq, Hkv, d, T, B, window = 4, 2, 64, 40, 2, 30
+    layer, g = make_layer(Hq, Hkv, d, window, "half", seed=6)
+    q, k, v = (torch.randn(B, T, h, d, generator=g).cuda() for h in (Hq, Hkv, Hkv))
+    pos = [7] * 400 + [39, 3] + [7] * 98 + [39] * 200 + [0]
+    indptr, opos = np.array([0, 500, 701], dtype=np.int32), torch.tensor(pos, dtype=torch.int32, device="cuda")
+    (ob, oo), saved = layer.forward(q, k, v, indptr, opos)
+    db, do = torch.randn(ob.shape, generator=g).cuda(), torch.randn(oo.shape, generator=g).cuda()
+    got = layer.backward(saved, db, do)["dq"]
+    for _ in range(5):
+        assert torch.equal(layer.backward(saved, db, do)["dq"], got)
+    qf, q_sel, _, tok, qr, kr, _, qo, _, _, out = saved
+    grads = ola.orthros_prefill_backward(qr, kr, v, *layer.identity, *layer.identity, indptr, opos, window, None, *out, db, do,
+                                         q_out=qo)
+    rope = dict(layout=layer.layout, amplitude=layer.amplitude)
+    base, _, _ = ola.orthros_rotate_backward(grads["dq"].flatten(0, 1), qf, tok, layer.steps, alpha=layer.affines[0], **rope)
+    sel, _, _ = ola.orthros_rotate_backward(grads["dq_out"], q_sel, opos, layer.steps, alpha=layer.affines[2], **rope)
+    rows = torch.repeat_interleave(torch.arange(B), torch.tensor([500, 201])).cuda() * T + opos
+    want = base.double().index_add_(0, rows, sel.double())
+    mag = base.double().abs().index_add_(0, rows, sel.double().abs())
+    assert bool(((got.flatten(0, 1).double() - want).abs() <= 500 * 2.0 ** -24 * mag).all())
