@@ -54,28 +54,55 @@ class RotaryLayer:
         dev = self.w_qkv.device
         self.steps = ops.orthros_rotary_steps(self.freq).to(dev)
         self.identity = (torch.ones(self.Hq, self.d, device=dev), torch.zeros(self.Hq, self.d, device=dev))
+        self._reports = []  # buffers that begin with a status word of the last step(), or forward() and backward()
 
     def _rope(self):
         return dict(layout=self.layout, amplitude=self.amplitude)
 
+    def check(self, stream=None):
+        """Synchronises `stream` (default: the current one) and returns (status, bits) of the last
+        step(), or of the last forward() with the backward() after it: the first status that is not
+        0 (orthros_check) and the ORTHROS_DEV_* bits of all its calls."""
+        found = [ops.orthros_check(w, stream) for w in self._reports]
+        bits = 0
+        for _, b in found:
+            bits |= b
+        return next((s for s, _ in found if s), 0), bits
+
     # ---- serving -------------------------------------------------------------
+    def step_workspaces(self, B, n_new, n_out, max_new, max_pages, page_size):
+        """Workspaces of step() for these sizes or smaller ones: projection, append, both attentions."""
+        sizes = [256, 256] + [ops.orthros_chunk_attention_workspace_size(B, n, m, self.Hq, self.Hkv, self.d, max_pages,
+                                                                        page_size, self.w_qkv.dtype)
+                              for n, m in ((n_new, max_new), (n_out, 1))]
+        return [torch.empty(max(s, 256), dtype=torch.uint8, device=self.w_qkv.device) for s in sizes]
+
     def step(self, x, n_new, k_cache, v_cache, block_table, token_seq, token_pos, new_indptr, kv_lens, out_indptr,
-             out_positions, max_new):
+             out_positions, max_new, workspaces=None):
         """One serving step.
 
         x [n_new + n_out, d_model]: the new tokens of the batch (rows new_indptr[b] ..
         new_indptr[b+1] belong to sequence b), then at most one output-stream token per
         sequence, at its last position (out_indptr, out_positions). kv_lens counts the
-        cached tokens with the new ones. Returns (o_base [n_new, Hq, d], o_out [n_out, Hq, d]).
+        cached tokens with the new ones. workspaces: step_workspaces(), kept by the caller, or None
+        (allocated here; the layer holds them until its next step, for check()). A token whose
+        sequence, position or page does not exist is not cached, which only check() tells.
+        Returns (o_base [n_new, Hq, d], o_out [n_out, Hq, d]).
         """
+        if workspaces is None:
+            workspaces = self.step_workspaces(block_table.shape[0], n_new, x.shape[0] - n_new, max_new,
+                                              block_table.shape[1], k_cache.shape[1])
+        project, append, base, out = workspaces
+        self._reports = []
         q, q_out, k, v = ops.orthros_qkv_project(x, n_new, self.w_qkv, self.Hq, self.Hkv, self.d, *self.affines,
-                                                 kv_out=True)
+                                                 kv_out=True, workspace=project)
         q, q_out = ops.orthros_rotate_append(q, k, v, k_cache, v_cache, block_table, token_seq, token_pos, self.steps,
-                                             q_out=q_out, out_positions=out_positions, **self._rope())
+                                             q_out=q_out, out_positions=out_positions, workspace=append, **self._rope())
         o_base, _ = ops.orthros_chunk_attention(q, new_indptr, kv_lens, k_cache, v_cache, block_table, self.window,
-                                                max_new=max_new)
+                                                max_new=max_new, workspace=base)
         o_out, _ = ops.orthros_chunk_attention(q_out, out_indptr, kv_lens, k_cache, v_cache, block_table, 2 ** 31 - 1,
-                                               max_new=1)
+                                               max_new=1, workspace=out)
+        self._reports = [project, append, base, out]
         return o_base, o_out
 
     # ---- training ------------------------------------------------------------
@@ -95,16 +122,23 @@ class RotaryLayer:
         qr = ops.orthros_rotate(qf, pos, self.steps, alpha=ab, beta=bb, **self._rope()).view_as(q)
         kr = ops.orthros_rotate(kf, pos, self.steps, **self._rope()).view_as(k)
         qo = ops.orthros_rotate(q_sel, out_positions, self.steps, alpha=ao, beta=bo, **self._rope())
+        need = ops.orthros_prefill_workspace_size(B, T, self.Hq, self.Hkv, self.d, qo.shape[0], self.window, q.dtype)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         out = ops.orthros_prefill(qr, kr, v, *self.identity, *self.identity, out_indptr, out_positions, self.window,
-                                  q_out=qo)
+                                  q_out=qo, workspace=ws)
+        self._reports = [ws[:256].clone()]  # the status word; the scratch is not held
         return (out[0], out[2]), (qf, q_sel, rows, pos, qr, kr, v, qo, out_indptr, out_positions, out)
 
     def backward(self, saved, do_base, do_out):
         """Gradients of q, k, v and of the four affines, in a dict."""
         qf, q_sel, rows, pos, qr, kr, v, qo, out_indptr, out_positions, out = saved
         ab, _, ao, _ = self.affines
+        need = ops.orthros_prefill_backward_workspace_size(*qr.shape[:2], self.Hq, self.Hkv, self.d, qo.shape[0],
+                                                           self.window, qr.dtype)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=qr.device)
         g = ops.orthros_prefill_backward(qr, kr, v, *self.identity, *self.identity, out_indptr, out_positions,
-                                         self.window, None, *out, do_base, do_out, q_out=qo)
+                                         self.window, None, *out, do_base, do_out, q_out=qo, workspace=ws)
+        self._reports = self._reports[:1] + [ws[:256].clone()]
         dq, da, db = ops.orthros_rotate_backward(g["dq"].flatten(0, 1), qf, pos, self.steps, alpha=ab, **self._rope())
         dk, _, _ = ops.orthros_rotate_backward(g["dk"].flatten(0, 1), None, pos, self.steps, affine_grads=False,
                                                **self._rope())

@@ -180,3 +180,70 @@ def test_repeated_output_positions_add_in_a_fixed_order():
     want = base.double().index_add_(0, rows, sel.double())
     mag = base.double().abs().index_add_(0, rows, sel.double().abs())
     assert bool(((got.flatten(0, 1).double() - want).abs() <= 500 * 2.0 ** -24 * mag).all())
+
+
+def test_check_reports_what_the_calls_of_a_step_found():
+    """A position, page or length that does not exist skips a cache write or makes rows NaN; check() and
+    the caller's own workspaces tell, and a good step after it is clean again."""
+    Hq, Hkv, d, page = 8, 2, 128, 16
+    layer, g = make_layer(Hq, Hkv, d, 100, "half", seed=8)
+    assert layer.check() == (0, 0)  # no call yet
+    x = torch.randn(5 + 2, 256, generator=g).bfloat16().cuda()
+    bt = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    kc = torch.zeros((4, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    good = dict(block_table=bt, token_seq=i32(0, 0, 0, 1, 1), token_pos=i32(0, 1, 2, 0, 1), new_indptr=i32(0, 3, 5),
+                kv_lens=i32(3, 2), out_indptr=i32(0, 1, 2), out_positions=i32(2, 1), max_new=3)
+    own = layer.step_workspaces(2, 5, 2, 3, 2, page)
+    clean = layer.step(x, 5, kc, vc, **good)
+    assert layer.check() == (0, 0)
+    for ws in (None, own):
+        for bad, bits in ((dict(token_pos=i32(0, 1, 2, 0, 2 * page)), 1), (dict(token_seq=i32(0, 0, 0, 1, 2)), 1),
+                          (dict(block_table=i32(0, 1, 4, 3).view(2, 2)), 2), (dict(kv_lens=i32(3, 2 * page + 1)), 4),
+                          (dict(max_new=2), 4)):
+            layer.step(x, 5, kc, vc, **dict(good, **bad), workspaces=ws)
+            assert layer.check() == (5, bits), bad
+            if ws is not None:
+                assert max(ola.orthros_check(w)[1] for w in ws) == bits
+            again = layer.step(x, 5, kc, vc, **good, workspaces=ws)
+            assert layer.check() == (0, 0)
+            assert all(torch.equal(a, b) for a, b in zip(again, clean))
+
+
+def test_check_reports_what_training_found():
+    layer, g = make_layer(4, 2, 64, 30, "half", seed=9)
+    q, k, v = (torch.randn(2, 50, h, 64, generator=g).bfloat16().cuda() for h in (4, 2, 2))
+    for pos, want in ((49, (0, 0)), (50, (5, 1)), (-1, (5, 1))):
+        opos = torch.tensor([10, pos, 0], dtype=torch.int32, device="cuda")
+        (_, oo), saved = layer.forward(q, k, v, np.array([0, 2, 3], dtype=np.int32), opos)
+        assert layer.check() == want
+        layer.backward(saved, torch.ones_like(q), torch.ones_like(oo))
+        assert layer.check() == want
+
+
+def test_step_in_a_graph_reports_after_a_replay():
+    """A captured step's check() reads what the last replay left."""
+    layer, g = make_layer(4, 2, 64, 30, "half", seed=10)
+    x = torch.randn(2, 256, generator=g).bfloat16().cuda()
+    bt = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    kc = torch.zeros((2, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pos, lens, args = i32(0), i32(1), dict(new_indptr=i32(0, 1), out_indptr=i32(0, 1), token_seq=i32(0), max_new=1)
+    ws = layer.step_workspaces(1, 1, 1, 1, 2, 16)
+
+    def step():
+        return layer.step(x, 1, kc, vc, bt, args["token_seq"], pos, args["new_indptr"], lens, args["out_indptr"], pos, 1,
+                          workspaces=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t, want in ((0, (0, 0)), (31, (0, 0)), (32, (5, 5)), (5, (0, 0))):
+        pos.fill_(t)
+        lens.fill_(t + 1)
+        graph.replay()
+        assert layer.check() == want, t
