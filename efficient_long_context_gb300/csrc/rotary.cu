@@ -11,10 +11,11 @@
 //
 // Angles. t * f_i in fp32 loses its fraction at long positions (an ulp at
 // t = 131072, f = 1 is 0.008 rad), so frequencies arrive as 64-bit fixed-point
-// fractions of a turn: the phase of position t is the low 64 bits of t * step,
-// an integer product that wraps as the angle does. Its top 32 bits (2^-32 turn,
-// 1.5e-9 rad) go through sincospif; sin and cos are good to about 1e-7 at every
-// 32-bit position, negative ones included.
+// fractions of a turn, rounded to half a unit: the phase of position t is the low
+// 64 bits of t * step, an integer product that wraps as the angle does, off by
+// 2^-34 turn at most. Its top 32 bits (2^-32 turn, 1.5e-9 rad), as a float (pi 2^-24),
+// go through sincospif (2^-23): sin and cos are off by less than 4e-7 at every 32-bit
+// position, negative ones included.
 //
 // Arithmetic is fp32 throughout, rounded once to the element type on the store;
 // the affine's gradients are accumulated and returned in fp32.

@@ -11,6 +11,25 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
+// freq / 2 pi modulo a turn, to the nearest 2^-64 turn. The quotient needs more than a
+// double's 53 bits (at position 2^31 those leave 4e-7 rad): freq times 1 / 2 pi, held as the sum
+// of two doubles, with the product's own rounding recovered by a fused multiply-add
+// (Dekker's two-term product). std::fma throughout, so that every machine gives the same steps.
+uint64_t turn_units(double freq) {
+    constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    if (freq < 0) return ~turn_units(-freq) + 1u;  // the opposite (q - floor(q) is exact for q >= 0 only)
+    const double q = freq * kHigh;
+    double rest = std::fma(freq, kLow, std::fma(freq, kHigh, -q));  // freq / 2 pi - q
+    rest = std::fmod(rest, 1.0);
+    const double a = std::ldexp(q - std::floor(q), 64);  // [0, 2^64)
+    const double b = std::ldexp(std::fabs(rest), 64);    // [0, 2^64)
+    const double ai = std::floor(a), bi = std::floor(b);
+    const double left = (a - ai) + (rest < 0 ? bi - b : b - bi);  // (-1, 2)
+    uint64_t u = static_cast<uint64_t>(ai);
+    u += rest < 0 ? ~static_cast<uint64_t>(bi) + 1u : static_cast<uint64_t>(bi);
+    return u + static_cast<uint64_t>(static_cast<int64_t>(std::floor(left + 0.5)));
+}
+
 int elem_bytes(orthros_dtype t) { return t == ORTHROS_F32 ? 4 : 2; }
 
 // What every rotating call has in common.
@@ -103,12 +122,7 @@ orthros_status orthros_rotary_steps(const double *freq, int n, uint64_t *steps) 
     if (n > 0 && (!freq || !steps)) return report_error(ORTHROS_EINVAL, "freq and steps must not be NULL");
     for (int i = 0; i < n; ++i)
         if (!std::isfinite(freq[i])) return report_error(ORTHROS_EINVAL, "freq[%d] is not finite", i);
-    for (int i = 0; i < n; ++i) {
-        double turn = freq[i] / kTwoPi;
-        turn -= std::floor(turn);  // whole turns per position change nothing
-        const double scaled = std::ldexp(turn, 64);
-        steps[i] = scaled < 18446744073709551616.0 ? static_cast<uint64_t>(scaled) : 0u;  // a whole turn is none
-    }
+    for (int i = 0; i < n; ++i) steps[i] = turn_units(freq[i]);
     return ORTHROS_OK;
 }
 

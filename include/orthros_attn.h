@@ -480,9 +480,10 @@ ORTHROS_API orthros_status orthros_rotary_frequencies(int rot_dim, double base, 
 
 /*
  * freq HOST [n] (radians per position, finite) -> steps HOST [n]: the fraction
- * of a turn per position in units of 2^-64. The calls below take a device copy
- * of steps: position times step, modulo 2^64, is the phase at any 32-bit
- * position without loss, where a float product has lost its fraction.
+ * of a turn per position in units of 2^-64, rounded to the nearest. The calls
+ * below take a device copy of steps: position times step, modulo 2^64, is the
+ * phase at any 32-bit position to 2^-34 turn, where a float product has lost its
+ * fraction.
  */
 ORTHROS_API orthros_status orthros_rotary_steps(const double *freq, int n, uint64_t *steps);
 

@@ -484,3 +484,66 @@ def test_stream_argument_owns_what_the_call_allocates(handle):
     got = step(stream=s.cuda_stream if handle else s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------------
+# steps and far positions against the angle itself
+# ---------------------------------------------------------------------------
+def inverse_two_pi(bits=400):
+    """floor(2^bits / 2 pi), from Machin's formula pi = 16 arctan(1/5) - 4 arctan(1/239) in integers."""
+    one = 1 << (bits + 64)
+
+    def arctan_of_one_over(n):
+        total, term, k = 0, one // n, 0
+        while term:
+            total += term // (2 * k + 1) * (-1) ** k
+            term //= n * n
+            k += 1
+        return total
+
+    pi = 16 * arctan_of_one_over(5) - 4 * arctan_of_one_over(239)
+    return (one << bits) // (2 * pi)
+
+
+def turn_units(x):
+    """x / 2 pi modulo a turn, in 2^-64 turns, as a Fraction (x a double or a Fraction)."""
+    from fractions import Fraction
+
+    return Fraction(x) * inverse_two_pi() / (1 << 400) % 1 * (1 << 64)
+
+
+def test_steps_are_the_nearest_units(lib):
+    """A step is the frequency's fraction of a turn rounded to 2^-64 turn, not to a double's 53 bits: at
+    position 2^31 the angle is off by 2^-34 turn (4e-10 rad) at most."""
+    freq = [1.0, 0.5, 1e-3, 2 * math.pi, -1.0, 2 * math.pi + 1.0, 3.0, 1e-12, -1e-30, 1e-25, 1e6, 123456.789, 2.0 ** 40]
+    for rule in (dict(), dict(scaling="bands", factor=8.0, original_length=8192.0)):
+        freq += ola.orthros_rotary_frequencies(128, 500000.0, **rule)[0].tolist()
+    steps = [int(s) % 2 ** 64 for s in ola.orthros_rotary_steps(freq).tolist()]
+    for f, s in zip(freq, steps):
+        off = (s - turn_units(f)) % (1 << 64)
+        assert min(off, (1 << 64) - off) <= 0.5 + 2.0 ** -20, (f, s)
+    # far outside any use: still a defined step, no overflow
+    ola.orthros_rotary_steps([1e300, -1e300, 1.7e308, 5e-324, -5e-324])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_far_positions_against_the_angle(layout):
+    """fp32 at the ends of the 32-bit positions, against position times frequency in 400 bits."""
+    rot, H, d = 64, 2, 64
+    freq = frequencies(rot)
+    pos = [0, 1, -1, 131071, 10 ** 6 + 1, 2 ** 29 + 3, 2 ** 30 + 7, 2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1, 1999999973]
+    x = torch.randn(len(pos), H, d, generator=torch.Generator().manual_seed(4))
+    from fractions import Fraction
+
+    ph = torch.tensor([[float(turn_units(Fraction(f) * t)) / 2.0 ** 64 for f in freq.tolist()] for t in pos],
+                      dtype=torch.float64)
+    c, s = torch.cos(2 * math.pi * ph)[:, None], torch.sin(2 * math.pi * ph)[:, None]
+    ia, ib = channels(rot, layout)
+    u, ref, mag = x.double(), x.double(), x.double().abs()
+    ref[..., ia], ref[..., ib] = u[..., ia] * c - u[..., ib] * s, u[..., ia] * s + u[..., ib] * c
+    m = mag[..., ia] + mag[..., ib]
+    mag[..., ia], mag[..., ib] = m, m
+    y = ola.orthros_rotate(x.cuda(), torch.tensor(pos, dtype=torch.int32).cuda(), ola.orthros_rotary_steps(freq).cuda(),
+                           layout=layout)
+    check(y, ref, mag, torch.float32, "far positions")
