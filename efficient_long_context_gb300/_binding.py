@@ -653,7 +653,12 @@ def _steps(t, dev):
 def orthros_rotary_frequencies(rot_dim, base, scaling="plain", *, factor=1.0, original_length=0.0, low_turns=1.0,
                                high_turns=4.0):
     """orthros_rotary_frequencies of include/orthros_attn.h: (freq float64 [rot_dim/2] CPU tensor, amplitude)
-    of a scaling rule ("plain", "linear", "stretch", "bands", "bands_tempered")."""
+    of a scaling rule ("plain", "linear", "stretch", "bands", "bands_tempered").
+
+    low_turns and high_turns bound the bands that are blended; their defaults, 1 and 4, are the
+    published ones of "bands". YaRN, which "bands_tempered" follows, was published with 1 and
+    32: give high_turns=32 for a model that was trained with it.
+    """
     lib = load_library()
     if scaling not in _ROPE_SCALINGS:
         raise OrthrosError(1, f"scaling {scaling!r}: one of {sorted(_ROPE_SCALINGS)}")

@@ -457,7 +457,8 @@ typedef enum { ORTHROS_ROPE_HALF = 0, ORTHROS_ROPE_INTERLEAVED = 1 } orthros_rop
  *            above high_turns, ((1-s) / factor + s) f_i between, with
  *            s = (r - low_turns) / (high_turns - low_turns)
  *   BANDS_TEMPERED  BANDS with amplitude 0.1 ln(factor) + 1 on cos and sin
- *            (YaRN; the other rules have amplitude 1)
+ *            (YaRN, published with low_turns 1 and high_turns 32; BANDS is common
+ *            with 1 and 4; the other rules have amplitude 1)
  */
 typedef enum {
     ORTHROS_ROPE_PLAIN = 0,
