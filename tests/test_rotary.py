@@ -547,3 +547,119 @@ def test_far_positions_against_the_angle(layout):
     y = ola.orthros_rotate(x.cuda(), torch.tensor(pos, dtype=torch.int32).cuda(), ola.orthros_rotary_steps(freq).cuda(),
                            layout=layout)
     check(y, ref, mag, torch.float32, "far positions")
+
+
+# ---------------------------------------------------------------------------
+# blocks that walk many tables of angles: with few heads a block has many tokens
+# side by side, with many heads few; either way more than 128 tokens (a run of
+# looked-up positions and page slots) here, and odd rests
+# ---------------------------------------------------------------------------
+def long_angles(pos, steps):
+    """cos, sin [n, pairs] in fp64 on the GPU: int64 products wrap as the phase does."""
+    ph = (pos.long()[:, None] * steps[None, :]).double() * 2.0 ** -64
+    return torch.cos(2 * math.pi * ph), torch.sin(2 * math.pi * ph)
+
+
+def long_rotate(u, mag, pos, steps, layout, amp, sign=1.0):
+    """plain_rotate on the GPU, with the magnitudes given."""
+    c, s = long_angles(pos, steps)
+    c, s = amp * c[:, None, :], amp * sign * s[:, None, :]
+    ia, ib = channels(2 * steps.numel(), layout)
+    y, m = u.clone(), mag.clone()
+    y[..., ia] = u[..., ia] * c - u[..., ib] * s
+    y[..., ib] = u[..., ia] * s + u[..., ib] * c
+    m[..., ia] = m[..., ib] = amp * (mag[..., ia] + mag[..., ib])
+    return y, m
+
+
+def long_check(got, raw, affine, pos, steps, layout, amp, what, sign=1.0):
+    for i in range(0, got.shape[0], 8192):
+        r = slice(i, i + 8192)
+        u = raw[r].double()
+        mag = u.abs()
+        if affine is not None:
+            al, be = affine[0].double(), affine[1].double()
+            mag = mag * al.abs() + be.abs()
+            u = u * al + be
+        ref, m = long_rotate(u, mag, pos[r], steps, layout, amp, sign)
+        tol = HALF_STEP[got.dtype] * ref.abs() + ANGLE * m + 1e-37
+        err = (got[r].double() - ref).abs() / tol
+        assert float(err.max()) <= 1, f"{what}, tokens from {i}: {float(err.max()):.3f} of the tolerance"
+
+
+def long_inputs(n, H, d, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    pos = torch.randint(0, 200000, (n,), generator=g, device="cuda", dtype=torch.int32)
+    return rn(n, H, d).to(dtype), 1.0 + 0.1 * rn(H, d), 0.1 * rn(H, d), pos, rn(n, H, d).to(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,H,d,rot,dtype", [
+    (200001, 1, 64, 64, torch.bfloat16), (45001, 5, 128, 48, torch.bfloat16), (45001, 32, 128, 128, torch.bfloat16),
+    (100001, 1, 64, 32, torch.float32), (25001, 32, 128, 128, torch.float32)])
+def test_rotate_long(n, H, d, rot, dtype, layout):
+    x, al, be, pos, _ = long_inputs(n, H, d, dtype, seed=H)
+    steps = ola.orthros_rotary_steps(frequencies(rot)).cuda()
+    y = ola.orthros_rotate(x, pos, steps, layout=layout, amplitude=1.25, alpha=al, beta=be)
+    long_check(y, x, (al, be), pos, steps, layout, 1.25, "rotate")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,H,d,rot,dtype", [
+    (24001, 2, 64, 64, torch.bfloat16), (24001, 32, 128, 128, torch.bfloat16), (21001, 8, 128, 96, torch.float32),
+    (24001, 40, 64, 16, torch.float32)])
+def test_backward_long(n, H, d, rot, dtype, layout):
+    x, al, _, pos, dy = long_inputs(n, H, d, dtype, seed=3 * H)
+    steps = ola.orthros_rotary_steps(frequencies(rot)).cuda()
+    dx, da, db = ola.orthros_rotate_backward(dy, x, pos, steps, layout=layout, amplitude=0.75, alpha=al)
+    sums = [torch.zeros(H, d, dtype=torch.float64, device="cuda") for _ in range(4)]
+    for i in range(0, n, 8192):
+        r = slice(i, i + 8192)
+        g, m = long_rotate(dy[r].double(), dy[r].double().abs(), pos[r], steps, layout, 0.75, -1.0)
+        err = (dx[r].double() - g * al.double()).abs() / (HALF_STEP[dtype] * (g * al).abs() + ANGLE * m * al.abs() + 1e-37)
+        assert float(err.max()) <= 1, f"dx, tokens from {i}: {float(err.max()):.3f} of the tolerance"
+        for to, v in zip(sums, ((g * x[r].double()), g, m * x[r].double().abs(), m)):
+            to += v.sum(0)
+    # additions in a row: a block's tokens, its token lanes (16 at most), the blocks' partials
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    depth = 2 * ((n + sms - 1) // sms + 16 + sms)  # (twice: groups of heads share the SMs)
+    for got, ref, terms in ((da, sums[0], sums[2]), (db, sums[1], sums[3])):
+        assert bool(((got.double() - ref).abs() <= ((depth + 12) * 2.0 ** -24 + ANGLE) * terms).all())
+    dx2, none, _ = ola.orthros_rotate_backward(dy, None, pos, steps, layout=layout, amplitude=0.75, alpha=al, affine_grads=False)
+    assert none is None and torch.equal(dx, dx2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,n_out,Hq,Hkv,d,page,rot,layout", [
+    ([9000, 1, 4000, 7001], 9001, 32, 8, 128, 16, 128, "half"), ([70001], 3, 1, 1, 64, 7, 32, "interleaved")])
+def test_append_long(new, n_out, Hq, Hkv, d, page, rot, layout, dtype):
+    B, n = len(new), sum(new)
+    packed, al, be, _, _ = long_inputs(n, Hq + 2 * Hkv, d, dtype, seed=n)
+    q_out, al2, be2, opos, _ = long_inputs(n_out, Hq, d, dtype, seed=n + 1)
+    al, be = al[:Hq].contiguous(), be[:Hq].contiguous()
+    g = torch.Generator().manual_seed(n)
+    mp = max((m + 50 + page - 1) // page for m in new)
+    bt = torch.randperm(B * mp, generator=g).to(torch.int32).view(B, mp).cuda()
+    seq = torch.cat([torch.full((m,), b, dtype=torch.int32) for b, m in enumerate(new)]).cuda()
+    pos = torch.cat([torch.arange(7 * b, 7 * b + m, dtype=torch.int32) for b, m in enumerate(new)]).cuda()
+    kc = torch.full((B * mp, page, Hkv, d), 7.0, dtype=dtype, device="cuda")
+    vc = torch.full_like(kc, 9.0)
+    steps = ola.orthros_rotary_steps(frequencies(rot)).cuda()
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    q, k, v = packed[:, :Hq], packed[:, Hq:Hq + Hkv], packed[:, Hq + Hkv:]
+    qr, qor = ola.orthros_rotate_append(q, k, v, kc, vc, bt, seq, pos, steps, layout=layout, amplitude=1.1, q_out=q_out,
+                                        out_positions=opos, alpha_base=al, beta_base=be, alpha_out=al2, beta_out=be2,
+                                        workspace=ws)
+    assert ola.orthros_check(ws) == (0, 0)
+    slots = bt[seq.long(), torch.div(pos, page, rounding_mode="floor").long()].long() * page + (pos % page).long()
+    long_check(qr, q, (al, be), pos, steps, layout, 1.1, "queries")
+    long_check(qor, q_out, (al2, be2), opos, steps, layout, 1.1, "output queries")
+    long_check(kc.flatten(0, 1)[slots], k, None, pos, steps, layout, 1.1, "keys")
+    assert torch.equal(vc.flatten(0, 1)[slots], v)
+    rest = torch.ones(B * mp * page, dtype=torch.bool, device="cuda")
+    rest[slots] = False
+    assert bool((kc.flatten(0, 1)[rest] == 7).all()) and bool((vc.flatten(0, 1)[rest] == 9).all())
