@@ -8,6 +8,10 @@ ex2.approx (2^-22). So |lse| is off by at most 2^-17 S + 8e-5 + 2^-20 |lse| (sum
 product with scale), and o by the same relative error of every weight and of the
 sum (2 (2^-17 S + 8e-5) A), by P's rounding to bf16 (half a step: 2^-8 A) and by its
 own (2^-8 |o|).
+
+The cubic is gone from the kernel: every exponential is ex2.approx, so 8e-5 is wider than
+it need be. check_fp32 below has the bound of the present code, and its tests hold the sums
+and weights to it.
 """
 import numpy as np
 import pytest
@@ -470,3 +474,43 @@ def test_row_without_a_finite_logit_is_nan(new, total, Hq, Hkv, d, page):
         keep[i, h] = False
         assert bool(torch.isnan(o[i, h]).all()) and float(lse[i, h]) == -float("inf"), (i, h)
     assert torch.equal(o[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
+
+
+# ---------------------------------------------------------------------------
+# the sums and weights beside the products, to fp32
+# ---------------------------------------------------------------------------
+def check_fp32(got, ref, tiles, what=""):
+    """The bound of the present code, in units of u = 2^-24 (an fp32 half step): a logit is off by 128 u S
+    (128 products accumulated) and, with its shift, by 8 u S more (c2 = scale log2 e, m c2 and the
+    difference are rounded); every exponential is ex2.approx, 4 u. A weight has one exponential for
+    its key, one for each rescale of its row (the shift moves by 2^8 at least, so at most 1 + S log2(e) / 4),
+    one for the join of two slots and one for each group of two parts in the merge (a part is two key
+    tiles or more). The sum adds 36 values per tile, then tiles and groups: u each. lse adds logf
+    (2 u |lse| with m scale taken off, which S bounds) and a sum (u). In o, P and the result are rounded
+    to bf16 (2^-8 each), and P V accumulates tiles of 128 products (u each, at most 2 u where the unit truncates)."""
+    u = 2.0 ** -24
+    o, lse = got[0].double(), got[1].double()
+    ro, rl, A, S = ref
+    groups = tiles / 4 + 1
+    weight = u * (136 * S + 4 * (3 + S * 1.4427 / 4 + groups) + 36 + tiles + groups)
+    tol_l = weight + 4 * u * (rl.abs() + S)
+    tol_o = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2 * weight[..., None] + 256 * u * tiles) * A + 1e-30
+    el, eo = ((lse - rl).abs() / tol_l).max(), ((o - ro).abs() / tol_o).max()
+    assert float(el) <= 1 and float(eo) <= 1, f"{what}: lse {float(el):.3f}, o {float(eo):.3f} of the tolerance"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qscale", [2.0 ** -6, 1.5])
+@pytest.mark.parametrize("new,total,Hq,Hkv,d,page,window", CASES,
+                         ids=lambda v: "-".join(map(str, v)) if isinstance(v, list) else str(v))
+def test_sums_and_weights_hold_fp32(new, total, Hq, Hkv, d, page, window, qscale):
+    w = make(new, total, Hq, Hkv, d, page, window, seed=sum(total) + page + 1, qscale=qscale)
+    check_fp32(call(w, max_new=max(new)), plain(w, d ** -0.5), (max(total) + 127) // 128)
+
+
+@pytest.mark.gpu
+def test_many_parts_hold_fp32():
+    """One token over 40000 keys of a single kv head: 152 parts joined."""
+    for qscale in (2.0 ** -6, 1.5, 60.0):
+        w = make([1], [40000], 8, 1, 128, 64, 1 << 20, seed=21, qscale=qscale)
+        check_fp32(call(w), plain(w, 128 ** -0.5), 313, f"q scale {qscale}")
