@@ -39,8 +39,8 @@
 //
 // Precision: products of bf16 values accumulate in fp32; m, l and o are fp32;
 // P is rounded to bf16 for the product with V (the sum l takes it unrounded),
-// at most half a bf16 step of each term, which the sum averages below the rounding
-// of o itself.
+// at most half a bf16 step of each term; over the keys of a row that is 0.0015 of o
+// (relative, measured with independent values), beside 0.0017 of o's own rounding.
 //
 // Bound and measured (GQA 32/8, d = 128): decoding by HBM, 32 sequences over 16K-32K
 // keys in 480 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that

@@ -595,8 +595,12 @@ ORTHROS_API size_t orthros_chunk_attention_workspace_size(int B, int n, int max_
  *              256-byte aligned; contents on entry do not matter.
  * Every length is read on the device: a step can be captured once and replayed
  * while the lengths grow. bf16 only; at most 128 query heads per kv head.
- * Keys and values at visible positions must be finite; what pages hold past a
- * sequence's length, or before every window of the call, does not matter.
+ * Keys and values that any row of the call sees must be finite (one that is not
+ * may also make NaN rows of its sequence that do not see it); what pages hold
+ * past a sequence's length, or before every window of the call, does not matter.
+ * Products accumulate in fp32, as do the running maximum, the sum and o; softmax
+ * weights are rounded to bf16 for their product with v, as in the other bf16
+ * calls: half a step, 2^-8, of each term.
  * A q_indptr that does not run from 0 to n sets ORTHROS_DEV_BAD_LENGTH and
  * every row is NaN; n_b > max_new, kv_lens[b] < n_b or past the block table
  * sets it for that sequence's rows. A page id outside [0, num_pages) sets
