@@ -810,10 +810,15 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     return q_rot, q_out_rot
 
 
+def _int32(x) -> int:
+    """A bound that may exceed 32 bits, held at their ends (ctypes would drop its upper bits)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size,
                                            dtype=torch.bfloat16) -> int:
-    return int(load_library().orthros_chunk_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size,
-                                                                     _DTYPES[dtype]))
+    return int(load_library().orthros_chunk_attention_workspace_size(B, n, _int32(max_new), Hq, Hkv, d, max_pages,
+                                                                     page_size, _DTYPES[dtype]))
 
 
 def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table, window, scale=None, *, max_new=None,
@@ -834,8 +839,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     n, Hq, d = shape
     num_pages, page_size, Hkv = k_cache.shape[:3]
     B, max_pages = block_table.shape
-    if max_new is None:
-        max_new = n
+    max_new = n if max_new is None else _int32(max_new)
     if out is None:
         o = torch.empty_like(q)
         lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
@@ -850,7 +854,7 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
     rc = lib.orthros_chunk_attention(
         _block("q", q, dev, dtype, shape), _index("q_indptr", q_indptr, dev, B + 1), _index("kv_lens", kv_lens, dev, B),
         _block("k_cache", k_cache, dev, dtype, pool), _block("v_cache", v_cache, dev, dtype, pool),
-        _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq, Hkv, d, window,
+        _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq, Hkv, d, _int32(window),
         d ** -0.5 if scale is None else scale, _dtype(q), max_pages, page_size, num_pages,
         oa, la, _addr(workspace, dev),
         workspace.numel(), here)

@@ -514,3 +514,22 @@ def test_many_parts_hold_fp32():
     for qscale in (2.0 ** -6, 1.5, 60.0):
         w = make([1], [40000], 8, 1, 128, 64, 1 << 20, seed=21, qscale=qscale)
         check_fp32(call(w), plain(w, 128 ** -0.5), 313, f"q scale {qscale}")
+
+
+def test_workspace_of_a_bound_past_32_bits(lib):
+    f = ola.orthros_chunk_attention_workspace_size
+    assert f(2, 40, 2 ** 32 + 1, 8, 2, 128, 9, 16) == f(2, 40, 40, 8, 2, 128, 9, 16)
+    assert f(2, 40, -2 ** 32 + 1, 8, 2, 128, 9, 16) == 0
+
+
+@pytest.mark.gpu
+def test_window_and_bound_past_32_bits():
+    """A window or a bound of the new tokens beyond 32 bits is every key, every token; their lower 32
+    bits mean nothing."""
+    w = make([40, 1], [300, 70], 8, 2, 64, 16, 1 << 20, seed=22)
+    want = call(w)
+    for window, max_new in ((2 ** 32 + 1, None), (2 ** 40, None), (1 << 20, 2 ** 32 + 1), (2 ** 33 + 5, 2 ** 35)):
+        got = call(dict(w, window=window), max_new=max_new)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ola.OrthrosError):
+        call(dict(w, window=-2 ** 32 + 5))
