@@ -10,6 +10,7 @@ from __future__ import annotations
 
 from ._binding import (  # noqa: F401
     OrthrosError,
+    StepPlan,
     lib_path,
     load_library,
     orthros_check,
@@ -22,6 +23,12 @@ from ._binding import (  # noqa: F401
     orthros_extend_workspace_size,
     orthros_last_error,
     orthros_merge_partials,
+    orthros_norm_rotate,
+    orthros_norm_rotate_append,
+    orthros_norm_rotate_backward,
+    orthros_norm_rotate_backward_workspace_size,
+    orthros_plan_step,
+    orthros_plan_step_buffers,
     orthros_prefill,
     orthros_prefill_backward,
     orthros_prefill_backward_workspace_size,
@@ -41,4 +48,7 @@ from ._binding import (  # noqa: F401
     orthros_selftest_wait_timeout,
     orthros_profile_end,
     orthros_status_string,
+    orthros_tree_attention,
+    orthros_tree_attention_workspace_size,
+    orthros_tree_commit,
 )

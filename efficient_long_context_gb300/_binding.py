@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -28,7 +29,11 @@ EXPORTS = ("orthros_prefill_workspace_size", "orthros_prefill", "orthros_prefill
            "orthros_decode_workspace_size",
            "orthros_decode", "orthros_decode_static", "orthros_rotary_frequencies", "orthros_rotary_steps",
            "orthros_rotate", "orthros_rotate_backward_workspace_size", "orthros_rotate_backward",
-           "orthros_rotate_append", "orthros_chunk_attention_workspace_size", "orthros_chunk_attention",
+           "orthros_rotate_append", "orthros_norm_rotate", "orthros_norm_rotate_backward_workspace_size",
+           "orthros_norm_rotate_backward", "orthros_norm_rotate_append",
+           "orthros_chunk_attention_workspace_size", "orthros_chunk_attention",
+           "orthros_plan_step", "orthros_tree_attention_workspace_size", "orthros_tree_attention",
+           "orthros_tree_commit",
            "orthros_check", "orthros_profile_begin", "orthros_profile_end",
            "orthros_selftest_wait_timeout", "orthros_status_string", "orthros_last_error")
 
@@ -129,6 +134,28 @@ def load_library(path: str | None = None):
         lib.orthros_chunk_attention.restype = i32
         lib.orthros_chunk_attention.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32,
                                                 i32, i32, i32, vp, vp, vp, sz, vp]
+        lib.orthros_norm_rotate.restype = i32
+        lib.orthros_norm_rotate.argtypes = [vp, ll, vp, vp, f32, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, vp, ll, vp]
+        lib.orthros_norm_rotate_backward_workspace_size.restype = sz
+        lib.orthros_norm_rotate_backward_workspace_size.argtypes = [i32] * 4
+        lib.orthros_norm_rotate_backward.restype = i32
+        lib.orthros_norm_rotate_backward.argtypes = [vp, ll, vp, ll, vp, vp, f32, vp, vp, i32, i32, f32, i32, i32, i32, i32,
+                                                     vp, ll, vp, vp, vp, vp, sz, vp]
+        lib.orthros_norm_rotate_append.restype = i32
+        lib.orthros_norm_rotate_append.argtypes = [vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, f32, vp, vp, vp, vp, vp, i32, i32,
+                                                   f32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32,
+                                                   vp, sz, vp]
+        lib.orthros_plan_step.restype = i32
+        lib.orthros_plan_step.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
+                                          vp, vp, vp, vp, sz, vp]
+        lib.orthros_tree_attention_workspace_size.restype = sz
+        lib.orthros_tree_attention_workspace_size.argtypes = [i32] * 9
+        lib.orthros_tree_attention.restype = i32
+        lib.orthros_tree_attention.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32,
+                                               i32, i32, i32, vp, vp, vp, sz, vp]
+        lib.orthros_tree_commit.restype = i32
+        lib.orthros_tree_commit.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp,
+                                            sz, vp]
         lib.orthros_selftest_wait_timeout.restype = i32
         lib.orthros_selftest_wait_timeout.argtypes = [ctypes.c_longlong, vp, sz, vp]
         lib.orthros_check.restype = i32
@@ -810,6 +837,199 @@ def orthros_rotate_append(q, k_new, v_new, k_cache, v_cache, block_table, token_
     return q_rot, q_out_rot
 
 
+def orthros_norm_rotate(x, positions, steps, weight=None, eps=1e-6, *, layout="half", amplitude=1.0, alpha=None, beta=None,
+                        out=None, stream=None):
+    """orthros_norm_rotate of include/orthros_attn.h: y = amplitude R(t) (alpha (.) (weight (.) x / rms(x)) + beta),
+    the mean of a head's squares plus eps under the root.
+
+    x [n, H, d] (any token stride), positions [n] int32, steps from orthros_rotary_steps on the GPU,
+    weight float [d], shared by the heads. Returns y [n, H, d] (`out` may be x).
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_norm_rotate(x, positions, steps, weight, eps, layout=layout, amplitude=amplitude, alpha=alpha,
+                                       beta=beta, out=out)
+    lib = _lib or load_library()
+    dev, here = _here(x)
+    shape, dtype = x.shape, x.dtype
+    n, H, d = shape
+    xa, xs = _rows("x", x, dev, dtype, shape)
+    if out is None:
+        out = _new(x, shape)
+        ya, ys = out.data_ptr(), H * d
+    else:
+        ya, ys = _rows("out", out, dev, dtype, shape)
+    st, rot = _steps(steps, dev)
+    rc = lib.orthros_norm_rotate(
+        xa, xs, _index("positions", positions, dev, n), _block("weight", weight, dev, torch.float32, (d,)), eps,
+        _block("alpha", alpha, dev, torch.float32, (H, d)), _block("beta", beta, dev, torch.float32, (H, d)), st, rot,
+        _rope_layout(layout), amplitude, n, H, d, _dtype(x), ya, ys, here)
+    if rc:
+        _raise_if(rc, lib)
+    return out
+
+
+def orthros_norm_rotate_backward_workspace_size(n, H, d, dtype=torch.bfloat16) -> int:
+    return int(load_library().orthros_norm_rotate_backward_workspace_size(n, H, d, _DTYPES[dtype]))
+
+
+def orthros_norm_rotate_backward(dy, x, positions, steps, weight=None, eps=1e-6, *, layout="half", amplitude=1.0, alpha=None,
+                                 weight_grad=True, affine_grads=True, out=None, workspace=None, stream=None):
+    """orthros_norm_rotate_backward of include/orthros_attn.h.
+
+    dy, x [n, H, d] (any token strides). Returns (dx, d_weight, d_alpha, d_beta): float [d] without
+    weight_grad None, the last two float [H, d] or, without affine_grads, None; `out` gives the four tensors.
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_norm_rotate_backward(dy, x, positions, steps, weight, eps, layout=layout, amplitude=amplitude,
+                                                alpha=alpha, weight_grad=weight_grad, affine_grads=affine_grads, out=out,
+                                                workspace=workspace)
+    lib = _lib or load_library()
+    dev, here = _here(dy)
+    shape, dtype = dy.shape, dy.dtype
+    n, H, d = shape
+    if out is None:
+        dx, dw, da, db = _new(dy, shape), None, None, None
+        if weight_grad:
+            dw = torch.empty(d, dtype=torch.float32, device=dy.device)
+        if affine_grads:
+            da = torch.empty((H, d), dtype=torch.float32, device=dy.device)
+            db = torch.empty_like(da)
+        oa, os_ = dx.data_ptr(), H * d
+    else:
+        dx, dw, da, db = out
+        oa, os_ = _rows("dx", dx, dev, dtype, shape)
+    if workspace is None and (da is not None or dw is not None):
+        workspace = torch.empty(max(orthros_norm_rotate_backward_workspace_size(n, H, d, dtype), 256),
+                                dtype=torch.uint8, device=dy.device)
+    ga, gs = _rows("dy", dy, dev, dtype, shape)
+    xa, xs = _rows("x", x, dev, dtype, shape)
+    st, rot = _steps(steps, dev)
+    rc = lib.orthros_norm_rotate_backward(
+        ga, gs, xa, xs, _index("positions", positions, dev, n), _block("weight", weight, dev, torch.float32, (d,)), eps,
+        _block("alpha", alpha, dev, torch.float32, (H, d)), st, rot, _rope_layout(layout), amplitude, n, H, d, _dtype(dy), oa,
+        os_, _block("d_weight", dw, dev, torch.float32, (d,)), _block("d_alpha", da, dev, torch.float32, (H, d)),
+        _block("d_beta", db, dev, torch.float32, (H, d)), _addr(workspace, dev),
+        workspace.numel() if workspace is not None else 0, here)
+    _raise_if(rc, lib)
+    return dx, dw, da, db
+
+
+def orthros_norm_rotate_append(q, k_new, v_new, k_cache, v_cache, token_slots, token_pos, steps, *, eps=1e-6, q_weight=None,
+                               k_weight=None, layout="half", amplitude=1.0, q_out=None, out_positions=None, alpha_base=None,
+                               beta_base=None, alpha_out=None, beta_out=None, out=None, workspace=None, stream=None):
+    """orthros_norm_rotate_append of include/orthros_attn.h.
+
+    k_new, v_new [n, Hkv, d] go to the slots token_slots (orthros_plan_step; -1: not cached), keys normed
+    and rotated; q [n, Hq, d] (or None) and q_out [n_out, Hq, d] are normed, scaled and rotated. eps = 0:
+    no norm. Returns (q_rot or None, q_out_rot or None); k_cache / v_cache are updated in place.
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_norm_rotate_append(
+                q, k_new, v_new, k_cache, v_cache, token_slots, token_pos, steps, eps=eps, q_weight=q_weight,
+                k_weight=k_weight, layout=layout, amplitude=amplitude, q_out=q_out, out_positions=out_positions,
+                alpha_base=alpha_base, beta_base=beta_base, alpha_out=alpha_out, beta_out=beta_out, out=out,
+                workspace=workspace)
+    lib = _lib or load_library()
+    dev, here = _here(k_cache)
+    dtype = k_new.dtype
+    n, Hkv, d = k_new.shape
+    n_out = q_out.shape[0] if q_out is not None else 0
+    Hq = q.shape[1] if q is not None else (q_out.shape[1] if q_out is not None else Hkv)
+    num_pages, page_size = k_cache.shape[:2]
+    if out is None:
+        q_rot = _new(q, (n, Hq, d)) if q is not None else None
+        q_out_rot = _new(q_out, (n_out, Hq, d)) if q_out is not None else None
+    else:
+        q_rot, q_out_rot = out
+        _block("q_rot", q_rot, dev, dtype, (n, Hq, d))
+        _block("q_out_rot", q_out_rot, dev, dtype, (n_out, Hq, d))
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=k_new.device)
+    qa, qs = _rows("q", q, dev, dtype, (n, Hq, d))
+    qoa, qos = _rows("q_out", q_out, dev, dtype, (n_out, Hq, d))
+    ka, ks = _rows("k_new", k_new, dev, dtype, (n, Hkv, d))
+    va, vs = _rows("v_new", v_new, dev, dtype, (n, Hkv, d))
+    aff = [_block(name, t, dev, torch.float32, (Hq, d)) for name, t in
+           (("alpha_base", alpha_base), ("beta_base", beta_base), ("alpha_out", alpha_out), ("beta_out", beta_out))]
+    st, rot = _steps(steps, dev)
+    pool = (num_pages, page_size, Hkv, d)
+    rc = lib.orthros_norm_rotate_append(
+        qa, qs, qoa, qos, ka, ks, va, vs, _block("q_weight", q_weight, dev, torch.float32, (d,)),
+        _block("k_weight", k_weight, dev, torch.float32, (d,)), eps, *aff, st, rot, _rope_layout(layout), amplitude,
+        _index("token_slots", token_slots, dev, n), _index("token_pos", token_pos, dev, n),
+        _index("out_positions", out_positions, dev, n_out), n, n_out, Hq, Hkv, d, _dtype(k_new),
+        _addr(q_rot, dev), _addr(q_out_rot, dev), _block("k_cache", k_cache, dev, dtype, pool),
+        _block("v_cache", v_cache, dev, dtype, pool), page_size, num_pages, _addr(workspace, dev), workspace.numel(), here)
+    _raise_if(rc, lib)
+    return q_rot, q_out_rot
+
+
+class StepPlan(NamedTuple):
+    """What orthros_plan_step makes of a step's lengths: int32 tensors on the GPU."""
+
+    q_indptr: torch.Tensor     # [B + 1]
+    kv_lens: torch.Tensor      # [B]
+    pages_held: torch.Tensor   # [B]
+    free_count: torch.Tensor   # [1]
+    token_seq: torch.Tensor    # [n]
+    token_pos: torch.Tensor    # [n]
+    token_slots: torch.Tensor  # [n]
+    tree_mask: torch.Tensor | None  # [n, words], None without trees
+    cache_lens: torch.Tensor | None = None  # [B], all new tokens counted
+
+
+def orthros_plan_step_buffers(B, n, max_tree=0, device="cuda") -> StepPlan:
+    """Outputs for orthros_plan_step(out=...): B sequences, n token rows, trees of up to max_tree tokens."""
+    def new(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=device)
+
+    return StepPlan(new(B + 1), new(B), new(B), new(1), new(n), new(n), new(n),
+                    new(n, (max_tree + 31) // 32) if max_tree else None, new(B))
+
+
+def orthros_plan_step(cache_lens, new_lens, pages_held, free_pages, free_count, block_table, page_size, n, *, parents=None,
+                      max_tree=0, out=None, workspace=None, stream=None):
+    """orthros_plan_step of include/orthros_attn.h on int32 CUDA tensors.
+
+    cache_lens, new_lens (-1: the sequence has ended), pages_held [B]; free_pages [num_pages], of which
+    the first free_count [1] are free; block_table [B, max_pages]. n token rows are described, those behind
+    the last token as padding. parents [n] with max_tree: the new tokens are drafted trees. free_pages and
+    block_table are updated in place; `out` (orthros_plan_step_buffers) may hold cache_lens, pages_held and
+    free_count themselves. Returns a StepPlan.
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_plan_step(cache_lens, new_lens, pages_held, free_pages, free_count, block_table, page_size, n,
+                                     parents=parents, max_tree=max_tree, out=out, workspace=workspace)
+    lib = _lib or load_library()
+    dev, here = _here(block_table)
+    B, max_pages = block_table.shape
+    if (parents is None) != (max_tree == 0):
+        raise OrthrosError(1, "parents and max_tree: both or neither")
+    if out is None:
+        out = orthros_plan_step_buffers(B, n, max_tree, block_table.device)
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=block_table.device)
+    words = (max_tree + 31) // 32
+    if max_tree and out.tree_mask is None:
+        raise OrthrosError(1, "out.tree_mask must be a tensor")
+    rc = lib.orthros_plan_step(
+        _index("cache_lens", cache_lens, dev, B), _index("new_lens", new_lens, dev, B), _index("pages_held", pages_held, dev, B),
+        _index("free_count", free_count, dev, 1), _index("parents", parents, dev, n), max_tree,
+        _index("free_pages", free_pages, dev, free_pages.numel()), _index("block_table", block_table, dev, B * max_pages), B, n,
+        max_pages, page_size, free_pages.numel(), _index("q_indptr", out.q_indptr, dev, B + 1),
+        _index("kv_lens", out.kv_lens, dev, B), _index("cache_lens", out.cache_lens, dev, B),
+        _index("pages_held", out.pages_held, dev, B), _index("free_count", out.free_count, dev, 1), _index("token_seq", out.token_seq, dev, n),
+        _index("token_pos", out.token_pos, dev, n), _index("token_slots", out.token_slots, dev, n),
+        _index("tree_mask", out.tree_mask, dev, n * words) if max_tree else None, _addr(workspace, dev), workspace.numel(), here)
+    if rc:
+        _raise_if(rc, lib)
+    return out
+
+
 def _int32(x) -> int:
     """A bound that may exceed 32 bits, held at their ends (ctypes would drop its upper bits)."""
     return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
@@ -860,6 +1080,93 @@ def orthros_chunk_attention(q, q_indptr, kv_lens, k_cache, v_cache, block_table,
         workspace.numel(), here)
     _raise_if(rc, lib)
     return o, lse
+
+
+def orthros_tree_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype=torch.bfloat16) -> int:
+    return int(load_library().orthros_tree_attention_workspace_size(B, n, _int32(max_new), Hq, Hkv, d, max_pages, page_size,
+                                                                    _DTYPES[dtype]))
+
+
+def orthros_tree_attention(q, q_indptr, kv_lens, tree_mask, k_cache, v_cache, block_table, window, scale=None, *, max_new=None,
+                           out=None, workspace=None, stream=None):
+    """orthros_tree_attention of include/orthros_attn.h on torch CUDA tensors.
+
+    q [n, Hq, d] with the drafted tokens of sequence b at q_indptr[b] .. q_indptr[b+1]; tree_mask [n, words]
+    int32: bit j of row i is token j of its sequence's tree. Rows behind q_indptr[B] are left as they were.
+    max_new bounds the tokens of a tree (default: what the mask holds). Returns (o [n, Hq, d], lse [n, Hq]).
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_tree_attention(q, q_indptr, kv_lens, tree_mask, k_cache, v_cache, block_table, window, scale,
+                                          max_new=max_new, out=out, workspace=workspace)
+    lib = _lib or load_library()
+    dev, here = _here(q)
+    shape, dtype = q.shape, q.dtype
+    n, Hq, d = shape
+    num_pages, page_size, Hkv = k_cache.shape[:3]
+    B, max_pages = block_table.shape
+    if tree_mask.dim() != 2:
+        raise OrthrosError(1, "tree_mask must be [n, words]")
+    words = tree_mask.shape[1]
+    max_new = max(min(n, 32 * words), 0) if max_new is None else _int32(max_new)
+    if out is None:
+        o = torch.empty_like(q)
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        oa, la = o.data_ptr(), lse.data_ptr()
+    else:
+        o, lse = out
+        oa, la = _block("o", o, dev, dtype, shape), _block("lse", lse, dev, torch.float32, (n, Hq))
+    if workspace is None:
+        ws = orthros_tree_attention_workspace_size(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype)
+        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=q.device)
+    pool = (num_pages, page_size, Hkv, d)
+    rc = lib.orthros_tree_attention(
+        _block("q", q, dev, dtype, shape), _index("q_indptr", q_indptr, dev, B + 1), _index("kv_lens", kv_lens, dev, B),
+        _block("tree_mask", tree_mask, dev, torch.int32, (n, words)), words, _block("k_cache", k_cache, dev, dtype, pool),
+        _block("v_cache", v_cache, dev, dtype, pool), _index("block_table", block_table, dev, B * max_pages), B, n, max_new, Hq,
+        Hkv, d, _int32(window), d ** -0.5 if scale is None else scale, _dtype(q), max_pages, page_size, num_pages, oa, la,
+        _addr(workspace, dev), workspace.numel(), here)
+    _raise_if(rc, lib)
+    return o, lse
+
+
+def orthros_tree_commit(k_cache, v_cache, block_table, q_indptr, kv_lens, accepted, n_accepted, *, out=None, workspace=None,
+                        stream=None):
+    """orthros_tree_commit of include/orthros_attn.h.
+
+    k_cache, v_cache [num_pages, page_size, Hkv, d], or [layers, ...] of all layers at once, updated in
+    place; accepted [B, most] int32, ascending tokens of each sequence's tree, of which the first
+    n_accepted [B] count. Returns the cached tokens after it [B]; `out`, a buffer other than kv_lens, may be
+    the one that the plan took as cache_lens: sequences that had no place in the step keep theirs.
+    """
+    if stream is not None:
+        with _on(stream):
+            return orthros_tree_commit(k_cache, v_cache, block_table, q_indptr, kv_lens, accepted, n_accepted, out=out,
+                                       workspace=workspace)
+    lib = _lib or load_library()
+    dev, here = _here(k_cache)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) not in (4, 5):
+        raise OrthrosError(1, "k_cache must be [num_pages, page_size, Hkv, d] or [layers, num_pages, page_size, Hkv, d]")
+    layers = shape[0] if len(shape) == 5 else 1
+    num_pages, page_size, Hkv, d = shape[-4:]
+    B, max_pages = block_table.shape
+    if accepted.dim() != 2:
+        raise OrthrosError(1, "accepted must be [B, most]")
+    most = accepted.shape[1]
+    if out is None:
+        out = torch.zeros(B, dtype=torch.int32, device=k_cache.device)
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=k_cache.device)
+    rc = lib.orthros_tree_commit(
+        _block("k_cache", k_cache, dev, dtype, shape), _block("v_cache", v_cache, dev, dtype, shape), layers,
+        _index("block_table", block_table, dev, B * max_pages), _index("q_indptr", q_indptr, dev, B + 1),
+        _index("kv_lens", kv_lens, dev, B), _block("accepted", accepted, dev, torch.int32, (B, most)),
+        _index("n_accepted", n_accepted, dev, B), most, B, Hkv, d, _dtype(k_cache), max_pages, page_size, num_pages,
+        _index("cache_lens", out, dev, B), _addr(workspace, dev), workspace.numel(), here)
+    if rc:
+        _raise_if(rc, lib)
+    return out
 
 
 def orthros_selftest_wait_timeout(limit_cycles, workspace, stream=None):

@@ -1,5 +1,6 @@
 // chunk_api.cu -- C entry points of the attention of new tokens over the paged
-// cache: argument checks, workspace carving, dispatch to chunk_attn.cu.
+// cache, consecutive ones or drafted trees: argument checks, workspace carving,
+// dispatch to chunk_attn.cu.
 #include <algorithm>
 #include <cmath>
 #include <numeric>
@@ -58,33 +59,21 @@ orthros_status check_shape(int B, int n, int max_new, int Hq, int Hkv, int d, in
     return ORTHROS_OK;
 }
 
-}  // namespace
-}  // namespace orthros
-
-using namespace orthros;
-
-extern "C" {
-
-size_t orthros_chunk_attention_workspace_size(int B, int n, int max_new, int Hq, int Hkv, int d, int max_pages,
-                                              int page_size, orthros_dtype dtype) {
-    if (check_shape(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype) != ORTHROS_OK) return 0;
-    return chunk_layout(B, n, std::min(max_new, n), Hq, Hkv, d).total;
-}
-
-orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, const int32_t *kv_lens,
-                                       const void *k_cache, const void *v_cache, const int32_t *block_table, int B,
-                                       int n, int max_new, int Hq, int Hkv, int d, int window, float scale,
-                                       orthros_dtype dtype, int max_pages, int page_size, int num_pages, void *o,
-                                       float *lse, void *workspace, size_t workspace_bytes, orthros_stream_t stream_) {
-    clear_error();
+// Both attentions: consecutive new tokens, or (tree) drafted trees with their masks.
+orthros_status attend(const void *q, const int32_t *q_indptr, const int32_t *kv_lens, const int32_t *tree_mask, bool tree, int words,
+                      const void *k_cache, const void *v_cache, const int32_t *block_table, int B, int n, int max_new, int Hq,
+                      int Hkv, int d, int window, float scale, orthros_dtype dtype, int max_pages, int page_size, int num_pages,
+                      void *o, float *lse, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (const orthros_status st = check_shape(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype); st != ORTHROS_OK)
         return st;
+    max_new = std::min(max_new, n);
+    if (tree) max_new = std::min(max_new, 32 * words);
     if (window < 1) return report_error(ORTHROS_EINVAL, "window = %d must be >= 1", window);
     if (!std::isfinite(scale) || !(scale > 0.f)) return report_error(ORTHROS_EINVAL, "scale must be finite and > 0");
     if (num_pages < 1) return report_error(ORTHROS_EINVAL, "num_pages = %d must be >= 1", num_pages);
     if ((long long)num_pages * page_size > 0x7fffffffLL - 128 || (long long)max_pages * page_size > 0x7fffffffLL - 128)
         return report_error(ORTHROS_EUNSUPPORTED, "a pool or block table of 2^31 token slots");
-    const ChunkLayout L = chunk_layout(B, n, std::min(max_new, n), Hq, Hkv, d);
+    const ChunkLayout L = chunk_layout(B, n, max_new, Hq, Hkv, d);
     if (!workspace || workspace_bytes < L.total)
         return report_error(ORTHROS_EWORKSPACE, "workspace needs %zu bytes, got %zu", L.total, workspace ? workspace_bytes : (size_t)0);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -93,10 +82,11 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
         if (!q || !o || !k_cache || !v_cache) return report_error(ORTHROS_EINVAL, "q, o, k_cache and v_cache must not be NULL");
         if (!q_indptr || !kv_lens || !block_table)
             return report_error(ORTHROS_EINVAL, "q_indptr, kv_lens and block_table must not be NULL");
+        if (tree && (!tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 3u)))
+            return report_error(ORTHROS_EINVAL, "tree_mask must not be NULL and 4-byte aligned");
         if (!aligned16(q) || !aligned16(o) || !aligned16(k_cache) || !aligned16(v_cache))
             return report_error(ORTHROS_EINVAL, "q, o, k_cache and v_cache must be 16-byte aligned");
     }
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (n == 0) {
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), stream);
@@ -111,7 +101,9 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
     p.block_table = block_table;
     p.B = B;
     p.n = n;
-    p.max_new = std::min(max_new, n);
+    p.max_new = max_new;
+    p.tree_mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    p.words = words;
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.window = window;
@@ -143,7 +135,49 @@ orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, c
     p.part_ml = reinterpret_cast<float2 *>(ws + L.ml_off);
     p.part_o = reinterpret_cast<float *>(ws + L.o_off);
     const cudaError_t e = launch_chunk_attention(p, d, stream);
-    return e == cudaSuccess ? ORTHROS_OK : report_error(ORTHROS_ECUDA, "chunk attention launch: %s", cudaGetErrorString(e));
+    return e == cudaSuccess ? ORTHROS_OK : report_error(ORTHROS_ECUDA, "attention launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace orthros
+
+using namespace orthros;
+
+extern "C" {
+
+size_t orthros_chunk_attention_workspace_size(int B, int n, int max_new, int Hq, int Hkv, int d, int max_pages,
+                                              int page_size, orthros_dtype dtype) {
+    if (check_shape(B, n, max_new, Hq, Hkv, d, max_pages, page_size, dtype) != ORTHROS_OK) return 0;
+    return chunk_layout(B, n, std::min(max_new, n), Hq, Hkv, d).total;
+}
+
+orthros_status orthros_chunk_attention(const void *q, const int32_t *q_indptr, const int32_t *kv_lens,
+                                       const void *k_cache, const void *v_cache, const int32_t *block_table, int B,
+                                       int n, int max_new, int Hq, int Hkv, int d, int window, float scale,
+                                       orthros_dtype dtype, int max_pages, int page_size, int num_pages, void *o,
+                                       float *lse, void *workspace, size_t workspace_bytes, orthros_stream_t stream) {
+    clear_error();
+    return attend(q, q_indptr, kv_lens, nullptr, false, 0, k_cache, v_cache, block_table, B, n, max_new, Hq, Hkv, d, window, scale,
+                  dtype, max_pages, page_size, num_pages, o, lse, workspace, workspace_bytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t orthros_tree_attention_workspace_size(int B, int n, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
+                                             orthros_dtype dtype) {
+    return orthros_chunk_attention_workspace_size(B, n, std::min(max_new, kTreeMaxTokens), Hq, Hkv, d, max_pages, page_size, dtype);
+}
+
+orthros_status orthros_tree_attention(const void *q, const int32_t *q_indptr, const int32_t *kv_lens, const int32_t *tree_mask,
+                                      int mask_words, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                                      int B, int n, int max_new, int Hq, int Hkv, int d, int window, float scale,
+                                      orthros_dtype dtype, int max_pages, int page_size, int num_pages, void *o, float *lse,
+                                      void *workspace, size_t workspace_bytes, orthros_stream_t stream) {
+    clear_error();
+    if (mask_words < 1 || mask_words > kTreeMaxTokens / 32)
+        return report_error(ORTHROS_EINVAL, "mask_words = %d must lie in [1, %d]", mask_words, kTreeMaxTokens / 32);
+    return attend(q, q_indptr, kv_lens, tree_mask, true, mask_words, k_cache, v_cache, block_table, B, n, max_new, Hq, Hkv, d,
+                  window, scale, dtype, max_pages, page_size, num_pages, o, lse, workspace, workspace_bytes,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -12,6 +12,11 @@
 // * g + head), so a key/value tile staged once serves g times as many rows and a
 // decoding token fills g rows instead of one.
 //
+// Trees (kTree). The new tokens of a sequence may be a drafted tree: token i then sees the cached
+// keys before the tree, in the window of its position, and the tokens of the tree that its mask
+// row names. Every unit of the sequence has the same keys; only tiles that reach the tree (or the
+// window's edge) take a mask, 32 keys a word, put together while the products run. The mask may leave a row without a key.
+//
 // Units and the split of the key axis. A unit is up to two row tiles of one
 // sequence and the key tiles (128 tokens) they see. The plan kernel lists the
 // units with the running count of their key tiles (at most 32 units are listed by
@@ -87,11 +92,16 @@ template <int D> struct Cfg {
 struct Segment {
     int end;                 // no more segments
     int b, kv, tok0, cnt;    // sequence, kv head, first token and tokens of the unit
-    int pos0;                // position of the unit's first token
+    int pos0;                // position of the unit's first token (tree: cached tokens before the tree)
     int kt0, nkt;            // key tiles kt0 .. kt0 + nkt - 1
     int pair;                // two row tiles (else both slots share one)
     int partial;             // partial index, or -1: the unit is complete here
     int lo[2], hi[2];        // pair: tiles of the run that slot s works on (lo > hi: none)
+};
+
+// What a tree's segment needs besides: the keys of the sequence, its first token.
+struct TreeSegment {
+    int key_end, seq0;
 };
 
 constexpr int kSegRing = 2;
@@ -112,6 +122,7 @@ struct Meta {
     int abort;
     volatile int bad[kFlagRing];  // per key tile (running count): its keys [bad >> 8, bad & 255) had page ids outside the pool
     Segment seg[kSegRing];
+    TreeSegment tree[kSegRing];
     float2 ml[kRows];             // slot 1's running max and sum, for slot 0 (shared row tile)
 };
 static_assert(sizeof(Meta) <= 2048, "barriers and metadata must fit their shared-memory region");
@@ -208,18 +219,62 @@ __device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0
     return new_tokens(p, p.q_indptr[b + 1] - tok0, len, wrong);
 }
 
-// The unit that begins at token i of a sequence's nb (i < nb).
-__device__ __forceinline__ ChunkUnit unit_at(const ChunkParams &p, int b, int tok0, int nb, int len, int i) {
+// The unit that begins at token i of a sequence's nb (i < nb). The tokens of a tree may all see
+// one another: every unit has all the sequence's keys from the window of the first position on.
+template <bool kTree> __device__ __forceinline__ ChunkUnit unit_at(const ChunkParams &p, int b, int tok0, int nb, int len, int i) {
     ChunkUnit u;
     u.b = b;
     u.tok0 = tok0 + i;
     u.cnt = min(2 * p.tile_tokens, nb - i);
-    u.pos0 = len - nb + i;
+    u.pos0 = kTree ? len - nb : len - nb + i;
+    if constexpr (kTree) u.key_end = len, u.seq0 = tok0;
     int hi;
-    key_tiles(u.pos0, u.pos0 + u.cnt - 1, p.window, u.kt_lo, hi);
+    key_tiles(u.pos0, kTree ? len - 1 : u.pos0 + u.cnt - 1, p.window, u.kt_lo, hi);
     u.n_kt = hi - u.kt_lo + 1;
     u.start = 0;
     return u;
+}
+
+// Drafted trees. Token i's mask row has a bit per token of its own sequence's tree; its position is
+// the number of them that it sees, itself among them, behind the cached ones.
+struct TreeRow {
+    const uint32_t *bits;  // the row's mask words
+    int words, tree0, nb;  // words, cached tokens before the tree (its first key), tokens of the tree
+    __device__ __forceinline__ uint32_t word(int i) const {
+        if (i < 0 || i >= words || 32 * i >= nb) return 0;
+        const uint32_t w = __ldg(bits + i);
+        return nb - 32 * i < 32 ? w & ((1u << (nb - 32 * i)) - 1) : w;
+    }
+    __device__ __forceinline__ int position() const {
+        int c = 0;
+        for (int i = 0; i < words; ++i) c += __popc(word(i));
+        return tree0 + max(c, 1) - 1;
+    }
+};
+// Which of the 32 keys from `key` on a row sees: cached ones from `lo` on, and its mask's tokens of
+// the tree that begins at row seq0 of q, where the window is shorter than the tree those within it.
+__device__ __forceinline__ uint32_t tree_seen(const ChunkParams &p, const TreeRow &t, int seq0, int key, int lo) {
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; };
+    uint32_t seen = below(t.tree0 - key) & ~below(lo - key);
+    const int o = key - t.tree0;  // the tree's token that key is
+    if (o <= -32 || o >= t.nb) return seen;
+    uint32_t in = __funnelshift_r(t.word(o >> 5), t.word((o >> 5) + 1), o & 31);
+    if (p.window < t.nb) {
+        const int first = t.position() - p.window + 1;
+        for (uint32_t left = in; left; left &= left - 1) {
+            const int c = __ffs(left) - 1;
+            const TreeRow k{p.tree_mask + (long long)(seq0 + o + c) * p.words, t.words, t.tree0, t.nb};
+            if (k.position() < first) in &= ~(1u << c);
+        }
+    }
+    return seen | in;
+}
+
+// What a row of a tree is scaled by: it may see no key at all, which is 0 (a sum of 0); a row that
+// saw only logits of -inf has a mark for a sum (kMark).
+constexpr float kMark = 1e-30f;
+__device__ __forceinline__ float inverse_tree(float m, float l) {
+    return m != -INFINITY ? inverse_sum(l) : l == 0.f ? 0.f : __int_as_float(0x7fc00000);
 }
 
 // ---------------------------------------------------------------------------
@@ -243,7 +298,7 @@ __device__ void fill_nan(const ChunkParams &p, long long tok0, long long tok1, i
         for (long long i = tok0 * p.Hq + tid; i < tok1 * p.Hq; i += nthreads) p.lse[i] = __int_as_float(0x7fc00000);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p, int d) {
+template <bool kTree> __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p, int d) {
     __shared__ long long wsum[2][32];
     __shared__ long long carry[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -254,7 +309,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
     }
     int bad = 0;
     for (int b = tid; b < p.B; b += kPlanThreads) bad |= p.q_indptr[b + 1] < p.q_indptr[b];
-    if (tid == 0) bad |= p.q_indptr[0] != 0 || p.q_indptr[p.B] != p.n;
+    if (tid == 0) bad |= p.q_indptr[0] != 0 || (kTree ? p.q_indptr[p.B] > p.n : p.q_indptr[p.B] != p.n);
     if (__syncthreads_or(bad)) {  // no token's sequence is known
         if (tid == 0) *p.plan = ChunkPlan{0, ORTHROS_DEV_BAD_LENGTH, 0};
         fill_nan(p, 0, p.n, d, tid, kPlanThreads);
@@ -270,7 +325,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
             fill_nan(p, tok0, p.q_indptr[b + 1], d, lane, 32);
         }
         long long tiles = 0;
-        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_at(p, b, tok0, nb, len, i).n_kt;
+        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_at<kTree>(p, b, tok0, nb, len, i).n_kt;
         tiles = warp_scan(tiles, lane);
         if (lane == 31) {
             p.seq_units[b] = (nb + ut - 1) / ut;
@@ -319,7 +374,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPar
         for (int i0 = 0; i0 < nb; i0 += 32 * ut) {
             const int i = i0 + lane * ut;
             ChunkUnit u{};
-            if (i < nb) u = unit_at(p, b, tok0, nb, len, i);
+            if (i < nb) u = unit_at<kTree>(p, b, tok0, nb, len, i);
             const long long sum = warp_scan(u.n_kt, lane);
             u.start = at + sum - u.n_kt;
             if (i < nb) p.units[u0 + i / ut] = u;
@@ -374,14 +429,14 @@ __device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
 
 // Whether key tile `it` of a segment has rows that none of its unit's tokens sees:
 // all but rows [r0, r1).
-__device__ __forceinline__ bool unseen_rows(const Segment &sg, int window, int it, int &r0, int &r1) {
+template <bool kTree> __device__ __forceinline__ bool unseen_rows(const Segment &sg, const TreeSegment &ts, int window, int it, int &r0, int &r1) {
     const int key0 = (sg.kt0 + it) * kKeys;
     r0 = max(0, max(0, sg.pos0 - window + 1) - key0);  // (in this order: a window may be INT_MAX)
-    r1 = min(kKeys, sg.pos0 + sg.cnt - key0);
+    r1 = min(kKeys, (kTree ? ts.key_end : sg.pos0 + sg.cnt) - key0);
     return r0 > 0 || r1 < kKeys;
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kBound, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
@@ -463,7 +518,7 @@ __global__ void __launch_bounds__(kBound, 1)
             const int b = one ? 0 : lane;
             bool wrong;
             const int nb = new_tokens(p, tok1 - tok0, len, wrong);
-            const bool order = __all_sync(0xffffffffu, tok1 >= tok0 && tok_first == 0 && tok_last == p.n);
+            const bool order = __all_sync(0xffffffffu, tok1 >= tok0 && tok_first == 0 && (kTree ? tok_last <= p.n : tok_last == p.n));
             if (!order || __any_sync(0xffffffffu, wrong)) {
                 // impossible lengths: NaN for their rows, or for all rows when no token's sequence is known
                 if (lane == 0 && blockIdx.x == 0) set_status(status, ORTHROS_DEV_BAD_LENGTH);
@@ -474,7 +529,7 @@ __global__ void __launch_bounds__(kBound, 1)
                 }
             }
             const int i = one ? lane * ut : 0;
-            if (order && i < nb) own = unit_at(p, b, tok0, nb, len, i);
+            if (order && i < nb) own = unit_at<kTree>(p, b, tok0, nb, len, i);
             const long long sum = warp_scan(own.n_kt, lane);
             own.start = sum - own.n_kt;
             pl.units = 32;
@@ -492,6 +547,10 @@ __global__ void __launch_bounds__(kBound, 1)
             r.kt_lo = __shfl_sync(0xffffffffu, own.kt_lo, u);
             r.n_kt = __shfl_sync(0xffffffffu, own.n_kt, u);
             r.start = __shfl_sync(0xffffffffu, own.start, u);
+            if constexpr (kTree) {
+                r.key_end = __shfl_sync(0xffffffffu, own.key_end, u);
+                r.seq0 = __shfl_sync(0xffffffffu, own.seq0, u);
+            }
             return r;
         };
         // unit that holds key tile x of the list
@@ -507,12 +566,13 @@ __global__ void __launch_bounds__(kBound, 1)
         uint32_t nq[2] = {0, 0};  // query tiles issued per slot
         int ring = 0;
         bool alive = true;
-        auto publish = [&](const Segment &sg) -> bool {
+        auto publish = [&](const Segment &sg, const TreeSegment &ts) -> bool {
             const int r = ring % kSegRing;
             if (ring >= kSegRing && !mbar_wait_warp(&mt.g_empty[r], ((ring / kSegRing) - 1) & 1, abort, status))
                 return false;
             if (lane == 0) {
                 mt.seg[r] = sg;
+                if constexpr (kTree) mt.tree[r] = ts;
                 mbar_arrive(&mt.g_full[r]);
             }
             __syncwarp();
@@ -560,6 +620,8 @@ __global__ void __launch_bounds__(kBound, 1)
                     sg.tok0 = un.tok0;
                     sg.cnt = un.cnt;
                     sg.pos0 = un.pos0;
+                    TreeSegment ts;
+                    if constexpr (kTree) ts.key_end = un.key_end, ts.seq0 = un.seq0;
                     sg.kt0 = un.kt_lo + a;
                     sg.nkt = n_tiles;
                     sg.pair = un.cnt > tt;
@@ -575,7 +637,7 @@ __global__ void __launch_bounds__(kBound, 1)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         int lo = 0, hi = n_tiles - 1;
-                        if (sg.pair) {
+                        if (!kTree && sg.pair) {
                             const int c0 = s * tt, c1 = s ? un.cnt : tt;
                             int kl, kh;
                             key_tiles(un.pos0 + c0, un.pos0 + c1 - 1, p.window, kl, kh);
@@ -585,7 +647,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         sg.lo[s] = lo;
                         sg.hi[s] = hi;
                     }
-                    if (!(alive = publish(sg))) break;
+                    if (!(alive = publish(sg, ts))) break;
                     // query tiles (rows past the tile's tokens keep whatever was there: their results are dropped)
                     for (int s = 0; alive && s < (sg.pair ? 2 : 1); ++s) {
                         if (nq[s] > 0 && !mbar_wait_warp(&mt.q_empty[s], (nq[s] - 1) & 1, abort, status)) {
@@ -604,7 +666,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     if (!alive) break;
                     // key/value tiles: keys [key_lo, key_hi] exist for this unit
                     const int32_t *bt = p.block_table + (long long)sg.b * p.max_pages;
-                    const int key_hi = un.pos0 + un.cnt - 1;
+                    const int key_hi = kTree ? un.key_end - 1 : un.pos0 + un.cnt - 1;
                     const int key_lo = max(0, un.pos0 - p.window + 1);
                     const int oob = p.num_pages * p.page_size;  // past the pool: the copy fills zeros
                     const int box = p.box;
@@ -653,7 +715,7 @@ __global__ void __launch_bounds__(kBound, 1)
                                 break;
                             }
                             int r0, r1;
-                            const bool edge = unseen_rows(sg, p.window, it, r0, r1);
+                            const bool edge = unseen_rows<kTree>(sg, ts, p.window, it, r0, r1);
                             uint64_t *full = edge ? &mt.ve_full[sv] : &mt.v_full[sv];
                             if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
                             __syncwarp();
@@ -707,7 +769,7 @@ __global__ void __launch_bounds__(kBound, 1)
         if (alive) {
             Segment sg{};
             sg.end = 1;
-            publish(sg);
+            publish(sg, TreeSegment{});
         }
         if (head_n > 0) {
             // the CTAs whose share begins inside the unit hold its other parts
@@ -901,13 +963,15 @@ __global__ void __launch_bounds__(kBound, 1)
             const int r = i % kSegRing;
             if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status)) break;
             const Segment sg = mt.seg[r];
+            TreeSegment ts;
+            if constexpr (kTree) ts = mt.tree[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&mt.g_empty[r]);
             if (sg.end) break;
             if (!p.box) continue;  // gathered rows come clean
             for (int it = 0; it < sg.nkt; ++it) {
                 int r0, r1;
-                if (!unseen_rows(sg, p.window, it, r0, r1)) continue;
+                if (!unseen_rows<kTree>(sg, ts, p.window, it, r0, r1)) continue;
                 const uint32_t sv = (gk + it) % kNumV;
                 if (!(ok = mbar_wait_warp(&mt.ve_full[sv], (ne >> sv) & 1, abort, status))) break;
                 ne ^= 1u << sv;
@@ -939,6 +1003,8 @@ __global__ void __launch_bounds__(kBound, 1)
             const int r = i % kSegRing;
             if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status)) break;
             const Segment sg = mt.seg[r];
+            TreeSegment ts;
+            if constexpr (kTree) ts = mt.tree[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&mt.g_empty[r]);
             if (sg.end) break;
@@ -948,13 +1014,35 @@ __global__ void __launch_bounds__(kBound, 1)
             const bool idle = (warp & 3) * 32 >= n_tok * g;          // no real row in this warp
             const int t_first = sg.pos0 + c0, t_last = t_first + n_tok - 1;
             const int t_row = mine ? t_first + row_token(p, row) : t_last;
-            const int lo_row = max(0, t_row - p.window + 1);
-            const int lo_max = max(0, t_last - p.window + 1);
+            const int lo_band = max(0, t_row - p.window + 1), lo_band_max = max(0, t_last - p.window + 1);
+            TreeRow tree;
+            int lo_tree = 0, lo_tree_max = 0;
+            bool saw = false;  // tree: a key
+            if constexpr (kTree) {
+                tree.bits = p.tree_mask + (long long)(sg.tok0 + c0 + (mine ? row_token(p, row) : 0)) * p.words;
+                tree.words = p.words, tree.tree0 = sg.pos0, tree.nb = ts.key_end - sg.pos0;
+                lo_tree = p.window >= ts.key_end ? 0 : max(0, tree.position() - p.window + 1);
+                lo_tree_max = max(0, ts.key_end - p.window);
+            }
+            const int lo_row = kTree ? lo_tree : lo_band, lo_max = kTree ? lo_tree_max : lo_band_max;
             const int it0 = sg.pair ? sg.lo[s] : s, step = sg.pair ? 1 : 2, it1 = sg.pair ? sg.hi[s] : sg.nkt - 1;
             const int tiles = it0 <= it1 ? (it1 - it0) / step + 1 : 0;
             float m_ref = -INFINITY, l = 0.f;
             bool ok = true, bad = false;
             for (int it = it0; it <= it1; it += step) {
+                uint32_t vis[4];  // tree: the keys of a masked tile that the row sees
+                bool masked = false;
+                if constexpr (kTree) {
+                    const int key0 = (sg.kt0 + it) * kKeys;
+                    masked = key0 + kKeys > sg.pos0 || key0 < lo_max;  // warp-uniform
+                    if (masked) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) vis[q] = tree_seen(p, tree, ts.seq0, key0 + 32 * q, lo_row);
+                        saw |= (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
+                    } else {
+                        saw = true;
+                    }
+                }
                 if (!(ok = mbar_wait_warp(&mt.s_full[s], cnt & 1, abort, status))) break;
                 ++cnt;
                 if (idle) {
@@ -965,7 +1053,19 @@ __global__ void __launch_bounds__(kBound, 1)
                 tc_fence_after();
                 const int key0 = (sg.kt0 + it) * kKeys;
                 const int no_page = mt.bad[(gk + it) % kFlagRing];
-                if (no_page && key0 + (no_page >> 8) <= t_row && key0 + (no_page & 255) > lo_row) bad = true;
+                if constexpr (kTree) {
+                    if (no_page) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int a = (no_page >> 8) - 32 * q, b = (no_page & 255) - 32 * q;  // keys [a, b) of these 32
+                            const uint32_t in = (b >= 32 ? 0xffffffffu : b <= 0 ? 0u : (1u << b) - 1) &
+                                                ~(a >= 32 ? 0xffffffffu : a <= 0 ? 0u : (1u << a) - 1);
+                            if (in & (masked ? vis[q] : 0xffffffffu)) bad = true;
+                        }
+                    }
+                } else {
+                    if (no_page && key0 + (no_page >> 8) <= t_row && key0 + (no_page & 255) > lo_row) bad = true;
+                }
                 uint32_t xr[kKeys];
                 using Cols = uint32_t[32];
                 const float *x = reinterpret_cast<const float *>(xr);
@@ -977,9 +1077,15 @@ __global__ void __launch_bounds__(kBound, 1)
                     for (int q = 0; q < kKeys / 32; ++q) reg_fence(*reinterpret_cast<Cols *>(xr + 32 * q));
                     // A loop of no or one turn, so that the compiler keeps a branch around the mask: as 128
                     // predicated selects it ran for every tile (ALU instructions 2.8-fold, the kernel 1.5-fold).
-                    int turns = key0 + kKeys - 1 > t_first || key0 < lo_max;  // warp-uniform
+                    int turns = kTree ? masked : key0 + kKeys - 1 > t_first || key0 < lo_max;  // warp-uniform
                     asm volatile("" : "+r"(turns));
                     for (; turns > 0; --turns) {
+                        if constexpr (kTree) {
+#pragma unroll
+                            for (int c = 0; c < kKeys; ++c)
+                                if (!(vis[c / 32] >> (c & 31) & 1)) xr[c] = __float_as_uint(-INFINITY);
+                            continue;
+                        }
                         const int first = key0 - lo_row;
                         const unsigned span = t_row - lo_row;
 #pragma unroll
@@ -1045,6 +1151,7 @@ __global__ void __launch_bounds__(kBound, 1)
                 mbar_arrive(&mt.p_full[s]);
             }
             if (!ok) break;
+            if (kTree && saw && m_ref == -INFINITY && l == 0.f) l = kMark;
             if (bad) l = __int_as_float(0x7fc00000);  // the row saw a page that does not exist: NaN
 
             // ---- epilogue ----
@@ -1075,7 +1182,7 @@ __global__ void __launch_bounds__(kBound, 1)
                     const float mb = m == -INFINITY ? 0.f : m * c2;
                     w0 = ex2(m_ref * c2 - mb);
                     w1 = ex2(o.x * c2 - mb);
-                    l = l * w0 + o.y * w1;
+                    l = kTree && m == -INFINITY ? l + o.y : l * w0 + o.y * w1;
                 }
             }
             if (!idle) {
@@ -1088,7 +1195,7 @@ __global__ void __launch_bounds__(kBound, 1)
                 const long long out = tok * p.Hq + h;  // row of o, or of the partials
                 const long long at = ((long long)sg.partial * p.slots_cap + (sg.pair ? s : 0)) * p.rows_cap + row;
                 if (fin) {
-                    const float inv = inverse_sum(l);
+                    const float inv = kTree ? inverse_tree(m, l) : inverse_sum(l);
                     w0 *= inv;
                     w1 *= inv;
                     if (mine && p.lse) p.lse[out] = m * p.scale + logf(l);
@@ -1170,7 +1277,7 @@ constexpr int kMergeRows = 32;    // a block per row up to so many rows of a par
 constexpr int kMergeBlocks = 16;  // blocks of a unit beyond
 
 // Running joint of parts of one row: kLanes lanes, lane l with channels 4 kLanes i + 4 l .. + 3, i < V.
-template <int V> struct Joint {
+template <int V, bool kTree> struct Joint {
     float M, L;
     float4 acc[V];
     __device__ __forceinline__ void clear() {
@@ -1183,7 +1290,7 @@ template <int V> struct Joint {
 #pragma unroll
         for (int k = 0; k < kParts; ++k) m = fmaxf(m, ml[k].x);
         const float mb = m == -INFINITY ? 0.f : m * c2;
-        const float w0 = ex2(M * c2 - mb);
+        const float w0 = kTree && m == -INFINITY ? 1.f : ex2(M * c2 - mb);
         M = m;
         L *= w0;
 #pragma unroll
@@ -1207,7 +1314,7 @@ template <int V> struct Joint {
     }
 };
 
-template <int D, bool kRowBlocks>
+template <int D, bool kRowBlocks, bool kTree>
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
     const int tid = threadIdx.x, g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1247,7 +1354,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
         for (int r = (blockIdx.y * kMergeWarps * 32 + tid) / kLanes; r < cap; r += gridDim.y * kMergeWarps * (32 / kLanes)) {
             const long long out = out_row(r);
             if (out < 0) continue;
-            Joint<V> jt;
+            Joint<V, kTree> jt;
             jt.clear();
             for (int k0 = 0; k0 < hd.n_parts; k0 += kParts) {
                 float2 ml[kParts];
@@ -1264,7 +1371,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
                 }
                 jt.add(ml, x, c2);
             }
-            const float inv = inverse_sum(jt.L);
+            const float inv = kTree ? inverse_tree(jt.M, jt.L) : inverse_sum(jt.L);
 #pragma unroll
             for (int i = 0; i < V; ++i) store(out, lane + i * kLanes, jt.acc[i], inv);
             if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
@@ -1278,7 +1385,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
         const int r = blockIdx.y;
         const long long out = out_row(r);
         if (out >= 0) {
-            Joint<1> jt;
+            Joint<1, kTree> jt;
             jt.clear();
             for (int k0 = sub; k0 < hd.n_parts; k0 += kSub * kParts) {
                 float2 ml[kParts];
@@ -1303,7 +1410,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
                 for (int k = 0; k < kSub; ++k) ml[k] = sub_ml[k], x[k][0] = sub_x[k][lane];
                 jt.clear();
                 jt.add(ml, x, c2);
-                const float inv = inverse_sum(jt.L);
+                const float inv = kTree ? inverse_tree(jt.M, jt.L) : inverse_sum(jt.L);
                 store(out, lane, jt.acc[0], inv);
                 if (lane == 0 && p.lse) p.lse[out] = jt.M * p.scale + logf(jt.L);
             }
@@ -1311,7 +1418,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
     }
 }
 
-template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
+template <int D, bool kTree> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     const long long tokens = p.box ? (long long)p.num_pages * p.page_size : 8;  // (unused maps are valid ones)
     const int box = p.box ? p.box : 8;
@@ -1319,10 +1426,10 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
         !encode_kv_groups_map(&tk, p.k, tokens, p.Hkv, D, box) || !encode_kv_groups_map(&tv, p.v, tokens, p.Hkv, D, box))
         return cudaErrorInvalidValue;
     static SmemLimit limit;
-    if (cudaError_t e = limit.ensure((const void *)chunk_attn_kernel<D>, Cfg<D>::kSmem); e != cudaSuccess) return e;
+    if (cudaError_t e = limit.ensure((const void *)chunk_attn_kernel<D, kTree>, Cfg<D>::kSmem); e != cudaSuccess) return e;
     if (!p.direct) {
         ProfScope ps("chunk_plan", stream);
-        chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, D);
+        chunk_plan_kernel<kTree><<<1, kPlanThreads, 0, stream>>>(p, D);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }
     // the attention's set-up overlaps the plan, the merge's launch the attention
@@ -1338,7 +1445,7 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
     cfg.numAttrs = p.direct ? 0 : 1;
     {
         ProfScope ps("chunk_attn", stream);
-        if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D>, tq, tk, tv, p); e != cudaSuccess) return e;
+        if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D, kTree>, tq, tk, tv, p); e != cudaSuccess) return e;
     }
     const int rows = p.slots_cap * p.rows_cap;
     cudaLaunchConfig_t mc = {};
@@ -1348,7 +1455,8 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
     mc.attrs = attr;
     mc.numAttrs = 1;
     ProfScope ps("chunk_merge", stream);
-    if (cudaError_t e = cudaLaunchKernelEx(&mc, rows <= kMergeRows ? chunk_merge_kernel<D, true> : chunk_merge_kernel<D, false>, p); e != cudaSuccess) return e;
+    if (cudaError_t e = cudaLaunchKernelEx(&mc, rows <= kMergeRows ? chunk_merge_kernel<D, true, kTree> : chunk_merge_kernel<D, false, kTree>, p); e != cudaSuccess)
+        return e;
     return cudaGetLastError();
 }
 
@@ -1357,7 +1465,8 @@ template <int D> cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream)
 long long chunk_max_units(long long n, int B, int tile_tokens) { return n / (2 * tile_tokens) + B; }
 
 cudaError_t launch_chunk_attention(const ChunkParams &p, int d, cudaStream_t stream) {
-    return d == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
+    if (p.tree_mask) return d == 128 ? launch_d<128, true>(p, stream) : launch_d<64, true>(p, stream);
+    return d == 128 ? launch_d<128, false>(p, stream) : launch_d<64, false>(p, stream);
 }
 
 }  // namespace orthros

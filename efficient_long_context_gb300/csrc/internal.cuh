@@ -293,6 +293,8 @@ struct RotateParams {
     int H, rot, heads_per_block;  // heads_per_block: set by the launcher
     bool interleaved;
     float amplitude;
+    float eps;                  // > 0: rows are normed before the affine
+    const float *weight;        // [d] of the norm, or null
     // append only: the output stream's queries, and the new tokens' keys and values
     const void *x_out;
     void *y_out;
@@ -302,6 +304,8 @@ struct RotateParams {
     int n_out;
     const void *k, *v;
     long long k_stride, v_stride;
+    const float *k_weight;      // the keys' norm
+    const int32_t *slots;       // [n] token slots in the pool, or null: from token_seq, positions and block_table
     const int32_t *token_seq, *block_table;
     void *k_cache, *v_cache;
     int Hkv, B, max_pages, page_size, num_pages;
@@ -322,14 +326,21 @@ struct RotateBwdParams {
     float *partial;  // [n_part, 2, H d] sums of the affine's gradient per block of tokens
     int n_part;
     float *d_alpha, *d_beta;  // both null: not wanted
+    float eps;                // > 0: rows were normed
+    const float *weight;      // [d] or null
+    float *partial_w;         // [groups, n_part, d] sums of the weight's gradient per block, or null
+    float *d_weight;          // [d] or null
 };
+int rotate_grad_groups(int H, int d, int elem_bytes);
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes);
+cudaError_t launch_norm_grad_sum(const RotateBwdParams &p, int d, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t stream);
 cudaError_t launch_rotate_append(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 
-// chunk_attn.cu: attention of new tokens over the paged cache (orthros_chunk_attention).
+// chunk_attn.cu: attention of new tokens over the paged cache (orthros_chunk_attention,
+// orthros_tree_attention).
 // A unit is up to two 128-row query tiles of one sequence (a row is one query
 // head of a GQA group at one token) that read the same key/value tiles; the
 // plan lists the units of the batch once, for one kv head.
@@ -337,6 +348,7 @@ struct ChunkUnit {
     int b, tok0, cnt, pos0;  // sequence, first token (row of q), tokens, position of the first one
     int kt_lo, n_kt;         // key tiles the unit's tokens see
     long long start;         // key tiles of the units before it
+    int key_end, seq0;       // tree: keys of the sequence, its first token
 };
 struct ChunkPlan {
     int units;
@@ -356,6 +368,8 @@ struct ChunkParams {
     const int32_t *q_indptr;         // device [B + 1]
     const int32_t *kv_lens;          // device [B]
     const int32_t *block_table;      // [B, max_pages]
+    const uint32_t *tree_mask;       // [n, words]: the new tokens are drafted trees; null: consecutive ones
+    int words;
     int B, n, max_new, Hq, Hkv, window, max_pages, page_size, num_pages;
     int tile_tokens;                 // tokens of a 128-row tile: 128 / (Hq / Hkv)
     int g_inv;                       // 65536 / (Hq / Hkv) + 1: row / g = row * g_inv >> 16
@@ -426,5 +440,31 @@ cudaError_t launch_prefill_cache_fill(const void *k, const void *v, void *k_cach
 // cache.cu: chunked prefill helpers (output-row positions per chunk, status fold).
 cudaError_t launch_shift_positions(const int32_t *src, int32_t *dst, int n, int off, cudaStream_t stream);
 cudaError_t launch_fold_status(uint32_t *dst, const uint32_t *src, int n, int stride_words, cudaStream_t stream);
+
+// step_plan.cu: what a serving step needs from its lengths (orthros_plan_step), and the move of an
+// accepted path (orthros_tree_commit).
+constexpr int kPlanMaxSeqs = 8192;   // sequences of a plan: their prefix sums lie in shared memory
+constexpr int kTreeMaxTokens = 256;  // of a drafted tree
+struct StepPlanParams {
+    const int32_t *cache_lens, *new_lens;    // [B]
+    const int32_t *held_in, *count_in;       // [B], [1]
+    const int32_t *parents;                  // [n] or null
+    int32_t *free_pages, *block_table;       // [num_pages], [B, max_pages]
+    int32_t *q_indptr, *kv_lens, *lens_out, *held_out, *count_out;  // lens_out may be null
+    int32_t *token_seq, *token_pos, *token_slots;  // [n]
+    uint32_t *tree_mask;                     // [n, words]
+    int B, n, max_pages, page_size, num_pages, max_tree, words;
+    uint32_t *status;
+};
+cudaError_t launch_step_plan(const StepPlanParams &p, cudaStream_t stream);
+
+struct TreeCommitParams {
+    uint8_t *k_cache, *v_cache;  // [layers, num_pages, page_size] rows of row_bytes
+    const int32_t *block_table, *q_indptr, *kv_lens, *accepted, *n_accepted;
+    int32_t *cache_lens;
+    int layers, B, most, max_pages, page_size, num_pages, row_bytes;
+    uint32_t *status;
+};
+cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t stream);
 
 }  // namespace orthros

@@ -1,5 +1,6 @@
-// rotary_api.cu -- C entry points of the rotary positions: argument checks,
-// the host-side frequency rules, dispatch to rotary.cu.
+// rotary_api.cu -- C entry points of the rotary positions, with or without a norm
+// of the head: argument checks, the host-side frequency rules, dispatch to
+// rotary.cu.
 #include <cmath>
 
 #include "internal.cuh"
@@ -77,6 +78,233 @@ orthros_status cuda_error(cudaError_t e, const char *what) {
     return report_error(ORTHROS_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// The norm of a call that has one.
+orthros_status check_norm(const char *name, const float *weight, float eps) {
+    if (!std::isfinite(eps) || !(eps > 0.f)) return report_error(ORTHROS_EINVAL, "eps must be finite and > 0");
+    if (!aligned16(weight)) return report_error(ORTHROS_EINVAL, "%s must be 16-byte aligned", name);
+    return ORTHROS_OK;
+}
+
+// orthros_rotate, or with eps > 0 orthros_norm_rotate.
+orthros_status rotate_rows(const void *x, long long x_stride, const int32_t *positions, const float *weight, float eps,
+                           const float *alpha, const float *beta, const uint64_t *steps, int rot_dim, orthros_rope_layout layout,
+                           float amplitude, int n, int H, int d, orthros_dtype dtype, void *y, long long y_stride,
+                           cudaStream_t stream, const char *name) {
+    ORTHROS_TRY(check_rotation(n, H, d, dtype, steps, rot_dim, layout, amplitude));
+    ORTHROS_TRY(check_affine("", alpha, beta));
+    if (n == 0) return ORTHROS_OK;
+    ORTHROS_TRY(check_rows("x", x, x_stride, H, d, dtype, false));
+    ORTHROS_TRY(check_rows("y", y, y_stride, H, d, dtype, true));
+    if (x == y && x_stride != y_stride) return report_error(ORTHROS_EINVAL, "in place, x_stride and y_stride must agree");
+    if (!positions) return report_error(ORTHROS_EINVAL, "positions must not be NULL");
+    RotateParams p{};
+    p.x = x;
+    p.y = y;
+    p.x_stride = x_stride;
+    p.y_stride = y_stride;
+    p.positions = positions;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.steps = steps;
+    p.n = n;
+    p.H = H;
+    p.rot = rot_dim;
+    p.interleaved = layout == ORTHROS_ROPE_INTERLEAVED;
+    p.amplitude = amplitude;
+    p.eps = eps;
+    p.weight = weight;
+    ProfScope ps(name, stream);
+    const cudaError_t e = launch_rotate(p, d, dtype, stream);
+    return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, name);
+}
+
+// Where the gradient sums of a backward call lie in its workspace.
+struct GradLayout {
+    int parts;
+    size_t weight_off, total;
+};
+GradLayout grad_layout(int n, int H, int d, orthros_dtype dtype, bool norm) {
+    GradLayout L;
+    L.parts = rotate_grad_parts(n, H, d, elem_bytes(dtype));
+    L.weight_off = L.total = align_up((size_t)L.parts * 2 * H * d * sizeof(float), 256);
+    if (norm) L.total += align_up((size_t)rotate_grad_groups(H, d, elem_bytes(dtype)) * L.parts * d * sizeof(float), 256);
+    return L;
+}
+bool grad_shape_ok(int n, int H, int d, orthros_dtype dtype) {
+    return n >= 0 && H >= 1 && H <= 65536 && (d == 64 || d == 128) && (dtype == ORTHROS_BF16 || dtype == ORTHROS_F32);
+}
+
+// orthros_rotate_backward, or with eps > 0 orthros_norm_rotate_backward.
+orthros_status rotate_rows_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                    const int32_t *positions, const float *weight, float eps, const float *alpha,
+                                    const uint64_t *steps, int rot_dim, orthros_rope_layout layout, float amplitude, int n,
+                                    int H, int d, orthros_dtype dtype, void *dx, long long dx_stride, float *d_weight,
+                                    float *d_alpha, float *d_beta, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const bool norm = eps > 0.f, grads = d_alpha || d_weight;
+    ORTHROS_TRY(check_rotation(n, H, d, dtype, steps, rot_dim, layout, amplitude));
+    if (!aligned16(alpha)) return report_error(ORTHROS_EINVAL, "alpha must be 16-byte aligned");
+    if ((d_alpha == nullptr) != (d_beta == nullptr)) return report_error(ORTHROS_EINVAL, "d_alpha and d_beta: both or neither");
+    const GradLayout L = grad_layout(n, H, d, dtype, norm);
+    if (grads && (!workspace || workspace_bytes < L.total))
+        return report_error(ORTHROS_EWORKSPACE, "workspace needs %zu bytes, got %zu", L.total, workspace ? workspace_bytes : (size_t)0);
+    if (grads && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return report_error(ORTHROS_EINVAL, "workspace must be 256-byte aligned");
+    if (n == 0) {
+        cudaError_t e = cudaSuccess;
+        if (d_alpha) e = cudaMemsetAsync(d_alpha, 0, sizeof(float) * (size_t)H * d, stream);
+        if (d_beta && e == cudaSuccess) e = cudaMemsetAsync(d_beta, 0, sizeof(float) * (size_t)H * d, stream);
+        if (d_weight && e == cudaSuccess) e = cudaMemsetAsync(d_weight, 0, sizeof(float) * (size_t)d, stream);
+        return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "empty gradient");
+    }
+    ORTHROS_TRY(check_rows("dy", dy, dy_stride, H, d, dtype, false));
+    ORTHROS_TRY(check_rows("dx", dx, dx_stride, H, d, dtype, true));
+    if (norm || d_alpha) ORTHROS_TRY(check_rows("x", x, x_stride, H, d, dtype, false));
+    if (dx == dy && dx_stride != dy_stride) return report_error(ORTHROS_EINVAL, "in place, dy_stride and dx_stride must agree");
+    if (!positions) return report_error(ORTHROS_EINVAL, "positions must not be NULL");
+    RotateBwdParams p{};
+    p.dy = dy;
+    p.x = x;
+    p.dx = dx;
+    p.dy_stride = dy_stride;
+    p.x_stride = x_stride;
+    p.dx_stride = dx_stride;
+    p.positions = positions;
+    p.alpha = alpha;
+    p.steps = steps;
+    p.n = n;
+    p.H = H;
+    p.rot = rot_dim;
+    p.interleaved = layout == ORTHROS_ROPE_INTERLEAVED;
+    p.amplitude = amplitude;
+    p.partial = static_cast<float *>(workspace);
+    p.n_part = L.parts;
+    p.d_alpha = d_alpha;
+    p.d_beta = d_beta;
+    p.eps = eps;
+    p.weight = weight;
+    p.d_weight = d_weight;
+    if (d_weight) p.partial_w = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.weight_off);
+    {
+        ProfScope ps(norm ? "norm_rotate_backward" : "rotate_backward", stream);
+        const cudaError_t e = launch_rotate_backward(p, d, dtype, stream);
+        if (e != cudaSuccess) return cuda_error(e, "rotate backward launch");
+    }
+    if (grads) {
+        ProfScope ps(norm ? "norm_grad_sum" : "rotate_grad_sum", stream);
+        const cudaError_t e = norm ? launch_norm_grad_sum(p, d, elem_bytes(dtype), stream) : launch_rotate_grad_sum(p, d, stream);
+        if (e != cudaSuccess) return cuda_error(e, "gradient sum launch");
+    }
+    return ORTHROS_OK;
+}
+
+// What the two appends have in common. Token slots come from `slots`, or, when that is
+// null, from token_seq, token_pos and the block table.
+struct AppendArgs {
+    const void *q, *q_out, *k, *v;
+    long long q_stride, q_out_stride, k_stride, v_stride;
+    const float *q_weight, *k_weight;
+    float eps;
+    const float *alpha_base, *beta_base, *alpha_out, *beta_out;
+    const uint64_t *steps;
+    int rot_dim;
+    orthros_rope_layout layout;
+    float amplitude;
+    const int32_t *slots, *token_seq, *token_pos, *out_positions;
+    int n_new, n_out, Hq, Hkv, d;
+    orthros_dtype dtype;
+    void *q_rot, *q_out_rot, *k_cache, *v_cache;
+    const int32_t *block_table;
+    int B, max_pages, page_size, num_pages;
+    void *workspace;
+    size_t workspace_bytes;
+};
+orthros_status append_rows(const AppendArgs &a, bool by_slot, cudaStream_t stream, const char *name) {
+    if (a.n_out < 0) return report_error(ORTHROS_EINVAL, "n_out = %d must be >= 0", a.n_out);
+    if (a.Hkv < 1 || a.Hkv > 65536) return report_error(ORTHROS_EINVAL, "Hkv = %d must lie in [1, 65536]", a.Hkv);
+    ORTHROS_TRY(check_rotation(a.n_new, a.Hq, a.d, a.dtype, a.n_new + (long long)a.n_out > 0 ? a.steps : nullptr, a.rot_dim,
+                               a.layout, a.amplitude));
+    if (a.n_out > 0 && !a.steps) return report_error(ORTHROS_EINVAL, "steps must not be NULL");
+    if ((long long)a.n_new + a.n_out > 0x7fffffffLL)
+        return report_error(ORTHROS_EUNSUPPORTED, "%lld rows exceed 2^31 - 1", (long long)a.n_new + a.n_out);
+    ORTHROS_TRY(check_affine("_base", a.alpha_base, a.beta_base));
+    ORTHROS_TRY(check_affine("_out", a.alpha_out, a.beta_out));
+    if (!a.workspace || a.workspace_bytes < kStatusBytes)
+        return report_error(ORTHROS_EWORKSPACE, "workspace needs %zu bytes", kStatusBytes);
+    if ((reinterpret_cast<uintptr_t>(a.workspace) & 255u) != 0)
+        return report_error(ORTHROS_EINVAL, "workspace must be 256-byte aligned");
+    if (a.n_new > 0) {
+        ORTHROS_TRY(check_rows("k_new", a.k, a.k_stride, a.Hkv, a.d, a.dtype, false));
+        ORTHROS_TRY(check_rows("v_new", a.v, a.v_stride, a.Hkv, a.d, a.dtype, false));
+        if (a.q) {
+            ORTHROS_TRY(check_rows("q", a.q, a.q_stride, a.Hq, a.d, a.dtype, false));
+            if (!a.q_rot || !aligned16(a.q_rot)) return report_error(ORTHROS_EINVAL, "q_rot must not be NULL and 16-byte aligned");
+        }
+        if (by_slot) {
+            if (!a.slots || !a.token_pos || !a.k_cache || !a.v_cache)
+                return report_error(ORTHROS_EINVAL, "k_cache, v_cache, token_slots and token_pos must not be NULL");
+        } else if (!a.token_seq || !a.token_pos || !a.block_table || !a.k_cache || !a.v_cache) {
+            return report_error(ORTHROS_EINVAL, "k_cache, v_cache, block_table, token_seq and token_pos must not be NULL");
+        }
+        if (!aligned16(a.k_cache) || !aligned16(a.v_cache))
+            return report_error(ORTHROS_EINVAL, "k_cache and v_cache must be 16-byte aligned");
+        if ((!by_slot && (a.B < 1 || a.max_pages < 1)) || a.page_size < 1 || a.num_pages < 1)
+            return report_error(ORTHROS_EINVAL, by_slot ? "page_size and num_pages must be >= 1"
+                                                        : "B, max_pages, page_size and num_pages must be >= 1");
+    }
+    if (a.n_out > 0) {
+        ORTHROS_TRY(check_rows("q_out", a.q_out, a.q_out_stride, a.Hq, a.d, a.dtype, false));
+        if (!a.q_out_rot || !aligned16(a.q_out_rot)) return report_error(ORTHROS_EINVAL, "q_out_rot must not be NULL and 16-byte aligned");
+        if (!a.out_positions) return report_error(ORTHROS_EINVAL, "out_positions must not be NULL when n_out > 0");
+    }
+    uint32_t *status = static_cast<uint32_t *>(a.workspace);
+    if (a.n_new == 0 && a.n_out == 0) {
+        const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(uint32_t), stream);
+        return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "status reset");
+    }
+    RotateParams p{};
+    p.x = a.q;
+    p.y = a.q_rot;
+    p.x_stride = a.q_stride;
+    p.y_stride = (long long)a.Hq * a.d;
+    p.positions = a.token_pos;
+    p.alpha = a.alpha_base;
+    p.beta = a.beta_base;
+    p.steps = a.steps;
+    p.n = a.n_new;
+    p.H = a.Hq;
+    p.rot = a.rot_dim;
+    p.interleaved = a.layout == ORTHROS_ROPE_INTERLEAVED;
+    p.amplitude = a.amplitude;
+    p.eps = a.eps;
+    p.weight = a.q_weight;
+    p.k_weight = a.k_weight;
+    p.x_out = a.q_out;
+    p.y_out = a.q_out_rot;
+    p.x_out_stride = a.q_out_stride;
+    p.alpha_out = a.alpha_out;
+    p.beta_out = a.beta_out;
+    p.out_positions = a.out_positions;
+    p.n_out = a.n_out;
+    p.k = a.k;
+    p.v = a.v;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.slots = a.slots;
+    p.token_seq = a.token_seq;
+    p.block_table = a.block_table;
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.Hkv = a.Hkv;
+    p.B = a.B;
+    p.max_pages = a.max_pages;
+    p.page_size = a.page_size;
+    p.num_pages = a.num_pages;
+    p.status = status;
+    ProfScope ps(name, stream);
+    const cudaError_t e = launch_rotate_append(p, a.d, a.dtype, stream);
+    return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, name);
+}
+
 }  // namespace
 }  // namespace orthros
 
@@ -129,99 +357,52 @@ orthros_status orthros_rotary_steps(const double *freq, int n, uint64_t *steps) 
 orthros_status orthros_rotate(const void *x, long long x_stride, const int32_t *positions, const float *alpha,
                               const float *beta, const uint64_t *steps, int rot_dim, orthros_rope_layout layout,
                               float amplitude, int n, int H, int d, orthros_dtype dtype, void *y, long long y_stride,
-                              orthros_stream_t stream_) {
+                              orthros_stream_t stream) {
     clear_error();
-    ORTHROS_TRY(check_rotation(n, H, d, dtype, steps, rot_dim, layout, amplitude));
-    ORTHROS_TRY(check_affine("", alpha, beta));
-    if (n == 0) return ORTHROS_OK;
-    ORTHROS_TRY(check_rows("x", x, x_stride, H, d, dtype, false));
-    ORTHROS_TRY(check_rows("y", y, y_stride, H, d, dtype, true));
-    if (x == y && x_stride != y_stride) return report_error(ORTHROS_EINVAL, "in place, x_stride and y_stride must agree");
-    if (!positions) return report_error(ORTHROS_EINVAL, "positions must not be NULL");
-    RotateParams p{};
-    p.x = x;
-    p.y = y;
-    p.x_stride = x_stride;
-    p.y_stride = y_stride;
-    p.positions = positions;
-    p.alpha = alpha;
-    p.beta = beta;
-    p.steps = steps;
-    p.n = n;
-    p.H = H;
-    p.rot = rot_dim;
-    p.interleaved = layout == ORTHROS_ROPE_INTERLEAVED;
-    p.amplitude = amplitude;
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    ProfScope ps("rotate", stream);
-    const cudaError_t e = launch_rotate(p, d, dtype, stream);
-    return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "rotate launch");
+    return rotate_rows(x, x_stride, positions, nullptr, 0.f, alpha, beta, steps, rot_dim, layout, amplitude, n, H, d, dtype, y,
+                       y_stride, reinterpret_cast<cudaStream_t>(stream), "rotate");
+}
+
+orthros_status orthros_norm_rotate(const void *x, long long x_stride, const int32_t *positions, const float *weight, float eps,
+                                   const float *alpha, const float *beta, const uint64_t *steps, int rot_dim,
+                                   orthros_rope_layout layout, float amplitude, int n, int H, int d, orthros_dtype dtype,
+                                   void *y, long long y_stride, orthros_stream_t stream) {
+    clear_error();
+    ORTHROS_TRY(check_norm("weight", weight, eps));
+    return rotate_rows(x, x_stride, positions, weight, eps, alpha, beta, steps, rot_dim, layout, amplitude, n, H, d, dtype, y,
+                       y_stride, reinterpret_cast<cudaStream_t>(stream), "norm_rotate");
 }
 
 size_t orthros_rotate_backward_workspace_size(int n, int H, int d, orthros_dtype dtype) {
-    if (n < 0 || H < 1 || H > 65536 || (d != 64 && d != 128) || (dtype != ORTHROS_BF16 && dtype != ORTHROS_F32)) return 0;
-    return align_up((size_t)rotate_grad_parts(n, H, d, elem_bytes(dtype)) * 2 * H * d * sizeof(float), 256);
+    return grad_shape_ok(n, H, d, dtype) ? grad_layout(n, H, d, dtype, false).total : 0;
+}
+
+size_t orthros_norm_rotate_backward_workspace_size(int n, int H, int d, orthros_dtype dtype) {
+    return grad_shape_ok(n, H, d, dtype) ? grad_layout(n, H, d, dtype, true).total : 0;
 }
 
 orthros_status orthros_rotate_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
                                        const int32_t *positions, const float *alpha, const uint64_t *steps, int rot_dim,
                                        orthros_rope_layout layout, float amplitude, int n, int H, int d,
                                        orthros_dtype dtype, void *dx, long long dx_stride, float *d_alpha,
-                                       float *d_beta, void *workspace, size_t workspace_bytes,
-                                       orthros_stream_t stream_) {
+                                       float *d_beta, void *workspace, size_t workspace_bytes, orthros_stream_t stream) {
     clear_error();
-    ORTHROS_TRY(check_rotation(n, H, d, dtype, steps, rot_dim, layout, amplitude));
-    if (!aligned16(alpha)) return report_error(ORTHROS_EINVAL, "alpha must be 16-byte aligned");
-    if ((d_alpha == nullptr) != (d_beta == nullptr)) return report_error(ORTHROS_EINVAL, "d_alpha and d_beta: both or neither");
-    const size_t need = orthros_rotate_backward_workspace_size(n, H, d, dtype);
-    if (d_alpha && (!workspace || workspace_bytes < need))
-        return report_error(ORTHROS_EWORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : (size_t)0);
-    if (d_alpha && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return report_error(ORTHROS_EINVAL, "workspace must be 256-byte aligned");
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (n == 0) {
-        if (d_alpha) {
-            cudaError_t e = cudaMemsetAsync(d_alpha, 0, sizeof(float) * (size_t)H * d, stream);
-            if (e == cudaSuccess) e = cudaMemsetAsync(d_beta, 0, sizeof(float) * (size_t)H * d, stream);
-            if (e != cudaSuccess) return cuda_error(e, "empty gradient");
-        }
-        return ORTHROS_OK;
-    }
-    ORTHROS_TRY(check_rows("dy", dy, dy_stride, H, d, dtype, false));
-    ORTHROS_TRY(check_rows("dx", dx, dx_stride, H, d, dtype, true));
-    if (d_alpha) ORTHROS_TRY(check_rows("x", x, x_stride, H, d, dtype, false));
-    if (dx == dy && dx_stride != dy_stride) return report_error(ORTHROS_EINVAL, "in place, dy_stride and dx_stride must agree");
-    if (!positions) return report_error(ORTHROS_EINVAL, "positions must not be NULL");
-    RotateBwdParams p{};
-    p.dy = dy;
-    p.x = x;
-    p.dx = dx;
-    p.dy_stride = dy_stride;
-    p.x_stride = x_stride;
-    p.dx_stride = dx_stride;
-    p.positions = positions;
-    p.alpha = alpha;
-    p.steps = steps;
-    p.n = n;
-    p.H = H;
-    p.rot = rot_dim;
-    p.interleaved = layout == ORTHROS_ROPE_INTERLEAVED;
-    p.amplitude = amplitude;
-    p.partial = static_cast<float *>(workspace);
-    p.n_part = rotate_grad_parts(n, H, d, elem_bytes(dtype));
-    p.d_alpha = d_alpha;
-    p.d_beta = d_beta;
-    {
-        ProfScope ps("rotate_backward", stream);
-        const cudaError_t e = launch_rotate_backward(p, d, dtype, stream);
-        if (e != cudaSuccess) return cuda_error(e, "rotate backward launch");
-    }
-    if (d_alpha) {
-        ProfScope ps("rotate_grad_sum", stream);
-        const cudaError_t e = launch_rotate_grad_sum(p, d, stream);
-        if (e != cudaSuccess) return cuda_error(e, "affine gradient launch");
-    }
-    return ORTHROS_OK;
+    return rotate_rows_backward(dy, dy_stride, x, x_stride, positions, nullptr, 0.f, alpha, steps, rot_dim, layout, amplitude, n,
+                                H, d, dtype, dx, dx_stride, nullptr, d_alpha, d_beta, workspace, workspace_bytes,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+orthros_status orthros_norm_rotate_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                            const int32_t *positions, const float *weight, float eps, const float *alpha,
+                                            const uint64_t *steps, int rot_dim, orthros_rope_layout layout, float amplitude,
+                                            int n, int H, int d, orthros_dtype dtype, void *dx, long long dx_stride,
+                                            float *d_weight, float *d_alpha, float *d_beta, void *workspace,
+                                            size_t workspace_bytes, orthros_stream_t stream) {
+    clear_error();
+    ORTHROS_TRY(check_norm("weight", weight, eps));
+    return rotate_rows_backward(dy, dy_stride, x, x_stride, positions, weight, eps, alpha, steps, rot_dim, layout, amplitude, n, H,
+                                d, dtype, dx, dx_stride, d_weight, d_alpha, d_beta, workspace, workspace_bytes,
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 orthros_status orthros_rotate_append(
@@ -231,83 +412,35 @@ orthros_status orthros_rotate_append(
     const int32_t *token_seq, const int32_t *token_pos, const int32_t *out_positions, int n_new, int n_out, int Hq,
     int Hkv, int d, orthros_dtype dtype, void *q_rot, void *q_out_rot, void *k_cache, void *v_cache,
     const int32_t *block_table, int B, int max_pages, int page_size, int num_pages, void *workspace,
-    size_t workspace_bytes, orthros_stream_t stream_) {
+    size_t workspace_bytes, orthros_stream_t stream) {
     clear_error();
-    if (n_out < 0) return report_error(ORTHROS_EINVAL, "n_out = %d must be >= 0", n_out);
-    if (Hkv < 1 || Hkv > 65536) return report_error(ORTHROS_EINVAL, "Hkv = %d must lie in [1, 65536]", Hkv);
-    ORTHROS_TRY(check_rotation(n_new, Hq, d, dtype, n_new + (long long)n_out > 0 ? steps : nullptr, rot_dim, layout, amplitude));
-    if (n_out > 0 && !steps) return report_error(ORTHROS_EINVAL, "steps must not be NULL");
-    if ((long long)n_new + n_out > 0x7fffffffLL)
-        return report_error(ORTHROS_EUNSUPPORTED, "%lld rows exceed 2^31 - 1", (long long)n_new + n_out);
-    ORTHROS_TRY(check_affine("_base", alpha_base, beta_base));
-    ORTHROS_TRY(check_affine("_out", alpha_out, beta_out));
-    if (!workspace || workspace_bytes < kStatusBytes)
-        return report_error(ORTHROS_EWORKSPACE, "workspace needs %zu bytes", kStatusBytes);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return report_error(ORTHROS_EINVAL, "workspace must be 256-byte aligned");
-    if (n_new > 0) {
-        ORTHROS_TRY(check_rows("k_new", k_new, k_stride, Hkv, d, dtype, false));
-        ORTHROS_TRY(check_rows("v_new", v_new, v_stride, Hkv, d, dtype, false));
-        if (q) {
-            ORTHROS_TRY(check_rows("q", q, q_stride, Hq, d, dtype, false));
-            if (!q_rot || !aligned16(q_rot)) return report_error(ORTHROS_EINVAL, "q_rot must not be NULL and 16-byte aligned");
-        }
-        if (!token_seq || !token_pos || !block_table || !k_cache || !v_cache)
-            return report_error(ORTHROS_EINVAL, "k_cache, v_cache, block_table, token_seq and token_pos must not be NULL");
-        if (!aligned16(k_cache) || !aligned16(v_cache))
-            return report_error(ORTHROS_EINVAL, "k_cache and v_cache must be 16-byte aligned");
-        if (B < 1 || max_pages < 1 || page_size < 1 || num_pages < 1)
-            return report_error(ORTHROS_EINVAL, "B, max_pages, page_size and num_pages must be >= 1");
+    const AppendArgs a{q, q_out, k_new, v_new, q_stride, q_out_stride, k_stride, v_stride, nullptr, nullptr, 0.f, alpha_base,
+                       beta_base, alpha_out, beta_out, steps, rot_dim, layout, amplitude, nullptr, token_seq, token_pos,
+                       out_positions, n_new, n_out, Hq, Hkv, d, dtype, q_rot, q_out_rot, k_cache, v_cache, block_table, B,
+                       max_pages, page_size, num_pages, workspace, workspace_bytes};
+    return append_rows(a, false, reinterpret_cast<cudaStream_t>(stream), "rotate_append");
+}
+
+orthros_status orthros_norm_rotate_append(
+    const void *q, long long q_stride, const void *q_out, long long q_out_stride, const void *k_new, long long k_stride,
+    const void *v_new, long long v_stride, const float *q_weight, const float *k_weight, float eps, const float *alpha_base,
+    const float *beta_base, const float *alpha_out, const float *beta_out, const uint64_t *steps, int rot_dim,
+    orthros_rope_layout layout, float amplitude, const int32_t *token_slots, const int32_t *token_pos,
+    const int32_t *out_positions, int n_new, int n_out, int Hq, int Hkv, int d, orthros_dtype dtype, void *q_rot,
+    void *q_out_rot, void *k_cache, void *v_cache, int page_size, int num_pages, void *workspace, size_t workspace_bytes,
+    orthros_stream_t stream) {
+    clear_error();
+    if (eps == 0.f) {
+        if (q_weight || k_weight) return report_error(ORTHROS_EINVAL, "eps = 0 (no norm): q_weight and k_weight must be NULL");
+    } else {
+        ORTHROS_TRY(check_norm("q_weight", q_weight, eps));
+        ORTHROS_TRY(check_norm("k_weight", k_weight, eps));
     }
-    if (n_out > 0) {
-        ORTHROS_TRY(check_rows("q_out", q_out, q_out_stride, Hq, d, dtype, false));
-        if (!q_out_rot || !aligned16(q_out_rot)) return report_error(ORTHROS_EINVAL, "q_out_rot must not be NULL and 16-byte aligned");
-        if (!out_positions) return report_error(ORTHROS_EINVAL, "out_positions must not be NULL when n_out > 0");
-    }
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    uint32_t *status = static_cast<uint32_t *>(workspace);
-    if (n_new == 0 && n_out == 0) {
-        const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(uint32_t), stream);
-        return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "status reset");
-    }
-    RotateParams p{};
-    p.x = q;
-    p.y = q_rot;
-    p.x_stride = q_stride;
-    p.y_stride = (long long)Hq * d;
-    p.positions = token_pos;
-    p.alpha = alpha_base;
-    p.beta = beta_base;
-    p.steps = steps;
-    p.n = n_new;
-    p.H = Hq;
-    p.rot = rot_dim;
-    p.interleaved = layout == ORTHROS_ROPE_INTERLEAVED;
-    p.amplitude = amplitude;
-    p.x_out = q_out;
-    p.y_out = q_out_rot;
-    p.x_out_stride = q_out_stride;
-    p.alpha_out = alpha_out;
-    p.beta_out = beta_out;
-    p.out_positions = out_positions;
-    p.n_out = n_out;
-    p.k = k_new;
-    p.v = v_new;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.token_seq = token_seq;
-    p.block_table = block_table;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.Hkv = Hkv;
-    p.B = B;
-    p.max_pages = max_pages;
-    p.page_size = page_size;
-    p.num_pages = num_pages;
-    p.status = status;
-    ProfScope ps("rotate_append", stream);
-    const cudaError_t e = launch_rotate_append(p, d, dtype, stream);
-    return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, "rotated append launch");
+    const AppendArgs a{q, q_out, k_new, v_new, q_stride, q_out_stride, k_stride, v_stride, q_weight, k_weight, eps, alpha_base,
+                       beta_base, alpha_out, beta_out, steps, rot_dim, layout, amplitude, token_slots, nullptr, token_pos,
+                       out_positions, n_new, n_out, Hq, Hkv, d, dtype, q_rot, q_out_rot, k_cache, v_cache, nullptr, 0,
+                       0, page_size, num_pages, workspace, workspace_bytes};
+    return append_rows(a, true, reinterpret_cast<cudaStream_t>(stream), "norm_rotate_append");
 }
 
 }  // extern "C"

@@ -79,6 +79,7 @@ typedef enum { ORTHROS_BF16 = 0, ORTHROS_F32 = 1 } orthros_dtype;
  * takes the inverse), so any finite bf16 input is served. */
 #define ORTHROS_DEV_FP16_RANGE 0x8u
 #define ORTHROS_DEV_TIMEOUT 0x10u      /* a bounded wait inside a kernel ran out */
+#define ORTHROS_DEV_NO_PAGES 0x20u     /* a step needs more pages than are free */
 
 /*
  * Workspace bytes orthros_prefill needs for these sizes. n_out is the total
@@ -614,6 +615,177 @@ ORTHROS_API orthros_status orthros_chunk_attention(const void *q, const int32_t 
                                                    int Hkv, int d, int window, float scale, orthros_dtype dtype,
                                                    int max_pages, int page_size, int num_pages, void *o, float *lse,
                                                    void *workspace, size_t workspace_bytes, orthros_stream_t stream);
+
+/*
+ * orthros_rotate with a norm of each head before the affine (models that norm
+ * queries and keys): y = amplitude R(t) u with
+ *   u = alpha (.) (weight (.) xh) + beta,  xh = x / sqrt(mean_c x_c^2 + eps),
+ * the mean over the d channels of the head.
+ *
+ * weight       [d] float (16-byte aligned), shared by the heads, or NULL (1)
+ * eps          > 0
+ * The other arguments are orthros_rotate's. The squares are summed in fp32: a
+ * head whose sum of squares is past 3.4e38 has xh = 0.
+ */
+ORTHROS_API orthros_status orthros_norm_rotate(const void *x, long long x_stride, const int32_t *positions,
+                                               const float *weight, float eps, const float *alpha, const float *beta,
+                                               const uint64_t *steps, int rot_dim, orthros_rope_layout layout,
+                                               float amplitude, int n, int H, int d, orthros_dtype dtype, void *y,
+                                               long long y_stride, orthros_stream_t stream);
+
+/* Workspace bytes orthros_norm_rotate_backward needs for these sizes (0 if rejected). */
+ORTHROS_API size_t orthros_norm_rotate_backward_workspace_size(int n, int H, int d, orthros_dtype dtype);
+
+/*
+ * Gradients of orthros_norm_rotate: with g = amplitude R(-t) dy, r = 1 /
+ * sqrt(mean x^2 + eps), a = alpha (.) weight and S = sum over tokens of
+ * g (.) xh (per head),
+ *   dx = r (a (.) g - xh mean_c(a g xh)),   d_beta = sum over tokens of g,
+ *   d_alpha = weight (.) S,                 d_weight = sum over heads of alpha (.) S.
+ *
+ * d_weight     [d] float, overwritten, or NULL
+ * d_alpha, d_beta [H, d] float, overwritten, or both NULL
+ * x            the forward's input, always read
+ * The other arguments are orthros_rotate_backward's (dx may be dy; without
+ * gradients of weight and affine the workspace may be NULL). The sums run in a
+ * fixed order: the same call gives the same bits.
+ */
+ORTHROS_API orthros_status orthros_norm_rotate_backward(
+    const void *dy, long long dy_stride, const void *x, long long x_stride, const int32_t *positions, const float *weight,
+    float eps, const float *alpha, const uint64_t *steps, int rot_dim, orthros_rope_layout layout, float amplitude, int n, int H,
+    int d, orthros_dtype dtype, void *dx, long long dx_stride, float *d_weight, float *d_alpha, float *d_beta,
+    void *workspace, size_t workspace_bytes, orthros_stream_t stream);
+
+/*
+ * orthros_rotate_append with norms, and with the place of a new token in the
+ * cache given apart from its position (the tokens of a drafted tree lie one
+ * behind the other, while their positions are their depths):
+ *   - key i is normed with k_weight, rotated to token_pos[i] and written to
+ *     token slot token_slots[i] (page * page_size + place in the page), its
+ *     values copied there;
+ *   - q_rot[i] and q_out_rot[r] as orthros_norm_rotate gives them for q[i] at
+ *     token_pos[i] and q_out[r] at out_positions[r], with q_weight and the
+ *     stream's affine.
+ *
+ * token_slots  [n_new] int32, as orthros_plan_step makes them; -1: the token is
+ *              not cached (a row of padding). No two tokens may share a slot.
+ * q_weight, k_weight [d] float (16-byte aligned) or NULL (1)
+ * eps          > 0, or 0 for no norm (both weights NULL): slots alone
+ * The other arguments are orthros_rotate_append's. A slot below -1 or past the
+ * pool sets ORTHROS_DEV_BAD_PAGE; that token's cache write is skipped.
+ */
+ORTHROS_API orthros_status orthros_norm_rotate_append(
+    const void *q, long long q_stride, const void *q_out, long long q_out_stride, const void *k_new, long long k_stride,
+    const void *v_new, long long v_stride, const float *q_weight, const float *k_weight, float eps, const float *alpha_base,
+    const float *beta_base, const float *alpha_out, const float *beta_out, const uint64_t *steps, int rot_dim,
+    orthros_rope_layout layout, float amplitude, const int32_t *token_slots, const int32_t *token_pos,
+    const int32_t *out_positions, int n_new, int n_out, int Hq, int Hkv, int d, orthros_dtype dtype, void *q_rot,
+    void *q_out_rot, void *k_cache, void *v_cache, int page_size, int num_pages, void *workspace, size_t workspace_bytes,
+    orthros_stream_t stream);
+
+/*
+ * What a serving step needs from its lengths, made on the GPU. Sequence b has
+ * cache_lens[b] tokens in the cache and new_lens[b] new ones; it needs
+ * ceil((cache + new) / page_size) pages and takes those that it does not hold
+ * yet from the free pages.
+ *
+ * cache_lens, new_lens, pages_held [B] int32; new_lens[b] = -1: the sequence has
+ *              ended, all its pages go back (cache_lens is then not read further)
+ * free_pages   [num_pages], free_count [1]: the first free_count entries are the
+ *              free pages, a stack. Ended sequences push theirs, in order, first;
+ *              then the growing sequences, in order, take from the top. Updated
+ *              in place up to the new height; entries above it are left.
+ * block_table  [B, max_pages]: entries of new pages are written, others left
+ * n            rows of the token arrays; rows behind the last new token are
+ *              padding: token_seq -1, token_pos 0, token_slots -1, no mask bits
+ * parents      [n] with max_tree > 0 (at most 256): the new tokens of every
+ *              sequence are a drafted tree of at most max_tree tokens, and
+ *              parents[i] is the number within its tree (0, 1, ...) of token i's
+ *              parent, which comes before it, or -1 under the last cached token.
+ *              NULL with max_tree = 0: consecutive tokens
+ * q_indptr [B+1], kv_lens [B] (cache + new; 0 once ended), token_seq, token_pos,
+ * token_slots [n]: as orthros_norm_rotate_append, orthros_chunk_attention (for
+ *              which n has to be the number of tokens) and orthros_tree_attention
+ *              take them. Token j of sequence b lies at place cache_lens[b] + j; its
+ *              position is that place, or in a tree cache_lens[b] + its depth.
+ * tree_mask    [n, ceil(max_tree / 32)]: bit j of word j/32 of token i's row is
+ *              set for token j of its tree if that is i or one of i's ancestors
+ * cache_lens_out [B] or NULL, pages_held_out [B], free_count_out [1]: the state
+ *              after the step, all new tokens counted (orthros_tree_commit sets the
+ *              lengths after a tree's verification). They may be cache_lens,
+ *              pages_held and free_count; outputs must not overlap inputs otherwise.
+ * workspace    at least 256 bytes (status word), 256-byte aligned. B <= 8192.
+ * A sequence whose lengths cannot be (negative, past the block table, a tree
+ * over max_tree) sets ORTHROS_DEV_BAD_LENGTH, one whose pages are not all there
+ * ORTHROS_DEV_NO_PAGES: it changes nothing of its state, kv_lens[b] = 0, and its
+ * token rows are padding, so that the attention makes them NaN. More tokens than
+ * rows, or a stack that cannot hold the pages, set ORTHROS_DEV_BAD_LENGTH and
+ * refuse the step: no state changes, q_indptr is all -1. A page id outside
+ * [0, num_pages) sets ORTHROS_DEV_BAD_PAGE (slot -1), a parent that does not come
+ * before its token ORTHROS_DEV_BAD_POSITION (counted as -1).
+ */
+ORTHROS_API orthros_status orthros_plan_step(
+    const int32_t *cache_lens, const int32_t *new_lens, const int32_t *pages_held, const int32_t *free_count,
+    const int32_t *parents, int max_tree, int32_t *free_pages, int32_t *block_table, int B, int n, int max_pages, int page_size,
+    int num_pages, int32_t *q_indptr, int32_t *kv_lens, int32_t *cache_lens_out, int32_t *pages_held_out, int32_t *free_count_out,
+    int32_t *token_seq, int32_t *token_pos, int32_t *token_slots, int32_t *tree_mask, void *workspace, size_t workspace_bytes,
+    orthros_stream_t stream);
+
+/* Workspace bytes orthros_tree_attention needs for these sizes (0 if rejected). */
+ORTHROS_API size_t orthros_tree_attention_workspace_size(int B, int n, int max_new, int Hq, int Hkv, int d, int max_pages,
+                                                         int page_size, orthros_dtype dtype);
+
+/*
+ * Attention of drafted trees over a paged cache that already holds their keys
+ * and values: orthros_chunk_attention with a mask over the new tokens. The n_b =
+ * q_indptr[b+1] - q_indptr[b] tokens of sequence b lie at places L .. L + n_b - 1,
+ * L = kv_lens[b] - n_b. Token i sees token j of its own tree where bit j of its
+ * mask row is set; its position is t_i = L + max(bits, 1) - 1, bits being the
+ * number of tokens that it sees. It sees the keys before the tree from
+ * max(0, t_i - w + 1) on, and of the tree those at positions above t_i - w.
+ *
+ * q_indptr     [B+1] int32 DEVICE, from 0, non-decreasing, to at most n: rows
+ *              behind q_indptr[B] are left as they were
+ * tree_mask    [n, mask_words] int32, mask_words in [1, 8]; bits of tokens that
+ *              the tree does not have count for nothing. Any mask will do, also
+ *              one with later tokens or without the token itself: a row that sees
+ *              no key at all has o = 0, lse = -inf
+ * max_new      upper bound of the n_b (32 mask_words always serves)
+ * The other arguments, the precision and the reports are orthros_chunk_attention's.
+ * The keys and values of all n_b tokens, and the cached ones from max(0, L - w + 1)
+ * on, must be finite.
+ */
+ORTHROS_API orthros_status orthros_tree_attention(
+    const void *q, const int32_t *q_indptr, const int32_t *kv_lens, const int32_t *tree_mask, int mask_words,
+    const void *k_cache, const void *v_cache, const int32_t *block_table, int B, int n, int max_new, int Hq, int Hkv, int d,
+    int window, float scale, orthros_dtype dtype, int max_pages, int page_size, int num_pages, void *o, float *lse,
+    void *workspace, size_t workspace_bytes, orthros_stream_t stream);
+
+/*
+ * After a tree's verification: the accepted path's keys and values move from
+ * places L + accepted[b][i] to L + i, so that the cache holds consecutive tokens
+ * again, and cache_lens[b] = L + n_accepted[b].
+ *
+ * k_cache, v_cache [layers, num_pages, page_size, Hkv, d]: all layers at once
+ * q_indptr, kv_lens, block_table: the tree step's
+ * accepted     [B, most] int32, ascending tokens of the tree (numbers within it);
+ *              the first n_accepted[b] of a row count. most in [1, 256]
+ * cache_lens   [B], written; not kv_lens
+ * Sequences own the pages of their trees. Places behind L + n_accepted keep what
+ * they had. workspace: at least 256 bytes (status word), 256-byte aligned.
+ * A path that does not ascend or leaves the tree sets ORTHROS_DEV_BAD_POSITION,
+ * n_accepted outside [0, min(most, n_b)] ORTHROS_DEV_BAD_LENGTH, a page id outside
+ * [0, num_pages) ORTHROS_DEV_BAD_PAGE: nothing of that sequence moves, and
+ * cache_lens[b] = L. Impossible lengths (n_b < 0, kv_lens[b] < n_b, as of a sequence
+ * that had no place in the plan, or past the block table) set ORTHROS_DEV_BAD_LENGTH
+ * and leave cache_lens[b] as it was.
+ */
+ORTHROS_API orthros_status orthros_tree_commit(void *k_cache, void *v_cache, int layers, const int32_t *block_table,
+                                               const int32_t *q_indptr, const int32_t *kv_lens, const int32_t *accepted,
+                                               const int32_t *n_accepted, int most, int B, int Hkv, int d,
+                                               orthros_dtype dtype, int max_pages, int page_size, int num_pages,
+                                               int32_t *cache_lens, void *workspace, size_t workspace_bytes,
+                                               orthros_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the status word that the last call using
