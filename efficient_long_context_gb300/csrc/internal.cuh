@@ -333,6 +333,9 @@ struct RotateBwdParams {
 };
 int rotate_grad_groups(int H, int d, int elem_bytes);
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes);
+// norm_rotary.cu: the same with a norm of each head (eps > 0), an append where there is a status word
+cudaError_t launch_norm_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
+cudaError_t launch_norm_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_norm_grad_sum(const RotateBwdParams &p, int d, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_rotate(const RotateParams &p, int d, orthros_dtype dtype, cudaStream_t stream);
 cudaError_t launch_rotate_backward(const RotateBwdParams &p, int d, orthros_dtype dtype, cudaStream_t stream);

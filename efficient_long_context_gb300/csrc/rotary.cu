@@ -1,47 +1,20 @@
 // rotary.cu -- rotary positions: the affine of a query stream followed by the
 // rotation of its channel pairs, the gradient of both, and the paged append
-// that rotates new keys on their way into the cache; each with or without a
-// norm of the head before the affine.
+// that rotates new keys on their way into the cache.
 //
 // Mathematics. Pair i of a head at position t turns by the angle t * f_i:
 //   (y_a, y_b) = m (u_a cos - u_b sin, u_a sin + u_b cos),  u = alpha (.) x + beta,
 // over the first `rot` channels (pairs (i, i + rot/2) or (2i, 2i + 1)); the
 // other channels leave as u. The rotation is orthogonal, so its gradient is the
 // rotation by the opposite angle: g = m R(-t) dy, dx = alpha (.) g,
-// d_alpha = sum_t g (.) x, d_beta = sum_t g.
-//
-// With a norm, u = a (.) xh + beta with xh = r x, r = (mean_c x_c^2 + eps)^(-1/2)
-// and a = alpha (.) w, the weight w [d] being shared by the heads. Then
-// dx = r (a (.) g - xh mean_c(a g xh)); with S = sum_t g (.) xh per head,
-// d_alpha = w (.) S and d_w = sum_h alpha (.) S. The lanes that hold a row are
-// neighbours, so its sums are a few exchanges within a warp.
-//
-// Angles. t * f_i in fp32 loses its fraction at long positions (an ulp at
-// t = 131072, f = 1 is 0.008 rad), so frequencies arrive as 64-bit fixed-point
-// fractions of a turn, rounded to half a unit: the phase of position t is the low
-// 64 bits of t * step, an integer product that wraps as the angle does, off by
-// 2^-34 turn at most. Its top 32 bits (2^-32 turn, 1.5e-9 rad), as a float (pi 2^-24),
-// go through sincospif (2^-23): sin and cos are off by less than 4e-7 at every 32-bit
-// position, negative ones included.
-//
-// Arithmetic is fp32 throughout, rounded once to the element type on the store;
-// the affine's gradients are accumulated and returned in fp32.
-#include "internal.cuh"
+// d_alpha = sum_t g (.) x, d_beta = sum_t g. Angles and precision: rotary.cuh.
+#include "rotary.cuh"
 
 namespace orthros {
-namespace {
 
-// A row (one head of one token) is moved in work items of two 16-byte vectors.
-// Half layout: a rotated item holds the two vectors of VEC pairs, i and i +
-// rot/2/VEC; the channels past `rot` are items of two consecutive vectors.
-// Interleaved layout: pairs lie within a vector, so item i takes vectors i and
-// i + D/2/VEC, and neighbouring lanes move neighbouring vectors (two consecutive
-// vectors per lane left every 32-byte sector to two instructions: 189 against
-// 133 us for 32768 x 32 x 128 bf16). rot is a multiple of 16, so every vector is
-// rotated or not as a whole.
-template <typename T> struct Vec {
-    static constexpr int kN = 16 / (int)sizeof(T);
-};
+using namespace rope;
+
+namespace {
 
 template <typename T> __device__ __forceinline__ void unpack(const uint4 &r, float (&f)[Vec<T>::kN]);
 template <> __device__ __forceinline__ void unpack<float>(const uint4 &r, float (&f)[4]) {
@@ -71,42 +44,6 @@ template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float (&f
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-// 16 bytes from global to shared memory, not through registers.
-__device__ __forceinline__ void copy16(uint4 *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-
-// cos and sin of position t's angle for one frequency step, times the amplitude.
-__device__ __forceinline__ void angle(int t, uint64_t step, float amp, float &c, float &s) {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(t)) * step;  // modulo one turn
-    const int hi = static_cast<int>(static_cast<uint32_t>(phase >> 32));           // in units of 2^-32 turn
-    sincospif(static_cast<float>(hi) * 4.656612873077393e-10f, &s, &c);            // 2 pi hi 2^-32 = pi (hi 2^-31)
-    c *= amp;
-    s *= amp;
-}
-
-// The two vectors of a work item: first channels, and which of them rotate.
-// Pair j of the item's angles is pair first_a + j (vector a and, in the half
-// layout, b) for j < n_a, and first_b + j - VEC/2 for an interleaved vector b.
-template <int VEC, int D> struct Item {
-    int ca, cb;
-    bool ra, rb;
-    __device__ __forceinline__ Item(int i, int rot, bool interleaved) {
-        const bool split = !interleaved && 2 * VEC * i < rot;  // a rotated item of the half layout
-        ca = interleaved || split ? VEC * i : 2 * VEC * i;
-        cb = interleaved ? ca + D / 2 : split ? ca + (rot >> 1) : ca + VEC;
-        ra = interleaved ? ca < rot : split;
-        rb = interleaved ? cb < rot : split;
-    }
-    // pair of the item's j-th angle (interleaved: the first VEC/2 are vector a's, the others b's)
-    __device__ __forceinline__ int pair(int j, bool interleaved) const {
-        return !interleaved ? ca + j : j < VEC / 2 ? ca / 2 + j : cb / 2 + j - VEC / 2;
-    }
-    __device__ __forceinline__ bool turns(int j, bool interleaved) const {
-        return !interleaved || j < VEC / 2 ? ra : rb;
-    }
-};
 
 // Rotates the pairs of an item in place: (a[j], b[j]) in the half layout,
 // neighbours of the 2 VEC channels in the interleaved one.
@@ -141,36 +78,9 @@ __device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const flo
     }
 }
 
-// Sum over the kLanes neighbouring lanes that hold a row (they run together).
-template <int kLanes> __device__ __forceinline__ float row_sum(float x) {
-    const uint32_t mask = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) x += __shfl_xor_sync(mask, x, o);
-    return x;
-}
-
-template <int VEC>
-__device__ __forceinline__ void load_affine(const float *p, int ca, int cb, float (&a)[VEC], float (&b)[VEC]) {
-#pragma unroll
-    for (int j = 0; j < VEC; j += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(p + ca + j));
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(p + cb + j));
-        a[j] = x.x, a[j + 1] = x.y, a[j + 2] = x.z, a[j + 3] = x.w;
-        b[j] = y.x, b[j + 1] = y.y, b[j + 2] = y.z, b[j + 3] = y.w;
-    }
-}
-
 // Cosines and sines of a few tokens, computed once by the block and shared by its
 // heads: entry (token, j / 2, item) holds angles j and j + 1 of the item, so the
 // lanes of a row read consecutive 16-byte words.
-constexpr int kTabTokens = 16;  // at most
-constexpr int kRunTokens = 128;  // positions (and page slots) a block looks up at a time
-constexpr int kBatch = 4;        // tokens whose loads a thread of the moving kernel has in flight
-// Tokens of a table (a divisor of kRunTokens), for so many handled side by side: one
-// batch of loads a thread, which are under way while the angles are computed. Two
-// batches leave the second one's trip to memory bare: 16384 x 32 x 128 fp32 96 us
-// instead of 86, 32768 x 8 x 128 53 instead of 46.
-__device__ __forceinline__ int table_tokens(int lanes) { return lanes > 2 ? kTabTokens : kBatch * lanes; }
 template <typename T, int D> struct Table {
     static constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kQ = VEC / 2;
     float4 e[kTabTokens][kQ][IPR];
@@ -211,55 +121,7 @@ template <typename T, int D> struct Table {
 // heads and Hkv value heads. Blocks from p.blocks on (along x) move the output
 // stream's rows; an append's last one writes the status word.
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 512;  // at most
-
-// Token slot of new token i in the page pool, or -1 when it has none.
-__device__ __forceinline__ long long page_slot(const RotateParams &p, long long i) {
-    if (p.slots) {  // given by the caller
-        const int s = p.slots[i];
-        return s >= 0 && s < (long long)p.num_pages * p.page_size ? s : -1;
-    }
-    const int b = p.token_seq[i], t = p.positions[i];
-    if (b < 0 || b >= p.B || t < 0 || t / p.page_size >= p.max_pages) return -1;
-    const int pg = p.block_table[(long long)b * p.max_pages + t / p.page_size];
-    if (pg < 0 || pg >= p.num_pages) return -1;
-    return (long long)pg * p.page_size + t % p.page_size;
-}
-
-// The status word of an append, written by a block of its own that checks every new
-// token beside the moving ones: no reset launch before the kernel, no atomics.
-__device__ __forceinline__ void write_status(const RotateParams &p) {
-    constexpr int kBatchS = 8;  // tokens a thread looks up at once
-    uint32_t wrong = 0;
-    if (p.slots)  // -1: a token that is not cached
-        for (long long i = threadIdx.x; i < p.n; i += blockDim.x) {
-            const int s = p.slots[i];
-            if (s < -1 || s >= (long long)p.num_pages * p.page_size) wrong |= ORTHROS_DEV_BAD_PAGE;
-        }
-    for (long long i0 = threadIdx.x; !p.slots && i0 < p.n; i0 += (long long)kBatchS * blockDim.x) {
-        int b[kBatchS], t[kBatchS];
-#pragma unroll
-        for (int u = 0; u < kBatchS; ++u) {
-            const long long i = i0 + (long long)u * blockDim.x;
-            b[u] = i < p.n ? p.token_seq[i] : 0;
-            t[u] = i < p.n ? p.positions[i] : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < kBatchS; ++u) {
-            if (i0 + (long long)u * blockDim.x >= p.n) break;
-            if (b[u] < 0 || b[u] >= p.B || t[u] < 0 || t[u] / p.page_size >= p.max_pages) {
-                wrong |= ORTHROS_DEV_BAD_POSITION;
-            } else {
-                const int pg = p.block_table[(long long)b[u] * p.max_pages + t[u] / p.page_size];
-                if (pg < 0 || pg >= p.num_pages) wrong |= ORTHROS_DEV_BAD_PAGE;
-            }
-        }
-    }
-    const int pos = __syncthreads_or(wrong & ORTHROS_DEV_BAD_POSITION), pg = __syncthreads_or(wrong & ORTHROS_DEV_BAD_PAGE);
-    if (threadIdx.x == 0) *p.status = (pos ? ORTHROS_DEV_BAD_POSITION : 0u) | (pg ? ORTHROS_DEV_BAD_PAGE : 0u);
-}
-
-template <typename T, int D, bool kAppend, bool kNorm>
+template <typename T, int D, bool kAppend>
 __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateParams p) {
     constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC);
     __shared__ Table<T, D> tab[2];
@@ -283,7 +145,7 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
     const T *src = static_cast<const T *>(out ? p.x_out : p.x);
     T *dst = static_cast<T *>(out ? p.y_out : p.y);
     long long ss = out ? p.x_out_stride : p.x_stride, ds = p.y_stride;
-    const float *alpha = out ? p.alpha_out : p.alpha, *beta = out ? p.beta_out : p.beta, *weight = p.weight;
+    const float *alpha = out ? p.alpha_out : p.alpha, *beta = out ? p.beta_out : p.beta;
     int hh = h;                  // head within its tensor
     bool paged = false, value = false;
     if (kAppend && h >= p.H) {
@@ -295,7 +157,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
         dst = static_cast<T *>(value ? p.v_cache : p.k_cache);
         ss = value ? p.v_stride : p.k_stride;
         alpha = beta = nullptr;
-        weight = p.k_weight;
     }
     const bool active = tl < lanes && (kAppend ? (paged ? !out && h < p.H + 2 * p.Hkv : src != nullptr) : h < p.H);
     Item<VEC, D> it(item, p.rot, p.interleaved);
@@ -307,20 +168,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
     if (affine) {
         load_affine<VEC>(alpha + hh * D, it.ca, it.cb, al[0], al[1]);
         load_affine<VEC>(beta + hh * D, it.ca, it.cb, be[0], be[1]);
-    }
-    if constexpr (kNorm) {  // the norm's weight goes into alpha
-        float w[2][VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) w[0][j] = w[1][j] = 1.f;
-        if (active && weight && !value) load_affine<VEC>(weight, it.ca, it.cb, w[0], w[1]);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                al[v][j] = affine ? al[v][j] * w[v][j] : w[v][j];
-                if (!affine) be[v][j] = 0.f;
-            }
-        }
     }
     const long long n0 = n * bx / nbx, n1 = n * (bx + 1) / nbx;
     const int step = table_tokens(lanes);
@@ -337,8 +184,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
                 if (k < cnt) {
                     ra[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (base + k) * ss + it.ca));
                     rb[u] = __ldcs(reinterpret_cast<const uint4 *>(src + (base + k) * ss + it.cb));
-                } else if (kNorm) {
-                    ra[u] = rb[u] = make_uint4(0, 0, 0, 0);  // (its sum is taken, and not used)
                 }
             }
         };
@@ -359,23 +204,6 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
         if (!active) continue;
         for (int k0 = tl; k0 < cnt; k0 += kBatch * lanes) {
             if (k0 != tl) load(k0);
-            float r[kBatch];
-            if constexpr (kNorm) {  // 1 / rms of the batch's rows, their exchanges side by side
-                if (!value) {
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        float a[VEC], b[VEC];
-                        unpack<T>(ra[u], a);
-                        unpack<T>(rb[u], b);
-                        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) s0 = fmaf(a[j], a[j], s0), s1 = fmaf(b[j], b[j], s1);
-                        r[u] = s0 + s1;
-                    }
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) r[u] = rsqrtf(fmaf(row_sum<IPR>(r[u]), 1.f / D, p.eps));
-                }
-            }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + u * lanes;
@@ -390,11 +218,7 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
                 float a[VEC], b[VEC], c[VEC], s[VEC];
                 unpack<T>(ra[u], a);
                 unpack<T>(rb[u], b);
-                if constexpr (kNorm) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) a[j] *= r[u], b[j] *= r[u];
-                }
-                if (kNorm || affine) {
+                if (affine) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         a[j] = fmaf(a[j], al[0][j], be[0][j]);
@@ -425,14 +249,11 @@ __global__ void __launch_bounds__(kMoveThreads) rotate_move_kernel(const RotateP
 // threads. The moving kernel above keeps its loads in registers: through
 // shared memory it took 84 to 110 us by the depth, and its append 38 to 46.
 // ---------------------------------------------------------------------------
-constexpr int kBwdThreads = 512;
-constexpr int kBwdBlocks = 1;  // blocks per SM
 constexpr int kBwdDepth = 6;   // tokens a thread has in flight
 
-template <typename T, int D, bool kGrads, bool kNorm>
+template <typename T, int D, bool kGrads>
 __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kernel(const RotateBwdParams p) {
-    constexpr bool kX = kGrads || kNorm;  // x is read
-    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kV = kX ? 4 : 2;
+    constexpr int VEC = Vec<T>::kN, IPR = D / (2 * VEC), kV = kGrads ? 4 : 2;
     extern __shared__ uint4 fifo[];  // [kBwdDepth][kV][thread]
     __shared__ Table<T, D> tab[2];
     __shared__ int pos[kRunTokens];
@@ -457,7 +278,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
             const T *dy = static_cast<const T *>(p.dy) + i * p.dy_stride + h * D;
             copy16(to, dy + ca);
             copy16(to + kBwdThreads, dy + cb);
-            if constexpr (kX) {
+            if constexpr (kGrads) {
                 const T *x = static_cast<const T *>(p.x) + i * p.x_stride + h * D;
                 copy16(to + 2 * kBwdThreads, x + ca);
                 copy16(to + 3 * kBwdThreads, x + cb);
@@ -476,12 +297,6 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
         da[0][j] = da[1][j] = db[0][j] = db[1][j] = 0.f;
     }
     if (active && p.alpha) load_affine<VEC>(p.alpha + h * D, ca, cb, al[0], al[1]);
-    if (kNorm && active && p.weight) {
-        float w[2][VEC];
-        load_affine<VEC>(p.weight, ca, cb, w[0], w[1]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) al[0][j] *= w[0][j], al[1][j] *= w[1][j];
-    }
     int buf = 0, rd = 0;
     for (int base = 0; base < n; base += step, buf ^= 1) {
         const int cnt = min(step, n - base);
@@ -502,27 +317,12 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
             float x0[VEC], x1[VEC];
             unpack<T>(from[0], a);
             unpack<T>(from[kBwdThreads], b);
-            if constexpr (kX) {
+            if constexpr (kGrads) {
                 unpack<T>(from[2 * kBwdThreads], x0);
                 unpack<T>(from[3 * kBwdThreads], x1);
             }
             tab[buf].read(k, item, c, s);
             turn<VEC, D>(a, b, c, s, it, p.interleaved);
-            float r = 1.f, mean = 0.f;  // 1 / rms of the row, mean of a g xh over it
-            if constexpr (kNorm) {
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    s0 = fmaf(x0[j], x0[j], fmaf(x1[j], x1[j], s0));
-                    s1 = fmaf(a[j] * al[0][j], x0[j], fmaf(b[j] * al[1][j], x1[j], s1));
-                }
-                s0 = row_sum<IPR>(s0);
-                s1 = row_sum<IPR>(s1);
-                r = rsqrtf(fmaf(s0, 1.f / D, p.eps));
-                mean = s1 * r * (1.f / D);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) x0[j] *= r, x1[j] *= r;
-            }
             if constexpr (kGrads) {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -534,10 +334,6 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
             }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) a[j] *= al[0][j], b[j] *= al[1][j];
-            if constexpr (kNorm) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) a[j] = r * fmaf(-x0[j], mean, a[j]), b[j] = r * fmaf(-x1[j], mean, b[j]);
-            }
             T *dx = static_cast<T *>(p.dx) + (n0 + base + k) * p.dx_stride + h * D;
             *reinterpret_cast<uint4 *>(dx + ca) = pack<T>(a);
             *reinterpret_cast<uint4 *>(dx + cb) = pack<T>(b);
@@ -561,27 +357,6 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rotate_backward_kerne
         __syncthreads();
         float *part = p.partial + (long long)blockIdx.x * 2 * p.H * D;
         const int row = hb * IPR;  // threads of a token lane
-        if constexpr (kNorm) {
-            // the weight's gradient: channel tid, over the block's token lanes and heads
-            if (p.partial_w && tid < D) {
-                // where channel tid lies: item i, vector v, element j
-                int i, v, j = tid % VEC;
-                if (p.interleaved) v = tid / (D / 2), i = tid % (D / 2) / VEC;
-                else if (tid < p.rot) v = tid / (p.rot / 2), i = tid % (p.rot / 2) / VEC;
-                else i = tid / (2 * VEC), v = tid / VEC % 2;
-                const float *from = red + (v * VEC + j) * kBwdThreads + i;
-                const int heads = min(hb, p.H - (int)blockIdx.y * hb);
-                float sum = 0.f;
-                for (int hh = 0; hh < heads; ++hh) {
-                    const float at = p.alpha ? p.alpha[(blockIdx.y * hb + hh) * D + tid] : 1.f;
-                    float t = 0.f;
-                    for (int l = 0; l < lanes; ++l) t += from[l * row + hh * IPR];
-                    sum = fmaf(at, t, sum);
-                }
-                p.partial_w[((long long)blockIdx.y * gridDim.x + blockIdx.x) * D + tid] = sum;
-            }
-            if (!p.d_alpha) return;
-        }
         if (!active) return;
         for (int v = tl; v < 4 * VEC; v += lanes) {  // this thread's channels, shared with its fellows of other lanes
             const float *from = red + v * kBwdThreads + tid - tl * row;
@@ -621,110 +396,41 @@ __global__ void __launch_bounds__(256) rotate_grad_sum_kernel(const float *parti
     }
 }
 
-// The same for a norm's gradients: d_alpha = w (.) S and d_beta from the partials, and d_w from the
-// n_w block sums [n_w, D] of alpha (.) S. Blocks of 32 columns: 2 H D / 32 for the affine's (none when
-// they are not wanted), then D / 32 for the weight's.
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const RotateBwdParams p, int cols, int d, int n_w) {
-    __shared__ float red[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int affine = p.d_alpha ? 2 * cols / 32 : 0;
-    const bool weight = (int)blockIdx.x >= affine;
-    const int col = (weight ? blockIdx.x - affine : blockIdx.x) * 32 + lane;
-    const float *from = (weight ? p.partial_w : p.partial) + col;
-    const int n = weight ? n_w : p.n_part;
-    const long long step = weight ? d : 2 * cols;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int i = w;
-    for (; i + 24 < n; i += 32) {
-        s0 += from[i * step];
-        s1 += from[(i + 8) * step];
-        s2 += from[(i + 16) * step];
-        s3 += from[(i + 24) * step];
-    }
-    for (; i < n; i += 8) s0 += from[i * step];
-    red[w][lane] = (s0 + s1) + (s2 + s3);
-    __syncthreads();
-    if (w == 0) {
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s += red[k][lane];
-        if (weight) p.d_weight[col] = s;
-        else if (col < cols) p.d_alpha[col] = p.weight ? s * p.weight[col % d] : s;
-        else p.d_beta[col - cols] = s;
-    }
-}
-
-// The heads of a token are cut into equal groups, a block per group: as few groups
-// as fill the SM's registers with threads to within a tenth (a token's 48
-// virtual heads of 8 items in one group are a block of 384 threads where 512
-// fit, three groups of 16 fill them), since every group computes the token's
-// angles again. Several tokens go side by side when a group is narrow. Blocks
-// along the tokens: as many as run at once, with equal runs of tokens.
-template <typename T, int D, bool kAppend, bool kNorm> cudaError_t move_t(RotateParams p, int heads, cudaStream_t s) {
-    constexpr int IPR = D / (2 * Vec<T>::kN);
-    static std::atomic<int> resident{0};  // threads of this kernel an SM's registers hold
-    int per_sm = resident.load(std::memory_order_relaxed);
-    if (per_sm == 0) {
-        cudaFuncAttributes at;
-        if (cudaError_t e = cudaFuncGetAttributes(&at, (const void *)rotate_move_kernel<T, D, kAppend, kNorm>); e != cudaSuccess) return e;
-        per_sm = 65536 / ((at.numRegs + 7) / 8 * 8);
-        resident.store(per_sm, std::memory_order_relaxed);
-    }
-    int groups = 0, hb = 0, threads = 0, best = 0;
-    const int g0 = (heads * IPR + kMoveThreads - 1) / kMoveThreads;
-    for (int g = g0; g <= g0 + 3 && g <= heads; ++g) {
-        const int h = (heads + g - 1) / g, row = h * IPR;
-        const int side = row >= 256 ? 1 : 256 / row < kTabTokens ? 256 / row : kTabTokens;
-        const int t = (row * side + 31) / 32 * 32;
-        const int busy = (int)((long long)(per_sm / t) * (side * row) * heads / ((long long)h * g));  // threads with work
-        if (busy > best + best / 10) groups = g, hb = h, threads = t, best = busy;
-    }
-    p.heads_per_block = hb;
-    const int lanes = threads / (hb * IPR);  // (the kernel's)
-    // blocks that run at once (append: one of them, in each group's row, for the status
-    // word), shared between the new tokens and the output stream's rows by their
-    // number: a second wave of a few short blocks cost 3 us
-    const int fit = device_sm_count() * (per_sm / threads < 32 ? per_sm / threads : 32) / groups - (kAppend ? 1 : 0);
-    const long long most = (p.n + lanes - 1) / lanes, most_out = (p.n_out + lanes - 1) / lanes;
-    long long out = p.n_out == 0 ? 0 : fit * (long long)p.n_out / (p.n + p.n_out);
-    out = out > most_out ? most_out : out < 1 && p.n_out > 0 ? 1 : out;
-    long long blocks = fit - out;
-    blocks = blocks > most ? most : blocks < 1 && p.n > 0 ? 1 : blocks < 0 ? 0 : blocks;
-    p.blocks = (int)blocks;
-    const dim3 grid((unsigned)(blocks + out + (kAppend ? 1 : 0)), groups);
-    rotate_move_kernel<T, D, kAppend, kNorm><<<grid, threads, 0, s>>>(p);
+template <typename T, int D, bool kAppend> cudaError_t move_t(RotateParams p, int heads, cudaStream_t s) {
+    static std::atomic<int> resident{0};
+    int per_sm = 0;
+    if (cudaError_t e = resident_threads((const void *)rotate_move_kernel<T, D, kAppend>, resident, per_sm); e != cudaSuccess) return e;
+    const MoveGrid m = move_grid(heads, D / (2 * Vec<T>::kN), per_sm, p.n, p.n_out, kAppend);
+    p.heads_per_block = m.heads_per_block;
+    p.blocks = m.blocks;
+    const dim3 grid((unsigned)(m.blocks + m.out_blocks + (kAppend ? 1 : 0)), m.groups);
+    rotate_move_kernel<T, D, kAppend><<<grid, m.threads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int D> cudaError_t rotate_t(const RotateParams &p, cudaStream_t s) {
-    return p.eps > 0.f ? move_t<T, D, false, true>(p, p.H, s) : move_t<T, D, false, false>(p, p.H, s);
+    return move_t<T, D, false>(p, p.H, s);
 }
 template <typename T, int D> cudaError_t append_t(const RotateParams &p, cudaStream_t s) {
-    const int heads = p.H + 2 * p.Hkv;
-    return p.eps > 0.f ? move_t<T, D, true, true>(p, heads, s) : move_t<T, D, true, false>(p, heads, s);
+    return move_t<T, D, true>(p, p.H + 2 * p.Hkv, s);
 }
 
-template <typename T, int D, bool kGrads, bool kNorm> cudaError_t backward_k(RotateBwdParams p, cudaStream_t s) {
-    constexpr int IPR = D / (2 * Vec<T>::kN), kV = kGrads || kNorm ? 4 : 2;
+template <typename T, int D> cudaError_t backward_t(RotateBwdParams p, cudaStream_t s) {
+    constexpr int IPR = D / (2 * Vec<T>::kN);
     p.heads_per_block = p.H < kBwdThreads / IPR ? p.H : kBwdThreads / IPR;
     const dim3 grid(p.n_part, (p.H + p.heads_per_block - 1) / p.heads_per_block);
-    const auto kernel = rotate_backward_kernel<T, D, kGrads, kNorm>;
+    const bool grads = p.d_alpha != nullptr;
+    const auto kernel = grads ? rotate_backward_kernel<T, D, true> : rotate_backward_kernel<T, D, false>;
     constexpr int kSlot = kBwdThreads * 16;
-    static SmemLimit limit;
-    if (cudaError_t e = limit.ensure((const void *)kernel, kBwdDepth * kV * kSlot); e != cudaSuccess) return e;
+    static SmemLimit limit[2];
+    if (cudaError_t e = limit[grads].ensure((const void *)kernel, kBwdDepth * (grads ? 4 : 2) * kSlot); e != cudaSuccess) return e;
     // slots for the tokens of a thread, where those are few
     const int lanes = kBwdThreads / (p.heads_per_block * IPR), step = kTabTokens;
     const long long m = (p.n + p.n_part - 1) / p.n_part, most = (m + step - 1) / step * ((step + lanes - 1) / lanes);
-    int fifo = (int)(most < kBwdDepth ? most : kBwdDepth) * kV * kSlot;
-    if (kGrads && fifo < Vec<T>::kN * kSlot) fifo = Vec<T>::kN * kSlot;  // the sums' exchange
+    int fifo = (int)(most < kBwdDepth ? most : kBwdDepth) * (grads ? 4 : 2) * kSlot;
+    if (grads && fifo < Vec<T>::kN * kSlot) fifo = Vec<T>::kN * kSlot;  // the sums' exchange
     kernel<<<grid, kBwdThreads, fifo, s>>>(p);
     return cudaGetLastError();
-}
-
-template <typename T, int D> cudaError_t backward_t(const RotateBwdParams &p, cudaStream_t s) {
-    if (p.eps > 0.f) return p.d_alpha || p.d_weight ? backward_k<T, D, true, true>(p, s) : backward_k<T, D, false, true>(p, s);
-    return p.d_alpha ? backward_k<T, D, true, false>(p, s) : backward_k<T, D, false, false>(p, s);
 }
 
 }  // namespace
@@ -734,6 +440,7 @@ int rotate_grad_groups(int H, int d, int elem_bytes) {
     const int per = kBwdThreads / (d * elem_bytes / 32);  // heads of a block
     return (H + per - 1) / per;
 }
+
 // Partials of the affine's gradient (blocks along the tokens): kBwdBlocks per
 // SM over all head groups, but no fewer than 16 tokens a block.
 int rotate_grad_parts(long long n, int H, int d, int elem_bytes) {
@@ -768,20 +475,6 @@ cudaError_t launch_rotate_grad_sum(const RotateBwdParams &p, int d, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, rotate_grad_sum_kernel, (const float *)p.partial, p.n_part, cols, p.d_alpha, p.d_beta);
-}
-cudaError_t launch_norm_grad_sum(const RotateBwdParams &p, int d, int elem_bytes, cudaStream_t stream) {
-    const int cols = p.H * d;
-    const int blocks = (p.d_alpha ? 2 * cols / 32 : 0) + (p.d_weight ? d / 32 : 0);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_grad_sum_kernel, p, cols, d, p.n_part * rotate_grad_groups(p.H, d, elem_bytes));
 }
 #undef ORTHROS_BY_TYPE
 

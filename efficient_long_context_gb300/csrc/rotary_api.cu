@@ -1,6 +1,6 @@
 // rotary_api.cu -- C entry points of the rotary positions, with or without a norm
 // of the head: argument checks, the host-side frequency rules, dispatch to
-// rotary.cu.
+// rotary.cu and norm_rotary.cu.
 #include <cmath>
 
 #include "internal.cuh"
@@ -114,7 +114,7 @@ orthros_status rotate_rows(const void *x, long long x_stride, const int32_t *pos
     p.eps = eps;
     p.weight = weight;
     ProfScope ps(name, stream);
-    const cudaError_t e = launch_rotate(p, d, dtype, stream);
+    const cudaError_t e = eps > 0.f ? launch_norm_rotate(p, d, dtype, stream) : launch_rotate(p, d, dtype, stream);
     return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, name);
 }
 
@@ -186,7 +186,7 @@ orthros_status rotate_rows_backward(const void *dy, long long dy_stride, const v
     if (d_weight) p.partial_w = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.weight_off);
     {
         ProfScope ps(norm ? "norm_rotate_backward" : "rotate_backward", stream);
-        const cudaError_t e = launch_rotate_backward(p, d, dtype, stream);
+        const cudaError_t e = norm ? launch_norm_rotate_backward(p, d, dtype, stream) : launch_rotate_backward(p, d, dtype, stream);
         if (e != cudaSuccess) return cuda_error(e, "rotate backward launch");
     }
     if (grads) {
@@ -301,7 +301,7 @@ orthros_status append_rows(const AppendArgs &a, bool by_slot, cudaStream_t strea
     p.num_pages = a.num_pages;
     p.status = status;
     ProfScope ps(name, stream);
-    const cudaError_t e = launch_rotate_append(p, a.d, a.dtype, stream);
+    const cudaError_t e = a.eps > 0.f ? launch_norm_rotate(p, a.d, a.dtype, stream) : launch_rotate_append(p, a.d, a.dtype, stream);
     return e == cudaSuccess ? ORTHROS_OK : cuda_error(e, name);
 }
 
