@@ -35,7 +35,7 @@
 // own that the epilogue adds up, so that the softmax of one tile still runs
 // beside the products of the other.
 //
-// Roles (352 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
+// Roles (384 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
 // one thread per row), warp 8 copies (page lookups by its lanes, TMA boxes of
 // up to 128 tokens within a page), warp 9 issues tcgen05.mma, warp 10 clears value
 // rows that no row of the unit sees. S = Q K^T (bf16,
@@ -67,14 +67,13 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a tile
 constexpr int kKeys = 128;  // keys of a tile
-constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10;
-constexpr int kThreads = 352;
-// At most three of the eleven warps sit on a scheduler: 168 registers a thread
-// fit (3 x 32 x 168 of 16K), so the bound is taken for 384 threads.
-constexpr int kBound = 384;
+constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10, kValueWarp = 11;
+constexpr int kThreads = 384;
 constexpr int kFlagRing = 16;
 // A share of fewer key tiles than this is not worth a CTA of its own.
 constexpr int kMinTiles = 2;
+constexpr int kSingleCost = 3, kPairCost = 4;  // (trees; a share is longer than a tile costs)
+static_assert(kPairCost < kMinTiles * kSingleCost, "every share holds a tile");
 
 template <int D> struct Cfg {
     static constexpr int kNumK = D == 128 ? 3 : 6, kNumV = D == 128 ? 2 : 4;  // stages: 160 KB in flight
@@ -219,6 +218,13 @@ __device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0
     return new_tokens(p, p.q_indptr[b + 1] - tok0, len, wrong);
 }
 
+// What a key tile of a unit costs in the count that the CTAs share out. A tree's unit of two row
+// tiles takes longer for each than one of a single row tile, which waits for HBM: 32 trees of 9 to
+// 60 tokens over 12000 keys in 264 us instead of 284 with equal shares of tiles (265 at 4 : 5, 269 at 2 : 3).
+template <bool kTree> __device__ __forceinline__ int tile_cost(const ChunkParams &p, int cnt) {
+    return !kTree ? 1 : cnt > p.tile_tokens ? kPairCost : kSingleCost;
+}
+
 // The unit that begins at token i of a sequence's nb (i < nb). The tokens of a tree may all see
 // one another: every unit has all the sequence's keys from the window of the first position on.
 template <bool kTree> __device__ __forceinline__ ChunkUnit unit_at(const ChunkParams &p, int b, int tok0, int nb, int len, int i) {
@@ -325,7 +331,10 @@ template <bool kTree> __global__ void __launch_bounds__(kPlanThreads) chunk_plan
             fill_nan(p, tok0, p.q_indptr[b + 1], d, lane, 32);
         }
         long long tiles = 0;
-        for (int i = lane * ut; i < nb; i += 32 * ut) tiles += unit_at<kTree>(p, b, tok0, nb, len, i).n_kt;
+        for (int i = lane * ut; i < nb; i += 32 * ut) {
+            const ChunkUnit u = unit_at<kTree>(p, b, tok0, nb, len, i);
+            tiles += u.n_kt * tile_cost<kTree>(p, u.cnt);
+        }
         tiles = warp_scan(tiles, lane);
         if (lane == 31) {
             p.seq_units[b] = (nb + ut - 1) / ut;
@@ -375,8 +384,9 @@ template <bool kTree> __global__ void __launch_bounds__(kPlanThreads) chunk_plan
             const int i = i0 + lane * ut;
             ChunkUnit u{};
             if (i < nb) u = unit_at<kTree>(p, b, tok0, nb, len, i);
-            const long long sum = warp_scan(u.n_kt, lane);
-            u.start = at + sum - u.n_kt;
+            const int cost = u.n_kt * tile_cost<kTree>(p, u.cnt);
+            const long long sum = warp_scan(cost, lane);
+            u.start = at + sum - cost;
             if (i < nb) p.units[u0 + i / ut] = u;
             at += __shfl_sync(0xffffffffu, sum, 31);
         }
@@ -386,7 +396,7 @@ template <bool kTree> __global__ void __launch_bounds__(kPlanThreads) chunk_plan
 // ---------------------------------------------------------------------------
 // Main kernel
 // ---------------------------------------------------------------------------
-// The shares of a lane: `total` key tiles over `eff` CTAs, equal up to borders that
+// The shares of a lane: `total` key tiles (trees: their costs) over `eff` CTAs, equal up to borders that
 // move to a unit's end within kSnap key tiles (a quarter of a share at most): a
 // cut costs two partial epilogues and a merge, as much as a few tiles.
 constexpr int kSnap = 3;
@@ -398,17 +408,18 @@ struct Shares {
         if (total * eff <= 0xffffffffLL) return (uint32_t)total * (uint32_t)j / (uint32_t)eff;
         return total * j / eff;
     }
-    // border x, which falls into the unit [u0, u0 + n), where it ends up
-    __device__ long long moved(long long x, long long u0, int n) const {
-        return x - u0 <= snap ? u0 : u0 + n - x <= snap ? u0 + n : x;
+    // border x, which falls into the unit [u0, u0 + n) of tiles that cost w, where it ends up
+    __device__ long long moved(long long x, long long u0, int n, int w) const {
+        return x - u0 <= snap ? u0 : u0 + n - x <= snap ? u0 + n : w == 1 ? x : u0 + (int)(x - u0) / w * w;
     }
 };
-__device__ __forceinline__ Shares shares_of(const ChunkParams &p, const ChunkPlan &pl) {
+template <bool kTree> __device__ __forceinline__ Shares shares_of(const ChunkParams &p, const ChunkPlan &pl) {
+    constexpr int kOne = kTree ? kSingleCost : 1;
     Shares s;
     s.total = (long long)(p.Hkv / p.lanes) * pl.tiles;
-    s.eff = (int)max(1LL, min((long long)p.per_lane, s.total / kMinTiles));
-    s.snap = 0;  // the largest with 4 snap eff <= total, up to kSnap
-    while (s.snap < kSnap && 4LL * (s.snap + 1) * s.eff <= s.total) ++s.snap;
+    s.eff = (int)max(1LL, min((long long)p.per_lane, s.total / (kMinTiles * kOne)));
+    s.snap = 0;  // the largest with 4 snap eff <= total, up to kSnap tiles
+    while (s.snap < kSnap * kOne && 4LL * (s.snap + 1) * s.eff <= s.total) ++s.snap;
     return s;
 }
 
@@ -427,6 +438,20 @@ __device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
     return lo;
 }
 
+// First token row (of the pool) of box `lane` of key tile kt, for keys [lo, hi] that exist, or past the
+// pool: the copy then fills zeros. bad: a page id outside the pool.
+__device__ __forceinline__ int box_row(const ChunkParams &p, const int32_t *bt, int kt, int lo, int hi, int lane, int &bad) {
+    const int key = kt * kKeys + lane * p.box;
+    bad = 0;
+    if (lane * p.box >= kKeys || key > hi || key + p.box - 1 < lo) return p.num_pages * p.page_size;
+    const int pg = bt[key / p.page_size];
+    if (pg < 0 || pg >= p.num_pages) {
+        bad = 1;
+        return p.num_pages * p.page_size;
+    }
+    return pg * p.page_size + key % p.page_size;
+}
+
 // Whether key tile `it` of a segment has rows that none of its unit's tokens sees:
 // all but rows [r0, r1).
 template <bool kTree> __device__ __forceinline__ bool unseen_rows(const Segment &sg, const TreeSegment &ts, int window, int it, int &r0, int &r1) {
@@ -437,7 +462,7 @@ template <bool kTree> __device__ __forceinline__ bool unseen_rows(const Segment 
 }
 
 template <int D, bool kTree>
-__global__ void __launch_bounds__(kBound, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = Cfg<D>;
@@ -476,7 +501,7 @@ __global__ void __launch_bounds__(kBound, 1)
         mbar_init(&mt.ml_free, kRows);
         for (int r = 0; r < kSegRing; ++r) {
             mbar_init(&mt.g_full[r], 1);
-            mbar_init(&mt.g_empty[r], kSoftmaxWarps + 2);
+            mbar_init(&mt.g_empty[r], kSoftmaxWarps + 3);
         }
         mbar_init(&mt.mma_done, 1);
         mt.abort = 0;
@@ -530,8 +555,9 @@ __global__ void __launch_bounds__(kBound, 1)
             }
             const int i = one ? lane * ut : 0;
             if (order && i < nb) own = unit_at<kTree>(p, b, tok0, nb, len, i);
-            const long long sum = warp_scan(own.n_kt, lane);
-            own.start = sum - own.n_kt;
+            const int cost = own.n_kt * tile_cost<kTree>(p, own.cnt);
+            const long long sum = warp_scan(cost, lane);
+            own.start = sum - cost;
             pl.units = 32;
             pl.tiles = __shfl_sync(0xffffffffu, sum, 31);
         } else {
@@ -561,8 +587,8 @@ __global__ void __launch_bounds__(kBound, 1)
         const int ln = blockIdx.x % p.lanes, j = blockIdx.x / p.lanes;
         ChunkHead head{};
         long long head_u0 = 0;  // first key tile and key tiles of the unit it names
-        int head_n = 0;
-        uint32_t gk = 0, gv = 0;  // key and value copies issued
+        int head_n = 0, head_w = 1;
+        uint32_t gk = 0;  // key copies issued
         uint32_t nq[2] = {0, 0};  // query tiles issued per slot
         int ring = 0;
         bool alive = true;
@@ -580,7 +606,7 @@ __global__ void __launch_bounds__(kBound, 1)
             return true;
         };
         if (pl.tiles > 0) {
-            const Shares sh = shares_of(p, pl);
+            const Shares sh = shares_of<kTree>(p, pl);
             if (j < sh.eff) {
                 // both borders of the share, moved, the end first (one body for both: this code runs
                 // once, from a cold instruction cache); the unit that it begins with
@@ -597,8 +623,9 @@ __global__ void __launch_bounds__(kBound, 1)
                     u = find(x - kvo * pl.tiles);
                     const ChunkUnit e = get_unit(u);
                     const long long u0 = kvo * pl.tiles + e.start;
-                    x = sh.moved(x, u0, e.n_kt);
-                    past = x == u0 + e.n_kt;
+                    const int w = tile_cost<kTree>(p, e.cnt);
+                    x = sh.moved(x, u0, e.n_kt * w, w);
+                    past = x == u0 + e.n_kt * w;
                 }
                 auto next_unit = [&]() {  // (a lane without a unit is passed over)
                     do {
@@ -611,8 +638,10 @@ __global__ void __launch_bounds__(kBound, 1)
                 if (past) next_unit();
                 while (x < x1 && alive) {
                     const ChunkUnit un = get_unit(u);
-                    const int a = (int)(x - kvo * pl.tiles - un.start);
-                    const int n_tiles = (int)min((long long)(un.n_kt - a), x1 - x);
+                    const int w = tile_cost<kTree>(p, un.cnt);
+                    const int a = (int)(x - kvo * pl.tiles - un.start) / w;
+                    const int n_tiles = kTree ? min(un.n_kt - a, (int)(min(x1 - x, (long long)un.n_kt * w)) / w)
+                                              : (int)min((long long)(un.n_kt - a), x1 - x);
                     Segment sg;
                     sg.end = 0;
                     sg.b = un.b;
@@ -629,7 +658,8 @@ __global__ void __launch_bounds__(kBound, 1)
                     sg.partial = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
                     if (starts && !ends) {
                         head_u0 = x;
-                        head_n = un.n_kt;
+                        head_n = un.n_kt * w;
+                        head_w = w;
                         head.tok0 = un.tok0;
                         head.cnt = un.cnt;
                         head.kv = sg.kv;
@@ -668,23 +698,13 @@ __global__ void __launch_bounds__(kBound, 1)
                     const int32_t *bt = p.block_table + (long long)sg.b * p.max_pages;
                     const int key_hi = kTree ? un.key_end - 1 : un.pos0 + un.cnt - 1;
                     const int key_lo = max(0, un.pos0 - p.window + 1);
-                    const int oob = p.num_pages * p.page_size;  // past the pool: the copy fills zeros
                     const int box = p.box;
                     const int n_box = box ? kKeys / box : 0;
-                    // first token row of this lane's box of a tile (TMA), or oob; bad: page id outside the pool
                     // (The page is awaited here, a tile before its use: awaited at its use, decoding took 1 %
                     // longer, its copies less in step with those of the other heads.)
                     auto look = [&](int kt, int &bad) -> int {
                         bad = 0;
-                        if (lane >= n_box) return oob;
-                        const int key = kt * kKeys + lane * box;
-                        if (key > key_hi || key + box - 1 < key_lo) return oob;
-                        const int pg = bt[key / p.page_size];
-                        if (pg < 0 || pg >= p.num_pages) {
-                            bad = 1;
-                            return oob;
-                        }
-                        return pg * p.page_size + key % p.page_size;
+                        return box ? box_row(p, bt, kt, key_lo, key_hi, lane, bad) : 0;
                     };
                     int bad_next = 0, tok_next = look(sg.kt0, bad_next);
                     for (int it = 0; it < sg.nkt; ++it) {
@@ -708,20 +728,6 @@ __global__ void __launch_bounds__(kBound, 1)
                             __syncwarp();
                             if (lane < n_box)
                                 tma_load_5d(ks + lane * box * D * 2, &tm_k, &mt.k_full[sk], 0, 0, 0, tok >> 3, sg.kv);
-                            if (gi >= (uint32_t)kNumV &&
-                                !mbar_wait_warp(&mt.v_empty[sv], ((gi / kNumV) - 1) & 1, abort, status)) {
-                                ++gk;
-                                alive = false;
-                                break;
-                            }
-                            int r0, r1;
-                            const bool edge = unseen_rows<kTree>(sg, ts, p.window, it, r0, r1);
-                            uint64_t *full = edge ? &mt.ve_full[sv] : &mt.v_full[sv];
-                            if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
-                            __syncwarp();
-                            if (lane < n_box)
-                                tma_load_5d(vs + lane * box * D * 2, &tm_v, full, 0, 0, 0, tok >> 3, sg.kv);
-                            ++gv;
                         } else {
                             // page sizes without a copy box: the lanes gather the rows, 16 bytes at a time
                             if (gi >= (uint32_t)kNumV &&
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kBound, 1)
                         }
                         ++gk;
                     }
-                    x += n_tiles;
+                    x += n_tiles * w;
                     next_unit();
                 }
             }
@@ -773,11 +779,11 @@ __global__ void __launch_bounds__(kBound, 1)
         }
         if (head_n > 0) {
             // the CTAs whose share begins inside the unit hold its other parts
-            const Shares sh = shares_of(p, pl);
+            const Shares sh = shares_of<kTree>(p, pl);
             head.n_parts = 1;
             for (int k0 = j + 1; k0 < sh.eff; k0 += 32) {  // (a lane looks at one border)
                 const int k = k0 + lane;
-                const unsigned in = __ballot_sync(0xffffffffu, k < sh.eff && sh.moved(sh.border(k), head_u0, head_n) < head_u0 + head_n);
+                const unsigned in = __ballot_sync(0xffffffffu, k < sh.eff && sh.moved(sh.border(k), head_u0, head_n, head_w) < head_u0 + head_n);
                 head.n_parts += __popc(in);
                 if (in != 0xffffffffu) break;
             }
@@ -792,8 +798,6 @@ __global__ void __launch_bounds__(kBound, 1)
             if (p.box) {
                 for (uint32_t i = gk > (uint32_t)kNumK ? gk - kNumK : 0; i < gk; ++i)
                     mbar_wait_drain(&mt.k_full[i % kNumK], (i / kNumK) & 1, status);
-                for (uint32_t i = gv > (uint32_t)kNumV ? gv - kNumV : 0; i < gv; ++i)
-                    mbar_wait_drain(&mt.v_full[i % kNumV], (i / kNumV) & 1, status);
             }
             for (int s = 0; s < 2; ++s)
                 if (nq[s] > 0) mbar_wait_drain(&mt.q_full[s], (nq[s] - 1) & 1, status);
@@ -953,6 +957,45 @@ __global__ void __launch_bounds__(kBound, 1)
             if (lane == 0) mbar_wait_drain(&mt.mma_done, 0, status);
         }
         __syncwarp();
+    } else if (warp == kValueWarp) {
+        // ---------------- value copies: a warp of their own, so that neither kind waits for the
+        // other's free stage or for the issue of its boxes (pages of 16 tokens: eight a tile) ----------------
+        uint32_t gv = 0;  // value copies issued
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int r = i % kSegRing;
+            if (!mbar_wait_warp(&mt.g_full[r], (i / kSegRing) & 1, abort, status)) break;
+            const Segment sg = mt.seg[r];
+            TreeSegment ts;
+            if constexpr (kTree) ts = mt.tree[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mt.g_empty[r]);
+            if (sg.end) break;
+            if (!p.box) continue;  // (gathered with the keys)
+            const int32_t *bt = p.block_table + (long long)sg.b * p.max_pages;
+            int key_hi = sg.pos0 + sg.cnt - 1;
+            if constexpr (kTree) key_hi = ts.key_end - 1;
+            const int key_lo = max(0, sg.pos0 - p.window + 1);
+            int bad, tok_next = box_row(p, bt, sg.kt0, key_lo, key_hi, lane, bad);
+            for (int it = 0; it < sg.nkt; ++it) {
+                const int sv = gv % kNumV;
+                const int tok = tok_next;
+                if (it + 1 < sg.nkt) tok_next = box_row(p, bt, sg.kt0 + it + 1, key_lo, key_hi, lane, bad);
+                if (gv >= (uint32_t)kNumV && !(ok = mbar_wait_warp(&mt.v_empty[sv], ((gv / kNumV) - 1) & 1, abort, status))) break;
+                int r0, r1;
+                const bool edge = unseen_rows<kTree>(sg, ts, p.window, it, r0, r1);
+                uint64_t *full = edge ? &mt.ve_full[sv] : &mt.v_full[sv];
+                if (lane == 0) mbar_arrive_expect_tx(full, C::kTile);
+                __syncwarp();
+                if (lane * p.box < kKeys)
+                    tma_load_5d(smem + C::kV0 + sv * C::kTile + lane * p.box * D * 2, &tm_v, full, 0, 0, 0, tok >> 3, sg.kv);
+                ++gv;
+            }
+        }
+        // nothing may be in flight when the CTA leaves
+        if (lane == 0)
+            for (uint32_t i = gv > (uint32_t)kNumV ? gv - kNumV : 0; i < gv; ++i)
+                mbar_wait_drain(&mt.v_full[i % kNumV], (i / kNumV) & 1, status);
     } else if (warp == kClearWarp) {
         // ---------------- unseen value rows: a page that reaches past the unit's keys holds
         // anything there, and 0 * NaN is NaN ----------------
@@ -1274,7 +1317,12 @@ __global__ void __launch_bounds__(kBound, 1)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRows = 32;    // a block per row up to so many rows of a partial
+constexpr int kWide = 4;          // rows of a block (kWideRows; eight took 3 us longer for one tree)
 constexpr int kMergeBlocks = 16;  // blocks of a unit beyond
+
+// How the merge's threads take the rows: 8 lanes a row, as many lanes as a row has 16-byte words (and
+// four times the parts at once), or a block a row.
+enum MergeMap { kFewLanes, kWideRows, kRowBlocks };
 
 // Running joint of parts of one row: kLanes lanes, lane l with channels 4 kLanes i + 4 l .. + 3, i < V.
 template <int V, bool kTree> struct Joint {
@@ -1314,7 +1362,7 @@ template <int V, bool kTree> struct Joint {
     }
 };
 
-template <int D, bool kRowBlocks, bool kTree>
+template <int D, int kMap, bool kTree>
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
     const int tid = threadIdx.x, g = p.Hq / p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1348,8 +1396,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
     auto store = [&](long long out, int chunk, const float4 &a, float inv) {
         reinterpret_cast<uint2 *>(p.o + out * D)[chunk] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     };
-    if constexpr (!kRowBlocks) {
-        constexpr int kLanes = 8, V = D / (4 * kLanes), kParts = 2;
+    if constexpr (kMap != kRowBlocks) {
+        constexpr int kLanes = kMap == kFewLanes ? 8 : D / 4, V = D / (4 * kLanes), kParts = kMap == kFewLanes ? 2 : 8;
         const int lane = tid % kLanes;
         for (int r = (blockIdx.y * kMergeWarps * 32 + tid) / kLanes; r < cap; r += gridDim.y * kMergeWarps * (32 / kLanes)) {
             const long long out = out_row(r);
@@ -1448,14 +1496,21 @@ template <int D, bool kTree> cudaError_t launch_d(const ChunkParams &p, cudaStre
         if (cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_attn_kernel<D, kTree>, tq, tk, tv, p); e != cudaSuccess) return e;
     }
     const int rows = p.slots_cap * p.rows_cap;
+    // parts of a unit at least (the CTAs over all kv heads' units, were they alike): where they are many, a
+    // row's are read by as many lanes as have a word of it (a tree of 25 tokens over 32000 keys: 44 -> 38 us;
+    // 12 trees of 60 tokens over 6000 keys would take 84 instead of 77)
+    const long long units = (long long)p.Hkv * p.B * ((p.max_new + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
+    const bool wide = kTree && p.lanes * p.per_lane >= 8 * units;
     cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3(p.lanes * p.per_lane, rows <= kMergeRows ? rows : kMergeBlocks);
+    mc.gridDim = dim3(p.lanes * p.per_lane, rows <= kMergeRows ? rows : wide ? (rows + kWide - 1) / kWide : kMergeBlocks);
     mc.blockDim = dim3(kMergeWarps * 32);
     mc.stream = stream;
     mc.attrs = attr;
     mc.numAttrs = 1;
     ProfScope ps("chunk_merge", stream);
-    if (cudaError_t e = cudaLaunchKernelEx(&mc, rows <= kMergeRows ? chunk_merge_kernel<D, true, kTree> : chunk_merge_kernel<D, false, kTree>, p); e != cudaSuccess)
+    if (cudaError_t e = cudaLaunchKernelEx(&mc, rows <= kMergeRows ? chunk_merge_kernel<D, kRowBlocks, kTree>
+                                                     : wide             ? chunk_merge_kernel<D, kWideRows, kTree>
+                                                                        : chunk_merge_kernel<D, kFewLanes, kTree>, p); e != cudaSuccess)
         return e;
     return cudaGetLastError();
 }

@@ -466,8 +466,9 @@ struct TreeCommitParams {
     const int32_t *block_table, *q_indptr, *kv_lens, *accepted, *n_accepted;
     int32_t *cache_lens;
     int layers, B, most, max_pages, page_size, num_pages, row_bytes;
+    int layers_per_block;  // set by the launcher
     uint32_t *status;
 };
-cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t stream);
+cudaError_t launch_tree_commit(TreeCommitParams p, cudaStream_t stream);
 
 }  // namespace orthros

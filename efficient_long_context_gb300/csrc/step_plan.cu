@@ -46,9 +46,9 @@ __device__ __forceinline__ int last_at_most(const int *a, int n, int x) {
 
 // One sequence's part of the plan.
 struct Need {
-    int rows, cached, held, need;  // tokens of the step, cached ones, pages held, pages needed
-    int lack, back;                // pages to take, pages to give back
-    bool wrong;                    // lengths that cannot be
+    int rows, cached, held;  // tokens of the step, cached ones, pages held
+    int lack, back;          // pages to take, pages to give back
+    bool ends, wrong;        // has ended; lengths that cannot be
 };
 __device__ __forceinline__ Need need_of(const StepPlanParams &p, int b) {
     Need s;
@@ -59,16 +59,11 @@ __device__ __forceinline__ Need need_of(const StepPlanParams &p, int b) {
     const long long total = (long long)s.cached + s.rows;
     s.wrong = s.cached < 0 || m < -1 || s.held < 0 || s.held > p.max_pages || total > (long long)p.max_pages * p.page_size ||
               (p.parents && m > p.max_tree);
-    s.need = s.held;
     s.lack = s.back = 0;
+    s.ends = !s.wrong && m < 0;
     if (s.wrong) return s;
-    if (m < 0) {
-        s.back = s.held;
-        s.need = 0;
-    } else {
-        s.need = max(s.held, (int)((total + p.page_size - 1) / p.page_size));
-        s.lack = s.need - s.held;
-    }
+    if (s.ends) s.back = s.held;
+    else s.lack = max(s.held, (int)((total + p.page_size - 1) / p.page_size)) - s.held;
     return s;
 }
 
@@ -76,12 +71,13 @@ __device__ __forceinline__ void cluster_arrive_wait() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParams p) {
+// kWords: 32-bit words that hold a token's mask (0: no trees), at least p.words.
+template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParams p) {
     extern __shared__ int sm[];
-    int *start = sm;             // [B] first token row
-    int *cached = sm + p.B;      // [B] cached tokens, or -1: the sequence has no place in this step
-    int *held = sm + 2 * p.B;    // [B] pages held before
-    int *off = sm + 3 * p.B;     // [B] pages taken by the sequences before it
+    int *start = sm;                  // [B + 1] first token row
+    int *off = start + p.B + 1;       // [B + 1] pages taken by the sequences before it
+    int *cached = off + p.B + 1;      // [B] cached tokens, or -1: the sequence has no place in this step
+    int *held = cached + p.B;         // [B] pages held before, or -1: it has ended
     __shared__ long long wsum[3][kWarps], carry[3];
     __shared__ int s_taken;
     __shared__ uint32_t s_flags;
@@ -114,21 +110,31 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
         for (int k = 0; k < 3; ++k) v[k] += carry[k] + (warp ? wsum[k][warp - 1] : 0);
         if (b < p.B) {
             // (held to 32 bits: sums past the tokens or the pool refuse the step below)
-            start[b] = (int)min(v[0] - s.rows, 0x7fffffffLL);
+            start[b + 1] = (int)min(v[0], 0x7fffffffLL);
+            off[b + 1] = (int)min(v[1], 0x7fffffffLL);
             cached[b] = s.wrong ? -1 : s.cached;
-            held[b] = s.held;
-            off[b] = (int)min(v[1] - s.lack, 0x7fffffffLL);
+            held[b] = s.ends ? -1 : s.held;
+            if (b == 0) start[0] = off[0] = 0;
         }
-        // rank 0 gives the pages of ended sequences back, a warp its own lanes'; nobody reads the stack
-        // or these table rows yet
+        // ended sequences' pages go back, the lanes' of a warp one after the other by all of it, the warps
+        // shared out over the ranks; nobody reads the stack or these table rows yet
         const long long to = count + v[2] - s.back;
-        unsigned gives = __ballot_sync(0xffffffffu, rank == 0 && s.back > 0 && count >= 0 && to + s.back <= p.num_pages);
+        unsigned gives = __ballot_sync(0xffffffffu, warp % ctas == rank && s.back > 0 && count >= 0 && to + s.back <= p.num_pages);
         for (; gives; gives &= gives - 1) {
             const int src = __ffs(gives) - 1;
             const int n = __shfl_sync(0xffffffffu, s.back, src);
             int32_t *at = p.free_pages + __shfl_sync(0xffffffffu, to, src);
             const int32_t *row = p.block_table + (long long)(base + warp * 32 + src) * p.max_pages;
-            for (int i = lane; i < n; i += 32) at[i] = row[i];
+            constexpr int kPages = 8;  // of a lane at a time, loaded before the first is stored
+            for (int i0 = lane; i0 < n; i0 += 32 * kPages) {
+                int id[kPages];
+#pragma unroll
+                for (int u = 0; u < kPages; ++u)
+                    if (i0 + 32 * u < n) id[u] = row[i0 + 32 * u];
+#pragma unroll
+                for (int u = 0; u < kPages; ++u)
+                    if (i0 + 32 * u < n) at[i0 + 32 * u] = id[u];
+            }
         }
         __syncthreads();
         if (tid < 3) carry[tid] += wsum[tid][kWarps - 1];
@@ -141,11 +147,9 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
     // a sequence whose pages are not all there takes none
     int taken = 0;
     for (int b = tid; b < p.B && !none; b += kThreads) {
-        if (cached[b] < 0) continue;
-        const Need s = need_of(p, b);
-        if (s.lack == 0) continue;
-        if (off[b] + (long long)s.lack <= avail) {
-            taken = max(taken, off[b] + s.lack);
+        if (cached[b] < 0 || off[b + 1] == off[b]) continue;
+        if (off[b + 1] <= avail) {
+            taken = off[b + 1];  // (they ascend)
         } else {
             cached[b] = -1;
             flags |= ORTHROS_DEV_NO_PAGES;
@@ -153,25 +157,20 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
     }
     if (taken) atomicMax(&s_taken, taken);
     if (flags) atomicOr(&s_flags, flags);
-    __syncthreads();
-    taken = s_taken;
-    // what rank 0 writes for each sequence, before its inputs are written over
+    // lengths and pages of sequences that change nothing, before they may be written over
     constexpr int kMine = kPlanMaxSeqs / kThreads;
-    int kv[kMine], own[kMine], len[kMine];
+    int len[kMine], own[kMine];
     if (rank == 0) {
-        if (tid == 0) *p.status = s_flags;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
             const int b = tid + k * kThreads;
             if (b >= p.B) break;
-            const Need s = need_of(p, b);
-            const bool in = !none && cached[b] >= 0;
-            own[k] = in ? s.need : s.held;
-            const bool ends = p.new_lens[b] < 0;
-            kv[k] = in && !ends ? s.cached + s.rows : 0;
-            len[k] = !in ? s.cached : ends ? 0 : s.cached + s.rows;
+            if (none || cached[b] < 0) len[k] = p.cache_lens[b], own[k] = p.held_in[b];
         }
     }
+    __syncthreads();
+    taken = s_taken;
+    if (rank == 0 && tid == 0) *p.status = s_flags;
     if (ctas > 1) cluster_arrive_wait();
     else __syncthreads();
 
@@ -181,8 +180,14 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
         for (int k = 0; k < kMine; ++k) {
             const int b = tid + k * kThreads;
             if (b >= p.B) break;
+            int kv = 0;
+            if (!none && cached[b] >= 0) {
+                const bool ends = held[b] < 0;
+                kv = len[k] = ends ? 0 : cached[b] + start[b + 1] - start[b];
+                own[k] = ends ? 0 : held[b] + off[b + 1] - off[b];
+            }
             p.q_indptr[b] = none ? -1 : start[b];
-            p.kv_lens[b] = kv[k];
+            p.kv_lens[b] = kv;
             p.held_out[b] = own[k];
             if (p.lens_out) p.lens_out[b] = len[k];
         }
@@ -201,9 +206,9 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
     const int real = none ? 0 : (int)rows;
     for (int i = at0; i < p.n; i += step) {
         int seq = -1, pos = 0, slot = -1;
-        uint32_t m[kTreeMaxTokens / 32];
+        uint32_t m[kWords > 0 ? kWords : 1];
 #pragma unroll
-        for (int w = 0; w < kTreeMaxTokens / 32; ++w) m[w] = 0;
+        for (int w = 0; w < kWords; ++w) m[w] = 0;
         if (i < real) {
             const int b = last_at_most(start, p.B, i);
             if (cached[b] >= 0) {
@@ -212,13 +217,11 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
                 pos = cached[b] + j;
                 const int pg = pos / p.page_size, in = pos - pg * p.page_size;
                 const int id = pg < held[b] ? p.block_table[(long long)b * p.max_pages + pg] : on_stack(off[b] + pg - held[b]);
-                if (id >= 0 && id < p.num_pages) slot = id * p.page_size + in;
-                else found |= ORTHROS_DEV_BAD_PAGE;
-                if (p.parents) {  // up the tree
+                if constexpr (kWords > 0) {  // up the tree
                     int at = j, depth = 0;
                     while (true) {
 #pragma unroll
-                        for (int w = 0; w < kTreeMaxTokens / 32; ++w)
+                        for (int w = 0; w < kWords; ++w)
                             if (at >> 5 == w) m[w] |= 1u << (at & 31);
                         const int up = __ldg(p.parents + start[b] + at);
                         if (up < -1 || up >= at) found |= ORTHROS_DEV_BAD_POSITION;
@@ -228,16 +231,16 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
                     }
                     pos = cached[b] + depth;
                 }
+                if (id >= 0 && id < p.num_pages) slot = id * p.page_size + in;
+                else found |= ORTHROS_DEV_BAD_PAGE;
             }
         }
         p.token_seq[i] = seq;
         p.token_pos[i] = pos;
         p.token_slots[i] = slot;
-        if (p.parents) {
 #pragma unroll
-            for (int w = 0; w < kTreeMaxTokens / 32; ++w)
-                if (w < p.words) p.tree_mask[(long long)i * p.words + w] = m[w];
-        }
+        for (int w = 0; w < kWords; ++w)
+            if (w < p.words) p.tree_mask[(long long)i * p.words + w] = m[w];
     }
     if (found) atomicOr(p.status, found);
 }
@@ -246,8 +249,9 @@ __global__ void __launch_bounds__(kThreads) step_plan_kernel(const StepPlanParam
 // Commit: token acc[i] of sequence b's tree goes from place L + acc[i] to L + i, in every
 // layer's keys and values. The path ascends (acc[i] >= i), so a thread that owns 16 bytes of
 // the rows may move them in order, kMoves loads in flight before their stores: what a store
-// overwrites has been read. One block per sequence and layer; blocks past the sequences check all
-// paths and write the status word, as the moving blocks of the first layer write the lengths.
+// overwrites has been read. A block takes a sequence in as many layers as let all blocks run at once,
+// its moves laid end to end; blocks past the sequences check all paths and write the status word, as
+// the moving blocks of the first layer write the lengths.
 // ---------------------------------------------------------------------------
 constexpr int kCommitThreads = 256, kMoves = 8;
 
@@ -289,9 +293,10 @@ __device__ __forceinline__ uint32_t place_of(const TreeCommitParams &p, int b, c
 
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeCommitParams p) {
     __shared__ long long from[kTreeMaxTokens], to[kTreeMaxTokens];
-    const int tid = threadIdx.x, b = blockIdx.x, layer = blockIdx.y;
+    const int tid = threadIdx.x, b = blockIdx.x;
+    const int layer0 = blockIdx.y * p.layers_per_block, layers = min(p.layers_per_block, p.layers - layer0);
     if (b == p.B) {  // the status word
-        if (layer > 0) return;
+        if (layer0 > 0) return;
         uint32_t flags = 0;
         const long long places = (long long)p.B * p.most;
 #pragma unroll 4
@@ -313,20 +318,32 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
     uint32_t wrong = a.flags;
     for (int i = tid; i < a.n; i += kCommitThreads) wrong |= place_of(p, b, a, i, from[i], to[i]);
     wrong = __syncthreads_or(wrong);
-    if (layer == 0 && tid == 0 && a.known) p.cache_lens[b] = a.first + (wrong ? 0 : a.n);
+    if (layer0 == 0 && tid == 0 && a.known) p.cache_lens[b] = a.first + (wrong ? 0 : a.n);
     if (wrong) return;  // nothing of this sequence moves
     const int chunks = p.row_bytes / 16;
     const long long pool = (long long)p.num_pages * p.page_size * p.row_bytes;
     for (int c = tid; c < 2 * chunks; c += kCommitThreads) {
-        uint8_t *at = (c < chunks ? p.k_cache : p.v_cache) + layer * pool + (c < chunks ? c : c - chunks) * 16LL;
-        for (int i0 = 0; i0 < a.n; i0 += kMoves) {
+        uint8_t *at = (c < chunks ? p.k_cache : p.v_cache) + layer0 * pool + (c < chunks ? c : c - chunks) * 16LL;
+        // (a batch may span layers: their moves do not touch one another)
+        int i = 0, left = layers * a.n;
+        while (left > 0) {
             uint4 r[kMoves];
+            uint8_t *dst[kMoves];
+#pragma unroll
+            for (int u = 0; u < kMoves; ++u) {
+                dst[u] = nullptr;
+                if (u < left) {
+                    if (from[i] != to[i]) {
+                        r[u] = *reinterpret_cast<const uint4 *>(at + from[i] * p.row_bytes);
+                        dst[u] = at + to[i] * p.row_bytes;
+                    }
+                    if (++i == a.n) i = 0, at += pool;
+                }
+            }
 #pragma unroll
             for (int u = 0; u < kMoves; ++u)
-                if (i0 + u < a.n && from[i0 + u] != to[i0 + u]) r[u] = *reinterpret_cast<const uint4 *>(at + from[i0 + u] * p.row_bytes);
-#pragma unroll
-            for (int u = 0; u < kMoves; ++u)
-                if (i0 + u < a.n && from[i0 + u] != to[i0 + u]) *reinterpret_cast<uint4 *>(at + to[i0 + u] * p.row_bytes) = r[u];
+                if (dst[u]) *reinterpret_cast<uint4 *>(dst[u]) = r[u];
+            left -= kMoves;
         }
     }
 }
@@ -334,9 +351,11 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
 }  // namespace
 
 cudaError_t launch_step_plan(const StepPlanParams &p, cudaStream_t stream) {
-    static SmemLimit limit;
-    const int smem = 4 * p.B * (int)sizeof(int);
-    if (cudaError_t e = limit.ensure((const void *)step_plan_kernel, 4 * kPlanMaxSeqs * (int)sizeof(int)); e != cudaSuccess) return e;
+    const auto kernel = p.words == 0 ? step_plan_kernel<0> : p.words <= 2 ? step_plan_kernel<2> : step_plan_kernel<kTreeMaxTokens / 32>;
+    static SmemLimit limit[3];
+    const int which = p.words == 0 ? 0 : p.words <= 2 ? 1 : 2;
+    auto bytes = [](int B) { return (4 * B + 2) * (int)sizeof(int); };
+    if (cudaError_t e = limit[which].ensure((const void *)kernel, bytes(kPlanMaxSeqs)); e != cudaSuccess) return e;
     int ctas = 1;  // CTAs of the cluster: 1024 tokens each, up to the portable eight
     while (ctas < kMaxCluster && p.n > ctas * kThreads) ctas *= 2;
     cudaLaunchAttribute attr[1];
@@ -346,15 +365,20 @@ cudaError_t launch_step_plan(const StepPlanParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = bytes(p.B);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, step_plan_kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_tree_commit(const TreeCommitParams &p, cudaStream_t stream) {
-    tree_commit_kernel<<<dim3(p.B + 1, p.layers), kCommitThreads, 0, stream>>>(p);
+cudaError_t launch_tree_commit(TreeCommitParams p, cudaStream_t stream) {
+    // blocks that run at once: eight an SM, by threads
+    const int fit = 8 * device_sm_count();
+    p.layers_per_block = (int)(((long long)p.layers * p.B + fit - 1) / fit);
+    if (p.layers_per_block > p.layers) p.layers_per_block = p.layers;
+    const int groups = (p.layers + p.layers_per_block - 1) / p.layers_per_block;
+    tree_commit_kernel<<<dim3(p.B + 1, groups), kCommitThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
