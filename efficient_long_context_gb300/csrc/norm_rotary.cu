@@ -450,31 +450,35 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_backward_kernel(
 // The gradients from the blocks' sums: d_alpha = w (.) S and d_beta from the n_part partials
 // [n_part, 2, H d], and d_w from the n_w block sums [n_w, d] of alpha (.) S. Blocks of 32 columns:
 // 2 H d / 32 for the affine's (none when they are not wanted), then d / 32 for the weight's.
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const RotateBwdParams p, int cols, int d, int n_w) {
-    __shared__ float red[8][32];
+constexpr int kSumWarps = 32;  // of a block: a partial a lane and a few loads each, all in flight at once
+
+__global__ void __launch_bounds__(kSumWarps * 32) norm_grad_sum_kernel(const RotateBwdParams p, int cols, int d, int n_w) {
+    __shared__ float red[kSumWarps][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int affine = p.d_alpha ? 2 * cols / 32 : 0;
     const bool weight = (int)blockIdx.x >= affine;
-    const int col = (weight ? blockIdx.x - affine : blockIdx.x) * 32 + lane;
-    const float *from = (weight ? p.partial_w : p.partial) + col;
+    const int col0 = (weight ? blockIdx.x - affine : blockIdx.x) * 32;
+    const float *from = (weight ? p.partial_w : p.partial) + col0 + lane;
     const int n = weight ? n_w : p.n_part;
     const long long step = weight ? d : 2 * cols;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // (a dependent launch: the partials are there now)
-    int i = w;
-    for (; i + 24 < n; i += 32) {
-        s0 += from[i * step];
-        s1 += from[(i + 8) * step];
-        s2 += from[(i + 16) * step];
-        s3 += from[(i + 24) * step];
-    }
-    for (; i < n; i += 8) s0 += from[i * step];
-    red[w][lane] = (s0 + s1) + (s2 + s3);
-    __syncthreads();
-    if (w == 0) {
-        float s = 0.f;
+    constexpr int kLoads = 8;
+    float s = 0.f;
+    for (int i0 = w; i0 < n; i0 += kLoads * kSumWarps) {
+        float x[kLoads];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += red[k][lane];
+        for (int u = 0; u < kLoads; ++u) x[u] = i0 + u * kSumWarps < n ? from[(i0 + u * kSumWarps) * step] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) s += x[u];
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    // warp w adds up column w
+    s = red[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+        const int col = col0 + w;
         if (weight) p.d_weight[col] = s;
         else if (col < cols) p.d_alpha[col] = p.weight ? s * p.weight[col % d] : s;
         else p.d_beta[col - cols] = s;
@@ -541,7 +545,7 @@ cudaError_t launch_norm_grad_sum(const RotateBwdParams &p, int d, int elem_bytes
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kSumWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
