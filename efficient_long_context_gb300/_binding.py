@@ -933,6 +933,8 @@ def orthros_norm_rotate_append(q, k_new, v_new, k_cache, v_cache, token_slots, t
                 alpha_base=alpha_base, beta_base=beta_base, alpha_out=alpha_out, beta_out=beta_out, out=out,
                 workspace=workspace)
     lib = _lib or load_library()
+    if eps and not eps >= 1.2e-38:
+        raise OrthrosError(1, f"eps = {eps}: 0 (no norm), or positive in 32 bits")
     dev, here = _here(k_cache)
     dtype = k_new.dtype
     n, Hkv, d = k_new.shape
@@ -1018,7 +1020,7 @@ def orthros_plan_step(cache_lens, new_lens, pages_held, free_pages, free_count, 
         raise OrthrosError(1, "out.tree_mask must be a tensor")
     rc = lib.orthros_plan_step(
         _index("cache_lens", cache_lens, dev, B), _index("new_lens", new_lens, dev, B), _index("pages_held", pages_held, dev, B),
-        _index("free_count", free_count, dev, 1), _index("parents", parents, dev, n), max_tree,
+        _index("free_count", free_count, dev, 1), _index("parents", parents, dev, n), _int32(max_tree),
         _index("free_pages", free_pages, dev, free_pages.numel()), _index("block_table", block_table, dev, B * max_pages), B, n,
         max_pages, page_size, free_pages.numel(), _index("q_indptr", out.q_indptr, dev, B + 1),
         _index("kv_lens", out.kv_lens, dev, B), _index("cache_lens", out.cache_lens, dev, B),

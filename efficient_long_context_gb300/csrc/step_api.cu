@@ -61,7 +61,7 @@ orthros_status orthros_plan_step(const int32_t *cache_lens, const int32_t *new_l
                          {"pages_held_out", pages_held_out}, {"free_count_out", free_count_out}};
     if (orthros_status st = check_arrays(all); st != ORTHROS_OK) return st;
     if (kv_lens == cache_lens || kv_lens == cache_lens_out)
-        return report_error(ORTHROS_EINVAL, "kv_lens is a buffer of its own (0 for a sequence that has no place in the step)");
+        return report_error(ORTHROS_EINVAL, "kv_lens is a buffer of its own (-1 for a sequence that has no place in the step)");
     if (!aligned(cache_lens_out, 4)) return report_error(ORTHROS_EINVAL, "cache_lens_out must be 4-byte aligned");
     if (n > 0) {
         const Array rows[] = {{"token_seq", token_seq}, {"token_pos", token_pos}, {"token_slots", token_slots}};

@@ -57,8 +57,8 @@ __device__ __forceinline__ Need need_of(const StepPlanParams &p, int b) {
     const int m = p.new_lens[b];
     s.rows = max(m, 0);
     const long long total = (long long)s.cached + s.rows;
-    s.wrong = s.cached < 0 || m < -1 || s.held < 0 || s.held > p.max_pages || total > (long long)p.max_pages * p.page_size ||
-              (p.parents && m > p.max_tree);
+    s.wrong = m < -1 || s.held < 0 || s.held > p.max_pages ||
+              (m >= 0 && (s.cached < 0 || total > (long long)p.max_pages * p.page_size || (p.parents && m > p.max_tree)));
     s.lack = s.back = 0;
     s.ends = !s.wrong && m < 0;
     if (s.wrong) return s;
@@ -112,7 +112,7 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
             // (held to 32 bits: sums past the tokens or the pool refuse the step below)
             start[b + 1] = (int)min(v[0], 0x7fffffffLL);
             off[b + 1] = (int)min(v[1], 0x7fffffffLL);
-            cached[b] = s.wrong ? -1 : s.cached;
+            cached[b] = s.wrong ? -1 : s.ends ? 0 : s.cached;
             held[b] = s.ends ? -1 : s.held;
             if (b == 0) start[0] = off[0] = 0;
         }
@@ -180,7 +180,7 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
         for (int k = 0; k < kMine; ++k) {
             const int b = tid + k * kThreads;
             if (b >= p.B) break;
-            int kv = 0;
+            int kv = -1;
             if (!none && cached[b] >= 0) {
                 const bool ends = held[b] < 0;
                 kv = len[k] = ends ? 0 : cached[b] + start[b + 1] - start[b];
@@ -199,12 +199,13 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
     const int at0 = rank * kThreads + tid, step = ctas * kThreads;
     auto on_stack = [&](int i) { return __ldcg(p.free_pages + (int)avail - 1 - i); };  // i-th page taken
     uint32_t found = 0;
-    for (int j = at0; j < taken; j += step) {  // (none: taken is 0)
-        const int b = last_at_most(off, p.B, j);
+    for (long long e = at0; e < taken; e += step) {  // (none: taken is 0)
+        const int j = (int)e, b = last_at_most(off, p.B, j);
         p.block_table[(long long)b * p.max_pages + held[b] + j - off[b]] = on_stack(j);
     }
     const int real = none ? 0 : (int)rows;
-    for (int i = at0; i < p.n; i += step) {
+    for (long long e = at0; e < p.n; e += step) {
+        const int i = (int)e;
         int seq = -1, pos = 0, slot = -1;
         uint32_t m[kWords > 0 ? kWords : 1];
 #pragma unroll
@@ -249,7 +250,7 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
 // Commit: token acc[i] of sequence b's tree goes from place L + acc[i] to L + i, in every
 // layer's keys and values. The path ascends (acc[i] >= i), so a thread that owns 16 bytes of
 // the rows may move them in order, kMoves loads in flight before their stores: what a store
-// overwrites has been read. A block takes a sequence in as many layers as let all blocks run at once,
+// overwrites has been read. A block takes a sequence in one layer or a few,
 // its moves laid end to end; blocks past the sequences check all paths and write the status word, as
 // the moving blocks of the first layer write the lengths.
 // ---------------------------------------------------------------------------
@@ -373,7 +374,8 @@ cudaError_t launch_step_plan(const StepPlanParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_tree_commit(TreeCommitParams p, cudaStream_t stream) {
-    // blocks that run at once: eight an SM, by threads
+    // eight blocks an SM (three run at once: a few rounds of them; 48 sequences x 32 layers in 11.6 us, with
+    // three blocks an SM 12.0)
     const int fit = 8 * device_sm_count();
     p.layers_per_block = (int)(((long long)p.layers * p.B + fit - 1) / fit);
     if (p.layers_per_block > p.layers) p.layers_per_block = p.layers;

@@ -703,11 +703,12 @@ ORTHROS_API orthros_status orthros_norm_rotate_append(
  *              parents[i] is the number within its tree (0, 1, ...) of token i's
  *              parent, which comes before it, or -1 under the last cached token.
  *              NULL with max_tree = 0: consecutive tokens
- * q_indptr [B+1], kv_lens [B] (cache + new; 0 once ended), token_seq, token_pos,
- * token_slots [n]: as orthros_norm_rotate_append, orthros_chunk_attention (for
- *              which n has to be the number of tokens) and orthros_tree_attention
- *              take them. Token j of sequence b lies at place cache_lens[b] + j; its
- *              position is that place, or in a tree cache_lens[b] + its depth.
+ * q_indptr [B+1], token_seq, token_pos, token_slots [n], kv_lens [B] (cache + new;
+ *              0 once ended; -1 without a place in the step): as
+ *              orthros_norm_rotate_append, orthros_chunk_attention (for which n has
+ *              to be the number of tokens) and orthros_tree_attention take them.
+ *              Token j of sequence b lies at place cache_lens[b] + j; its position
+ *              is that place, or in a tree cache_lens[b] + its depth.
  * tree_mask    [n, ceil(max_tree / 32)]: bit j of word j/32 of token i's row is
  *              set for token j of its tree if that is i or one of i's ancestors
  * cache_lens_out [B] or NULL, pages_held_out [B], free_count_out [1]: the state
@@ -717,10 +718,10 @@ ORTHROS_API orthros_status orthros_norm_rotate_append(
  * workspace    at least 256 bytes (status word), 256-byte aligned. B <= 8192.
  * A sequence whose lengths cannot be (negative, past the block table, a tree
  * over max_tree) sets ORTHROS_DEV_BAD_LENGTH, one whose pages are not all there
- * ORTHROS_DEV_NO_PAGES: it changes nothing of its state, kv_lens[b] = 0, and its
- * token rows are padding, so that the attention makes them NaN. More tokens than
+ * ORTHROS_DEV_NO_PAGES: it has no place in the step. Nothing of its state changes,
+ * and its token rows are padding, which the attention makes NaN. More tokens than
  * rows, or a stack that cannot hold the pages, set ORTHROS_DEV_BAD_LENGTH and
- * refuse the step: no state changes, q_indptr is all -1. A page id outside
+ * refuse the step: no state changes, q_indptr and kv_lens are all -1. A page id outside
  * [0, num_pages) sets ORTHROS_DEV_BAD_PAGE (slot -1), a parent that does not come
  * before its token ORTHROS_DEV_BAD_POSITION (counted as -1).
  */

@@ -98,6 +98,10 @@ def test_binding_refusals(lib):
             ola.orthros_norm_rotate(x, pos, st, **bad)
     with pytest.raises(ola.OrthrosError):
         ola.orthros_norm_rotate(x, pos, st)  # not on the GPU
+    k = torch.zeros(2, 16, 4, 64)
+    for eps in (1e-50, -1.0, float("nan")):  # 0 in 32 bits is not "no norm"
+        with pytest.raises(ola.OrthrosError):
+            ola.orthros_norm_rotate_append(None, x, x, k, k, pos, pos, st, eps=eps)
 
 
 def test_workspace_size(lib):

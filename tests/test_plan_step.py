@@ -82,7 +82,8 @@ def plain_plan(cl, nl, held, free, count, bt, page, n, parents, max_tree):
     wrong = []
     for b in range(B):
         total = cl[b] + max(nl[b], 0)
-        w = cl[b] < 0 or nl[b] < -1 or not 0 <= held[b] <= mp or total > mp * page or (max_tree > 0 and nl[b] > max_tree)
+        w = nl[b] < -1 or not 0 <= held[b] <= mp or \
+            (nl[b] >= 0 and (cl[b] < 0 or total > mp * page or (max_tree > 0 and nl[b] > max_tree)))
         wrong.append(w)
         bits |= LENGTH if w else 0
         rows.append(at)
@@ -90,7 +91,7 @@ def plain_plan(cl, nl, held, free, count, bt, page, n, parents, max_tree):
     back = sum(held[b] for b in range(B) if not wrong[b] and nl[b] == -1)
     out = dict(token_seq=[-1] * n, token_pos=[0] * n, token_slots=[-1] * n, tree_mask=[[0] * words for _ in range(n)])
     if at > n or count < 0 or count + back > pool:
-        return dict(out, q_indptr=[-1] * (B + 1), kv_lens=[0] * B, cache_lens=cl, pages_held=held, free_count=count, block_table=bt,
+        return dict(out, q_indptr=[-1] * (B + 1), kv_lens=[-1] * B, cache_lens=cl, pages_held=held, free_count=count, block_table=bt,
                     free_pages=None, bits=bits | LENGTH)
     stack = free[:count]
     for b in range(B):
@@ -98,14 +99,14 @@ def plain_plan(cl, nl, held, free, count, bt, page, n, parents, max_tree):
             stack += bt[b][:held[b]]
     free[:len(stack)] = stack
     avail, taken = len(stack), 0
-    kv, new_held = [0] * B, list(held)
+    kv, new_held = [-1] * B, list(held)
     lens = list(cl)
     short = 0  # pages that sequences without enough of them would have taken
     for b in range(B):
         if wrong[b]:
             continue
         if nl[b] == -1:
-            new_held[b] = lens[b] = 0
+            new_held[b] = lens[b] = kv[b] = 0
             continue
         need = max(held[b], (cl[b] + nl[b] + page - 1) // page)
         lack = need - held[b]
@@ -267,6 +268,38 @@ def test_plan_reports_what_cannot_be():
     case[5][0][0], case[3][case[4] - 1] = 10 ** 6, -5
     case[0][0], case[2][0] = max(case[0][0], 1), max(case[2][0], 1)
     assert check(case)["bits"] in (0, PAGE)
+
+
+@pytest.mark.gpu
+def test_plan_of_an_ended_sequence_reads_no_length():
+    case = make(5, 4, 60, 8, seed=9)
+    case[1][2], case[0][2] = -1, 2 ** 31 - 1
+    case[1][4], case[0][4] = -1, -77
+    case[7] = sum(max(m, 0) for m in case[1])
+    for in_place in (False, True):
+        got = check(case, in_place=in_place)
+        assert got["bits"] == 0 and got["kv_lens"][2] == 0 == got["pages_held"][4]
+
+
+@pytest.mark.gpu
+def test_commit_after_a_refused_plan_keeps_the_lengths():
+    """A refused step, and a sequence without a place in one (also one without tokens), leave cache_lens to the
+    commit as they were."""
+    for change, keep in ((lambda c: c.__setitem__(7, c[7] - 1), range(5)), (lambda c: c[2].__setitem__(1, -3), [1]),
+                         (lambda c: c[0].__setitem__(3, 10 ** 6), [3])):
+        case = make(5, 6, 40, 8, seed=10, tree=6)
+        case[1] = [3, 0, 4, 0, 2]
+        case[7], case[8] = 9, [-1, 0, 1, -1, 0, 0, 2, -1, -1]
+        change(case)
+        case[8] = case[8][:case[7]]
+        got = run(case)
+        lens = i32(case[0])
+        kc = torch.zeros(len(case[3]), 8, 1, 64, device="cuda")
+        bt = [[max(x, 0) for x in row] for row in got["block_table"]]
+        ola.orthros_tree_commit(kc, kc.clone(), i32(bt), i32(got["q_indptr"]), i32(got["kv_lens"]), i32([[0]] * 5),
+                                i32([1, 0, 1, 0, 1]), out=lens)
+        want = [L + n if b not in keep else L for b, (L, n) in enumerate(zip(case[0], [1, 0, 1, 0, 1]))]
+        assert lens.tolist() == want
 
 
 @pytest.mark.gpu

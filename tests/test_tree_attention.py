@@ -203,6 +203,22 @@ def test_many_sequences(B):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(12))
+def test_mixed_batches(seed):
+    """Units of one and of two row tiles side by side, whose key tiles count differently in the CTAs' shares:
+    many borders in many places, every one a whole tile."""
+    r = random.Random(seed)
+    B, g, Hkv = r.randint(2, 32), r.choice([1, 4, 8, 16]), r.choice([1, 2, 3, 8])
+    tt = 128 // g
+    new = [r.choice([1, tt, min(tt + 1, 256), r.randint(1, min(2 * tt, 256)), r.randint(0, 256)]) for _ in range(B)]
+    total = [n + r.choice([0, r.randint(0, 200), r.randint(0, 3000)]) for n in new]
+    window = r.choice([1 << 20, r.randint(1, 2000)])
+    w = make(new, total, g * Hkv, Hkv, 64, r.choice([8, 16, 64]), window, seed=seed)
+    masks = tree_masks(new, seed=seed, kind=r.choice(["tree", "any"]))
+    check_tree(call(w, words_of(masks, 8)), plain(w, masks, 0.125), f"{new} {total}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("new,total,Hq,Hkv", [([9], [9], 4, 1), ([70], [5000], 8, 1), ([70] * 40, [80] * 40, 4, 2)])
 def test_rows_without_a_key(new, total, Hq, Hkv):
     """No bit and no cached key in the window: zeros and -inf. A window of 1 leaves an empty row the key
