@@ -57,6 +57,8 @@
 // read into a result: their copy boxes are skipped (zero fill), their logits
 // replaced by -inf and, where a page reaches past them, their value rows
 // cleared in shared memory, so whatever a stale page holds does not matter.
+#include <climits>
+
 #include "ptx.cuh"
 
 namespace orthros {
@@ -438,18 +440,19 @@ __device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
     return lo;
 }
 
-// First token row (of the pool) of box `lane` of key tile kt, for keys [lo, hi] that exist, or past the
-// pool: the copy then fills zeros. bad: a page id outside the pool.
-__device__ __forceinline__ int box_row(const ChunkParams &p, const int32_t *bt, int kt, int lo, int hi, int lane, int &bad) {
+// Box `lane` of key tile kt, for keys [lo, hi] that exist: the page that it lies in, as the block table
+// has it, or kNoPage when nothing of it exists.
+constexpr int kNoPage = INT_MIN;
+__device__ __forceinline__ int box_page(const ChunkParams &p, const int32_t *bt, int kt, int lo, int hi, int lane) {
     const int key = kt * kKeys + lane * p.box;
-    bad = 0;
-    if (lane * p.box >= kKeys || key > hi || key + p.box - 1 < lo) return p.num_pages * p.page_size;
-    const int pg = bt[key / p.page_size];
-    if (pg < 0 || pg >= p.num_pages) {
-        bad = 1;
-        return p.num_pages * p.page_size;
-    }
-    return pg * p.page_size + key % p.page_size;
+    if (lane * p.box >= kKeys || key > hi || key + p.box - 1 < lo) return kNoPage;
+    return bt[key / p.page_size];
+}
+// Its first token row of the pool, or past the pool: the copy then fills zeros. bad: a page id outside the pool.
+__device__ __forceinline__ int box_row(const ChunkParams &p, int pg, int kt, int lane, int &bad) {
+    bad = pg != kNoPage && (pg < 0 || pg >= p.num_pages);
+    if (pg == kNoPage || bad) return p.num_pages * p.page_size;
+    return pg * p.page_size + (kt * kKeys + lane * p.box) % p.page_size;
 }
 
 // Whether key tile `it` of a segment has rows that none of its unit's tokens sees:
@@ -700,18 +703,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int key_lo = max(0, un.pos0 - p.window + 1);
                     const int box = p.box;
                     const int n_box = box ? kKeys / box : 0;
-                    // (The page is awaited here, a tile before its use: awaited at its use, decoding took 1 %
-                    // longer, its copies less in step with those of the other heads.)
-                    auto look = [&](int kt, int &bad) -> int {
-                        bad = 0;
-                        return box ? box_row(p, bt, kt, key_lo, key_hi, lane, bad) : 0;
-                    };
-                    int bad_next = 0, tok_next = look(sg.kt0, bad_next);
+                    // pages are looked up two tiles before their use, so that no copy waits for them
+                    auto look = [&](int it) { return box && it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : kNoPage; };
+                    int page0 = look(0), page1 = look(1);
                     for (int it = 0; it < sg.nkt; ++it) {
                         const uint32_t gi = gk;
                         const int sk = gi % kNumK, sv = gi % kNumV;
-                        const int tok = tok_next, bad = bad_next;
-                        if (it + 1 < sg.nkt) tok_next = look(sg.kt0 + it + 1, bad_next);
+                        int bad;
+                        const int tok = box_row(p, page0, sg.kt0 + it, lane, bad);
+                        page0 = page1;
+                        page1 = look(it + 2);
                         if (gi >= (uint32_t)kNumK &&
                             !mbar_wait_warp(&mt.k_empty[sk], ((gi / kNumK) - 1) & 1, abort, status)) {
                             alive = false;
@@ -976,11 +977,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int key_hi = sg.pos0 + sg.cnt - 1;
             if constexpr (kTree) key_hi = ts.key_end - 1;
             const int key_lo = max(0, sg.pos0 - p.window + 1);
-            int bad, tok_next = box_row(p, bt, sg.kt0, key_lo, key_hi, lane, bad);
+            auto look = [&](int it) { return it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : kNoPage; };
+            int page0 = look(0), page1 = look(1);
             for (int it = 0; it < sg.nkt; ++it) {
                 const int sv = gv % kNumV;
-                const int tok = tok_next;
-                if (it + 1 < sg.nkt) tok_next = box_row(p, bt, sg.kt0 + it + 1, key_lo, key_hi, lane, bad);
+                int bad;  // (reported with the keys)
+                const int tok = box_row(p, page0, sg.kt0 + it, lane, bad);
+                page0 = page1;
+                page1 = look(it + 2);
                 if (gv >= (uint32_t)kNumV && !(ok = mbar_wait_warp(&mt.v_empty[sv], ((gv / kNumV) - 1) & 1, abort, status))) break;
                 int r0, r1;
                 const bool edge = unseen_rows<kTree>(sg, ts, p.window, it, r0, r1);
