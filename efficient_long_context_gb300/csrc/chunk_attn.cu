@@ -36,9 +36,9 @@
 // beside the products of the other.
 //
 // Roles (384 threads, one persistent CTA per SM): warps 0-7 softmax (slot w >> 2,
-// one thread per row), warp 8 copies (page lookups by its lanes, TMA boxes of
-// up to 128 tokens within a page), warp 9 issues tcgen05.mma, warp 10 clears value
-// rows that no row of the unit sees. S = Q K^T (bf16,
+// one thread per row), warp 8 lists the units and copies queries and keys (page lookups
+// by its lanes, TMA boxes of up to 128 tokens within a page), warp 11 copies values,
+// warp 9 issues tcgen05.mma, warp 10 clears value rows that no row of the unit sees. S = Q K^T (bf16,
 // M = 128, N = 128) goes to TMEM, P returns there as bf16 over S, O += P V. TMEM:
 // S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [384,384+d).
 //
@@ -48,10 +48,14 @@
 // (relative, measured with independent values), beside 0.0017 of o's own rounding.
 //
 // Bound and measured (GQA 32/8, d = 128): decoding by HBM, 32 sequences over 16K-32K
-// keys in 480 us, 6.6 TB/s, 97 % of the measured copy rate; chunks by the softmax that
-// has to run beside the products, 2 x 4000 tokens over 24K keys at 1484 TFLOP/s (76 %
-// of the measured bf16 rate; 1375 once the power limit lowers the clock), 2048
-// tokens at window 4096 in 110 us, 5 of them the merge.
+// keys in 440 us, 7.2 TB/s, above the rate of a copy, which also writes (one warp for
+// keys and values: 480 us; pages of 16 tokens, whose boxes take twice as long to issue as
+// those of 64: 451 instead of 518); chunks by the softmax that has to run beside the products,
+// 2 x 4000 tokens over 24K keys at 1530-1600 TFLOP/s in bursts (80 % of the measured
+// bf16 rate; 1375-1480 once the power limit lowers the clock), 2048 tokens at window 4096 in
+// 111 us, 5 of them the merge. Trees: 32 of 9 to 60 tokens over 4K-20K keys in pages of
+// 16 in 274 us (floor 246: HBM, with the softmax of two row tiles close behind), one of
+// 25 tokens over 32K keys in 37 us (floor 20: 7 us of start, 9 of end).
 //
 // Keys outside the sequence's length or before every row's window are never
 // read into a result: their copy boxes are skipped (zero fill), their logits

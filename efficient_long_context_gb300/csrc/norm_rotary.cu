@@ -11,7 +11,7 @@
 // half to the rotation's, so everything runs on pairs of channels (packed fp32
 // instructions), and the layout of the pairs is fixed at compile time: with one kernel for
 // both layouts the batch's loads and the affine did not fit the registers beside it
-// (108 to 130 us instead of the figures at the kernels).
+// (32768 x 32 x 128 bf16: 98 to 130 us instead of 89).
 #include "ptx.cuh"
 #include "rotary.cuh"
 
@@ -149,7 +149,9 @@ template <int kLanes> __device__ __forceinline__ float row_sum(float x) {
 // Forward and append: rotary.cu's moving kernel (its threads, tables, runs of tokens and
 // virtual heads) with the norm on the way. One kernel is both, a forward an append without
 // keys, output rows and status word: compiled for it alone, the compiler works on a
-// batch's tokens side by side and spills (160 bytes a thread).
+// batch's tokens side by side and spills (160 bytes a thread). Bound by HBM: 32768 x 32 x 128
+// bf16 with weight and affine 89 us, 6.1 TB/s (91 % of the measured copy rate; the rotation alone
+// 86); 8000 tokens of GQA 32/8 appended in 35 us (5.3 TB/s: start and end of a 28 us kernel).
 // ---------------------------------------------------------------------------
 constexpr int kTokens = 4;  // of a thread's batch of loads
 
@@ -291,7 +293,10 @@ __global__ void __launch_bounds__(kMoveThreads) norm_move_kernel(const RotatePar
 // ---------------------------------------------------------------------------
 // Backward: rotary.cu's gradient kernel (rows through shared memory, kDepth tokens ahead of
 // the thread that takes them, partials of a block added in a fixed order) with both sums of
-// a row, of x^2 and of a g x, taken in one exchange.
+// a row, of x^2 and of a g x, taken in one exchange. The weight's gradient is the block's sums per
+// head, weighed by alpha, added over its heads. Bound by HBM: 32768 x 32 x 128 bf16 with all
+// gradients 132 us, 6.1 TB/s (91 %), and 6 us of sum (with alpha read in the loop over the heads
+// that summed the weight's gradient the kernel took 8 us longer).
 // ---------------------------------------------------------------------------
 constexpr int kDepth = 6;
 

@@ -15,7 +15,9 @@
 // between the last read of the inputs and the first write of the outputs, so that
 // a length, a page count or the height of the stack may be updated in place. Bound by
 // the latency of that chain (load, scan, barrier, table look-up, store), not by
-// bytes: a step's arrays are a few hundred KB.
+// bytes: a step's arrays are a few hundred KB. 64 decoding sequences: 4.5 us; 500
+// trees of up to 64 tokens, 18000 rows, 31 ended sequences: 10.4 us (16.7 with one CTA's threads
+// returning a sequence's pages each and the lengths read again for every pass).
 #include "internal.cuh"
 
 namespace orthros {
