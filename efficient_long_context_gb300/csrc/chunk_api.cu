@@ -52,7 +52,7 @@ orthros_status check_shape(int B, int n, int max_new, int Hq, int Hkv, int d, in
         return report_error(ORTHROS_EINVAL, "Hq = %d must be a positive multiple of Hkv = %d", Hq, Hkv);
     if (max_pages < 1 || page_size < 1) return report_error(ORTHROS_EINVAL, "max_pages and page_size must be >= 1");
     if (dtype != ORTHROS_BF16 && dtype != ORTHROS_F32) return report_error(ORTHROS_EINVAL, "unknown dtype %d", (int)dtype);
-    if (dtype != ORTHROS_BF16) return report_error(ORTHROS_EUNSUPPORTED, "the chunk attention takes bf16 only");
+    if (dtype != ORTHROS_BF16) return report_error(ORTHROS_EUNSUPPORTED, "the attention of new tokens over the cache takes bf16 only");
     if (d != 64 && d != 128) return report_error(ORTHROS_EUNSUPPORTED, "head size d = %d (supported: 64, 128)", d);
     if (Hq / Hkv > 128) return report_error(ORTHROS_EUNSUPPORTED, "%d query heads per kv head (at most 128)", Hq / Hkv);
     if (Hkv > 65536) return report_error(ORTHROS_EUNSUPPORTED, "Hkv = %d exceeds 65536", Hkv);

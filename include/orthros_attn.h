@@ -692,9 +692,10 @@ ORTHROS_API orthros_status orthros_norm_rotate_append(
  * cache_lens, new_lens, pages_held [B] int32; new_lens[b] = -1: the sequence has
  *              ended, all its pages go back (cache_lens is then not read further)
  * free_pages   [num_pages], free_count [1]: the first free_count entries are the
- *              free pages, a stack. Ended sequences push theirs, in order, first;
- *              then the growing sequences, in order, take from the top. Updated
- *              in place up to the new height; entries above it are left.
+ *              free pages, a stack, updated in place. Ended sequences push theirs,
+ *              in order, first; then the growing sequences, in order, take from the
+ *              top. (A later one does not get what an earlier one found too little
+ *              of.) Entries from the new height on mean nothing.
  * block_table  [B, max_pages]: entries of new pages are written, others left
  * n            rows of the token arrays; rows behind the last new token are
  *              padding: token_seq -1, token_pos 0, token_slots -1, no mask bits

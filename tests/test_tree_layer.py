@@ -273,3 +273,51 @@ def test_refusals():
         layer.tree_step(x[:1], p, srv.kc, srv.vc, srv.bt, 1)
     with pytest.raises(ValueError):
         RotaryLayer(layer.w_qkv, layer.affines, layer.freq, 4, 2, 64, 30, q_norm=layer.q_norm)
+
+
+@pytest.mark.gpu
+def test_two_batches_at_once():
+    """Cycles of two batches on two streams, with workspaces of their own, give the bits of one after the other."""
+    B, page, n, max_tree, most = 6, 16, 90, 20, 4
+    layer, g = make_layer(8, 2, 128, 60, "interleaved", seed=7, normed=True)
+    r = random.Random(5)
+    rounds = []
+    for _ in range(8):
+        sizes = [r.randint(1, max_tree - 5) for _ in range(B)]
+        trees = [draft(r, m) for m in sizes]
+        flat = [q for t in trees for q in t]
+        paths = [path_to(t, r.randrange(len(t)))[:most] for t in trees]
+        rounds.append((i32(sizes), i32(flat + [0] * (n - len(flat))), i32([q + [0] * (most - len(q)) for q in paths]),
+                       i32([len(q) for q in paths]), torch.randn(2 * n, D_MODEL, generator=g).bfloat16().cuda(), sum(sizes)))
+    prompts = [[torch.randn(m, D_MODEL, generator=g).bfloat16().cuda() for m in ms] for ms in ((9, 200, 33, 1, 64, 300), (5, 1, 500, 2, 16, 17))]
+
+    def start():
+        out = []
+        for p in prompts:
+            out.append(Server(layer, B, page, 200))
+            out[-1].chunk(p)
+        torch.cuda.synchronize()
+        return out
+
+    def cycle(srv, rnd, cws):
+        new, parents, acc, cnt, x, m = rnd
+        p = srv.plan(new, n, parents, max_tree)
+        o = layer.tree_step(x, p, srv.kc, srv.vc, srv.bt, max_tree)
+        ola.orthros_tree_commit(srv.kc, srv.vc, srv.bt, p.q_indptr, p.kv_lens, acc, cnt, out=srv.lens, workspace=cws)
+        return [t[:m].clone() for t in o]
+
+    cws = [torch.empty(256, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = []
+    for i, srv in enumerate(start()):
+        want.append([cycle(srv, rounds[(k + 3 * i) % 8], cws[i]) for k in range(8)])
+    servers = start()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for k in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(cycle(servers[i], rounds[(k + 3 * i) % 8], cws[i]))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for s, t in zip(a, b) for x, y in zip(s, t))
+    assert all(ola.orthros_check(w) == (0, 0) for w in (*cws, *(s.ws for s in servers)))
