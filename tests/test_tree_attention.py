@@ -49,6 +49,80 @@ def test_workspace_size(lib):
 
 
 # ---------------------------------------------------------------------------
+# the CTAs' shares of weighed key tiles, replayed on the CPU with the kernel's constants
+# ---------------------------------------------------------------------------
+def share_out(units, heads, per_lane, single, pair, min_tiles, snap_tiles):
+    """units: (key tiles, two row tiles?) of one kv head. Checks that the shares of a lane of `heads` kv
+    heads cover every tile once and in whole tiles, that none is empty, and that a unit's parts are those its
+    first CTA counts; returns the largest share's cost beside an equal one's."""
+    cost = [pair if two else single for _, two in units]
+    start = np.concatenate([[0], np.cumsum([n * w for (n, _), w in zip(units, cost)])]).tolist()
+    tiles = start[-1]
+    total = heads * tiles
+    eff = max(1, min(per_lane, total // (min_tiles * single)))
+    snap = 0
+    while snap < snap_tiles * single and 4 * (snap + 1) * eff <= total:
+        snap += 1
+
+    def moved(x, u0, n, w):
+        return u0 if x - u0 <= snap else u0 + n if u0 + n - x <= snap else u0 + (x - u0) // w * w
+
+    def unit_of(x):
+        h = x // tiles
+        return h, max(i for i in range(len(units)) if units[i][0] > 0 and start[i] <= x - h * tiles)
+
+    def end(x):
+        if x >= total:
+            return total
+        h, u = unit_of(x)
+        return moved(x, h * tiles + start[u], units[u][0] * cost[u], cost[u])
+
+    borders = [end(total * j // eff) for j in range(eff + 1)]
+    seen, parts, counted = set(), {}, {}
+    for j in range(eff):
+        x, x1 = borders[j], borders[j + 1]
+        assert x < x1, "an empty share"
+        cut = 0
+        while x < x1:
+            h, u = unit_of(x)
+            u0, n, w = h * tiles + start[u], units[u][0], cost[u]
+            a = (x - u0) // w
+            assert (x - u0) % w == 0
+            m = min(n - a, min(x1 - x, n * w) // w)
+            assert m > 0
+            new = {(h, u, t) for t in range(a, a + m)}
+            assert not new & seen
+            seen |= new
+            if a > 0 or a + m < n:
+                cut += 1
+                parts.setdefault((h, u), []).append(j)
+                if a == 0:
+                    inside = [k for k in range(j + 1, eff) if moved(total * k // eff, u0, n * w, w) < u0 + n * w]
+                    counted[(h, u)] = list(range(j, j + 1)) + [k for i, k in enumerate(inside) if k == j + 1 + i]
+            x += m * w
+        assert cut <= 2
+    assert len(seen) == heads * sum(n for n, _ in units)
+    assert parts == counted
+    return max(b - a for a, b in zip(borders, borders[1:])), total / eff
+
+
+def test_shares_of_weighed_tiles():
+    import pathlib
+    import re
+
+    text = (pathlib.Path(ola.__file__).parent / "csrc" / "chunk_attn.cu").read_text()
+    single, pair, min_tiles, snap = (int(re.search(rf"{k} = (\d+)", text).group(1)) for k in
+                                     ("kSingleCost", "kPairCost", "kMinTiles", "kSnap"))
+    r = random.Random(1)
+    for _ in range(400):
+        units = [(r.choice([0, 1, 2, r.randint(1, 5), r.randint(1, 60)]), r.random() < 0.5) for _ in range(r.randint(1, 32))]
+        if any(n for n, _ in units):
+            most, even = share_out(units, r.choice([1, 1, 2, 3, 7]), r.choice([1, 2, 3, 9, 19, 38, 76, 152]), single, pair,
+                                   min_tiles, snap)
+            assert most <= 1.5 * even + pair + 1
+
+
+# ---------------------------------------------------------------------------
 # GPU parity
 # ---------------------------------------------------------------------------
 def tree_masks(new, seed, kind="tree"):
