@@ -15,7 +15,8 @@
 // Trees (kTree). The new tokens of a sequence may be a drafted tree: token i then sees the cached
 // keys before the tree, in the window of its position, and the tokens of the tree that its mask
 // row names. Every unit of the sequence has the same keys; only tiles that reach the tree (or the
-// window's edge) take a mask, 32 keys a word, put together while the products run. The mask may leave a row without a key.
+// window's edge) take a mask, 32 keys a word, put together while the products run. A row may be
+// left without a key.
 //
 // Units and the split of the key axis. A unit is up to two row tiles of one
 // sequence and the key tiles (128 tokens) they see. The plan kernel lists the
