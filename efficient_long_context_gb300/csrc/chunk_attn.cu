@@ -62,8 +62,6 @@
 // read into a result: their copy boxes are skipped (zero fill), their logits
 // replaced by -inf and, where a page reaches past them, their value rows
 // cleared in shared memory, so whatever a stale page holds does not matter.
-#include <climits>
-
 #include "ptx.cuh"
 
 namespace orthros {
@@ -445,18 +443,21 @@ __device__ int find_unit(const ChunkUnit *units, int n, long long x, int lane) {
     return lo;
 }
 
-// Box `lane` of key tile kt, for keys [lo, hi] that exist: the page that it lies in, as the block table
-// has it, or kNoPage when nothing of it exists.
-constexpr int kNoPage = INT_MIN;
-__device__ __forceinline__ int box_page(const ChunkParams &p, const int32_t *bt, int kt, int lo, int hi, int lane) {
+// Whether nothing of box `lane` of key tile kt exists, for keys [lo, hi] that do.
+__device__ __forceinline__ bool box_outside(const ChunkParams &p, int kt, int lo, int hi, int lane) {
     const int key = kt * kKeys + lane * p.box;
-    if (lane * p.box >= kKeys || key > hi || key + p.box - 1 < lo) return kNoPage;
-    return bt[key / p.page_size];
+    return lane * p.box >= kKeys || key > hi || key + p.box - 1 < lo;
+}
+// The page that the box lies in, as the block table has it: any 32 bits. (Not looked up for a box outside,
+// which is told again where the page is used: no id of the table can stand for it.)
+__device__ __forceinline__ int box_page(const ChunkParams &p, const int32_t *bt, int kt, int lo, int hi, int lane) {
+    return box_outside(p, kt, lo, hi, lane) ? 0 : bt[(kt * kKeys + lane * p.box) / p.page_size];
 }
 // Its first token row of the pool, or past the pool: the copy then fills zeros. bad: a page id outside the pool.
-__device__ __forceinline__ int box_row(const ChunkParams &p, int pg, int kt, int lane, int &bad) {
-    bad = pg != kNoPage && (pg < 0 || pg >= p.num_pages);
-    if (pg == kNoPage || bad) return p.num_pages * p.page_size;
+__device__ __forceinline__ int box_row(const ChunkParams &p, int pg, int kt, int lo, int hi, int lane, int &bad) {
+    const bool outside = box_outside(p, kt, lo, hi, lane);
+    bad = !outside && (pg < 0 || pg >= p.num_pages);
+    if (outside || bad) return p.num_pages * p.page_size;
     return pg * p.page_size + (kt * kKeys + lane * p.box) % p.page_size;
 }
 
@@ -709,13 +710,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int box = p.box;
                     const int n_box = box ? kKeys / box : 0;
                     // pages are looked up two tiles before their use, so that no copy waits for them
-                    auto look = [&](int it) { return box && it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : kNoPage; };
+                    auto look = [&](int it) { return box && it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : 0; };
                     int page0 = look(0), page1 = look(1);
                     for (int it = 0; it < sg.nkt; ++it) {
                         const uint32_t gi = gk;
                         const int sk = gi % kNumK, sv = gi % kNumV;
                         int bad;
-                        const int tok = box_row(p, page0, sg.kt0 + it, lane, bad);
+                        const int tok = box_row(p, page0, sg.kt0 + it, key_lo, key_hi, lane, bad);
                         page0 = page1;
                         page1 = look(it + 2);
                         if (gi >= (uint32_t)kNumK &&
@@ -982,12 +983,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int key_hi = sg.pos0 + sg.cnt - 1;
             if constexpr (kTree) key_hi = ts.key_end - 1;
             const int key_lo = max(0, sg.pos0 - p.window + 1);
-            auto look = [&](int it) { return it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : kNoPage; };
+            auto look = [&](int it) { return it < sg.nkt ? box_page(p, bt, sg.kt0 + it, key_lo, key_hi, lane) : 0; };
             int page0 = look(0), page1 = look(1);
             for (int it = 0; it < sg.nkt; ++it) {
                 const int sv = gv % kNumV;
                 int bad;  // (reported with the keys)
-                const int tok = box_row(p, page0, sg.kt0 + it, lane, bad);
+                const int tok = box_row(p, page0, sg.kt0 + it, key_lo, key_hi, lane, bad);
                 page0 = page1;
                 page1 = look(it + 2);
                 if (gv >= (uint32_t)kNumV && !(ok = mbar_wait_warp(&mt.v_empty[sv], ((gv / kNumV) - 1) & 1, abort, status))) break;

@@ -533,3 +533,22 @@ def test_window_and_bound_past_32_bits():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(ola.OrthrosError):
         call(dict(w, window=-2 ** 32 + 5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [8, 16, 64, 128, 12])  # the last one without a copy box
+@pytest.mark.parametrize("m", [70, 40])  # with and without a plan kernel
+def test_every_page_id_outside_the_pool_is_reported(m, page):
+    """No id of a block table is taken for anything but a page: not the least of 32 bits either."""
+    new, total = [2, m, 1], [300, 400, 90]
+    w = make(new, total, 8, 2, 64, page, 1 << 20, seed=19)
+    ref, pool = plain(w, 0.125), w["kc"].shape[0]
+    ws = torch.empty(ola.orthros_chunk_attention_workspace_size(3, 3 + m, m, 8, 2, 64, w["bt"].shape[1], page), dtype=torch.uint8,
+                     device="cuda")
+    for pid in (-2 ** 31, -2 ** 31 + 1, -2, -1, pool, 2 ** 31 - 1):
+        bt = w["bt"].clone()
+        bt[0, 130 // page] = pid
+        o, lse = call(dict(w, bt=bt), workspace=ws, max_new=m)
+        assert ola.orthros_check(ws) == (5, 2), pid
+        assert bool(torch.isnan(o[:2]).all()) and bool(torch.isnan(lse[:2]).all()), pid
+        check((o[2:], lse[2:]), [r[2:] for r in ref], f"page id {pid}")

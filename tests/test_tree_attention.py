@@ -455,3 +455,22 @@ def test_long_cache():
                                    torch.tensor([[5]], dtype=torch.int32, device="cuda"),
                                    torch.tensor([1], dtype=torch.int32, device="cuda"))
     assert lens.tolist() == [471] and torch.equal(kc.flatten(0, 1)[far[7] * page + 470 % page], want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [8, 16, 64, 128, 12])  # the last one without a copy box
+@pytest.mark.parametrize("B", [2, 40])  # without and with a plan kernel
+def test_every_page_id_outside_the_pool_is_reported(B, page):
+    new, total = [9, 20] + [1] * (B - 2), [300, 150] + [10] * (B - 2)
+    w = make(new, total, 8, 2, 128, page, 1 << 20, seed=20)
+    masks = tree_masks(new, 20)
+    mask, ref, pool = words_of(masks, 1), plain(w, masks, 128 ** -0.5), w["kc"].shape[0]
+    ws = torch.empty(ola.orthros_tree_attention_workspace_size(B, sum(new), 20, 8, 2, 128, w["bt"].shape[1], page), dtype=torch.uint8,
+                     device="cuda")
+    for pid in (-2 ** 31, -2 ** 31 + 1, -2, -1, pool, 2 ** 31 - 1):
+        bt = w["bt"].clone()
+        bt[0, 140 // page] = pid
+        o, lse = call(dict(w, bt=bt), mask, max_new=20, workspace=ws)
+        assert ola.orthros_check(ws) == (5, 2), pid
+        assert bool(torch.isnan(o[:9]).all()) and bool(torch.isnan(lse[:9]).all()), pid
+        check_tree((o[9:], lse[9:]), [r[9:] for r in ref], f"page id {pid}")
