@@ -1139,7 +1139,8 @@ def orthros_tree_commit(k_cache, v_cache, block_table, q_indptr, kv_lens, accept
     k_cache, v_cache [num_pages, page_size, Hkv, d], or [layers, ...] of all layers at once, updated in
     place; accepted [B, most] int32, ascending tokens of each sequence's tree, of which the first
     n_accepted [B] count. Returns the cached tokens after it [B]; `out`, a buffer other than kv_lens, may be
-    the one that the plan took as cache_lens: sequences that had no place in the step keep theirs.
+    the one that the plan took as cache_lens: sequences that had no place in the step keep theirs. Without
+    `out` theirs are not known and are -1 (a length that the next plan refuses; 0 is an ended sequence's).
     """
     if stream is not None:
         with _on(stream):
@@ -1157,7 +1158,7 @@ def orthros_tree_commit(k_cache, v_cache, block_table, q_indptr, kv_lens, accept
         raise OrthrosError(1, "accepted must be [B, most]")
     most = accepted.shape[1]
     if out is None:
-        out = torch.zeros(B, dtype=torch.int32, device=k_cache.device)
+        out = torch.full((B,), -1, dtype=torch.int32, device=k_cache.device)
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=k_cache.device)
     rc = lib.orthros_tree_commit(

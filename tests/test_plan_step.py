@@ -467,3 +467,32 @@ def test_commit_in_a_graph_and_on_a_stream():
     lens = ola.orthros_tree_commit(k2, v2, *args, stream=side)
     side.synchronize()
     assert torch.equal(k2, k) and torch.equal(v2, v) and torch.equal(lens, out)
+
+
+@pytest.mark.gpu
+def test_commit_without_out_knows_no_length_of_a_sequence_without_a_place():
+    """The lengths that the call allocates are -1 where the step had no place for the sequence: 0 would be the
+    length of an ended one. A plan that is given them refuses those sequences and leaves their pages alone."""
+    page, parents = 8, [-1, 0, 0, -1, 0, -1, 0, -1]
+    bt = [[0, 1] + [-1] * 4, [2, 3] + [-1] * 4, [4] + [-1] * 5, [5, 6] + [-1] * 4]
+    for third, lost in ((-1, []), (0, [1])):  # the second sequence needs a page: the third one's, if that ends
+        case = [[9, 16, 5, 8], [3, 4, third, 1], [2, 2, 1, 2], [-1] * 8, 0, bt, page, 8, parents, 6]
+        got = check(case)
+        assert [b for b, kv in enumerate(got["kv_lens"]) if kv < 0] == lost
+        kc = torch.zeros(8, 8, 1, 64, device="cuda")
+        args = (kc, kc.clone(), i32([[max(x, 0) for x in row] for row in got["block_table"]]), i32(got["q_indptr"]), i32(got["kv_lens"]), i32([[0]] * 4))
+        count = [1, 1, 0, 1]
+        lens = ola.orthros_tree_commit(*args, i32(count)).tolist()
+        want = [c + k for c, k in zip(case[0], count)]
+        if not lost:
+            want[2] = 0  # ended
+        for b in lost:
+            want[b] = -1
+        assert lens == want
+    # carried on: the sequence stays out of the step, its pages and table untouched
+    nxt = [lens, [1, 1, 1, 1], got["pages_held"], [7] + [-1] * 7, 1, got["block_table"], 8, 4, [-1] * 4, 6]
+    got = check(nxt)
+    assert got["bits"] == LENGTH and got["kv_lens"][1] == -1 and got["block_table"][1] == bt[1]
+    # a refused step: of every sequence
+    refused = i32([-1] * 5)
+    assert ola.orthros_tree_commit(*args[:3], refused, i32([-1] * 4), args[5], i32(count)).tolist() == [-1] * 4
