@@ -6,7 +6,7 @@
 // Plan. With L_b cached and m_b new tokens, sequence b needs ceil((L_b + m_b) / P)
 // pages; what it lacks it takes from the top of the free stack, the sequences in
 // order, so that its share is an exclusive prefix sum of the lacks. Ended
-// sequences (m_b = -1) push theirs before. A token's sequence is found by a binary
+// sequences (m_b = -1) push theirs before, if all their ids are the pool's. A token's sequence is found by a binary
 // search in the prefix sums of m_b, its page in the table or, if it is a new one,
 // on the stack: no thread waits for another's table entry.
 //
@@ -16,8 +16,9 @@
 // a length, a page count or the height of the stack may be updated in place. Bound by
 // the latency of that chain (load, scan, barrier, table look-up, store), not by
 // bytes: a step's arrays are a few hundred KB. 64 decoding sequences: 4.5 us; 500
-// trees of up to 64 tokens, 18000 rows, 31 ended sequences: 10.4 us (16.7 with one CTA's threads
-// returning a sequence's pages each and the lengths read again for every pass).
+// trees of up to 64 tokens, 18000 rows, 31 ended sequences: 11.3 us, 0.9 of them the look at
+// the ended ones' page ids (16.7 without it, but with one CTA's threads returning a sequence's
+// pages each and the lengths read again for every pass).
 #include "internal.cuh"
 
 namespace orthros {
@@ -69,6 +70,21 @@ __device__ __forceinline__ Need need_of(const StepPlanParams &p, int b) {
     return s;
 }
 
+// Whether this lane finds an id from outside the pool among the first n pages of sequence b (each lane looks at its own).
+__device__ __forceinline__ bool foreign_page(const StepPlanParams &p, int b, int n, int lane) {
+    const int32_t *row = p.block_table + (long long)b * p.max_pages;
+    constexpr int kPages = 16;  // of a lane at a time
+    bool foreign = false;
+    for (int i0 = lane; i0 < n; i0 += 32 * kPages) {
+        int id[kPages];
+#pragma unroll
+        for (int u = 0; u < kPages; ++u) id[u] = i0 + 32 * u < n ? row[i0 + 32 * u] : 0;
+#pragma unroll
+        for (int u = 0; u < kPages; ++u) foreign |= id[u] < 0 || id[u] >= p.num_pages;
+    }
+    return foreign;
+}
+
 __device__ __forceinline__ void cluster_arrive_wait() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -99,6 +115,17 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
         Need s{};
         if (b < p.B) s = need_of(p, b);
         if (s.wrong) flags |= ORTHROS_DEV_BAD_LENGTH;
+        // an id from outside the pool on the stack would come to another sequence, steps later: one that has
+        // such an id among its pages keeps them all
+        for (unsigned ends = __ballot_sync(0xffffffffu, s.back > 0); ends; ends &= ends - 1) {
+            const int src = __ffs(ends) - 1;
+            if (__any_sync(0xffffffffu, foreign_page(p, base + warp * 32 + src, __shfl_sync(0xffffffffu, s.back, src), lane)) && lane == src) {
+                s.wrong = true;
+                s.ends = false;
+                s.back = 0;
+                flags |= ORTHROS_DEV_BAD_PAGE;
+            }
+        }
         long long v[3] = {s.rows, s.lack, s.back};
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -203,7 +230,9 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
     uint32_t found = 0;
     for (long long e = at0; e < taken; e += step) {  // (none: taken is 0)
         const int j = (int)e, b = last_at_most(off, p.B, j);
-        p.block_table[(long long)b * p.max_pages + held[b] + j - off[b]] = on_stack(j);
+        const int id = on_stack(j);
+        if (id < 0 || id >= p.num_pages) found |= ORTHROS_DEV_BAD_PAGE;
+        p.block_table[(long long)b * p.max_pages + held[b] + j - off[b]] = id;
     }
     const int real = none ? 0 : (int)rows;
     for (long long e = at0; e < p.n; e += step) {

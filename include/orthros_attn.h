@@ -723,8 +723,12 @@ ORTHROS_API orthros_status orthros_norm_rotate_append(
  * and its token rows are padding, which the attention makes NaN. More tokens than
  * rows, or a stack that cannot hold the pages, set ORTHROS_DEV_BAD_LENGTH and
  * refuse the step: no state changes, q_indptr and kv_lens are all -1. A page id outside
- * [0, num_pages) sets ORTHROS_DEV_BAD_PAGE (slot -1), a parent that does not come
- * before its token ORTHROS_DEV_BAD_POSITION (counted as -1).
+ * [0, num_pages) sets ORTHROS_DEV_BAD_PAGE where the step meets it: under a new token
+ * (slot -1), among the pages taken from the stack (the table has it), or among those of
+ * an ended sequence, which then has not ended: nothing of its state changes, its kv_lens
+ * is -1 and none of its pages goes back. (Pages that hold only older tokens are not
+ * looked up here.) A parent that does not come before its token sets
+ * ORTHROS_DEV_BAD_POSITION (counted as -1).
  */
 ORTHROS_API orthros_status orthros_plan_step(
     const int32_t *cache_lens, const int32_t *new_lens, const int32_t *pages_held, const int32_t *free_count,

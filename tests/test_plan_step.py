@@ -496,3 +496,62 @@ def test_commit_without_out_knows_no_length_of_a_sequence_without_a_place():
     # a refused step: of every sequence
     refused = i32([-1] * 5)
     assert ola.orthros_tree_commit(*args[:3], refused, i32([-1] * 4), args[5], i32(count)).tolist() == [-1] * 4
+
+
+def check_bad_page(case, b, **kw):
+    """The plan of a case in which sequence b ends with a page id from outside the pool: it stays as it is, as one
+    whose lengths cannot be, and the others' step is that without it."""
+    as_wrong = [list(x) if isinstance(x, list) else x for x in case]
+    as_wrong[1][b] = -2
+    want, got = plain_plan(*as_wrong), run(case, **kw)
+    want["bits"] = want["bits"] & ~LENGTH | PAGE
+    for k, v in want.items():
+        if v is not None:
+            assert got[k] == v, (k, got[k], v)
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,new,hist,page,kw", [(3, 2, 40, 8, {}), (40, 9, 500, 16, dict(tree=9, ends=0.3, pad=7)),
+                                                (9, 1, 9000, 4, dict(ends=0.5)), (1500, 4, 60, 8, dict(ends=0.2)),
+                                                (600, 12, 90, 8, dict(tree=12, ends=0.1))], ids=lambda v: str(v))
+def test_plan_keeps_ids_of_elsewhere_off_the_stack(B, new, hist, page, kw, in_place):
+    """An ended sequence gives its pages back only if all of them are the pool's."""
+    base = make(B, new, hist, page, seed=B + page, **kw)
+    b = max(range(B), key=lambda s: base[2][s])
+    base[1][b] = -1
+    base[7] = sum(max(m, 0) for m in base[1]) + kw.get("pad", 0)
+    base[8] = [-1] * base[7]
+    held, pool = base[2][b], len(base[3])
+    for at in sorted({0, held // 2, held - 1}):
+        for pid in (-1, -2 ** 31, pool, 2 ** 31 - 1):
+            case = [list(x) if isinstance(x, list) else x for x in base]
+            case[5] = [list(r) for r in base[5]]
+            case[5][b][at] = pid
+            got = check_bad_page(case, b, in_place=in_place)
+            assert got["kv_lens"][b] == -1 and got["pages_held"][b] == held and got["cache_lens"][b] == base[0][b]
+            assert pid not in got["free_pages"][:got["free_count"]]
+    # what it does not hold is not read
+    case = [list(x) if isinstance(x, list) else x for x in base]
+    case[5] = [list(r) for r in base[5]]
+    case[5][b][held:] = [-2 ** 31] * (len(case[5][b]) - held)
+    assert check(case, in_place=in_place)["bits"] == 0
+
+
+@pytest.mark.gpu
+def test_plan_reports_pages_that_it_takes_without_a_token_on_them():
+    """A sequence that holds fewer pages than its cached tokens take gets the rest without new tokens of its
+    own; an id from outside the pool among them is reported in that step."""
+    for tree in (0, 4):
+        case = [[20, 3], [0, 1], [1, 1], [5, -7, 6, 3] + [-1] * 4, 4, [[0, -1, -1, -1], [1, -1, -1, -1]], 8, 2, [-1] * 2, tree]
+        want = plain_plan(*case)
+        got = run(case)
+        assert want["bits"] == 0 and want["block_table"][0][:3] == [0, 3, 6]  # two taken, both good
+        assert got["bits"] == 0 and got["block_table"] == want["block_table"]
+        for pid in (-7, 8, -2 ** 31):
+            case[3][2] = pid
+            want, got = plain_plan(*case), run(case)
+            assert got.pop("bits") == PAGE
+            want.pop("bits")
+            assert all(got[k] == v for k, v in want.items() if v is not None)
