@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) norm_backward_kernel(
                 s1 = fma(mul(gx[q], ax[q]), x, fma(mul(gy[q], ay[q]), y, s1));
             }
             const float r = rsqrtf(fmaf(row_sum<IPR>(sum(s0)), 1.f / D, p.eps));
-            const float mean = row_sum<IPR>(sum(s1)) * r * (1.f / D);
+            // (a row whose squares overflow has r = 0 and xh = 0, while its sum of a g x may be inf or NaN)
+            const float dot = row_sum<IPR>(sum(s1)), mean = r > 0.f ? dot * r * (1.f / D) : 0.f;
             const F2 rr = f2(r, r), mm = f2(-mean * r, -mean * r);
             F2 ox[N], oy[N];
 #pragma unroll

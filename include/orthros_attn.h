@@ -648,7 +648,8 @@ ORTHROS_API size_t orthros_norm_rotate_backward_workspace_size(int n, int H, int
  * x            the forward's input, always read
  * The other arguments are orthros_rotate_backward's (dx may be dy; without
  * gradients of weight and affine the workspace may be NULL). The sums run in a
- * fixed order: the same call gives the same bits.
+ * fixed order: the same call gives the same bits. A head with xh = 0 for its size
+ * (orthros_norm_rotate) has r = 0, and so dx = 0.
  */
 ORTHROS_API orthros_status orthros_norm_rotate_backward(
     const void *dy, long long dy_stride, const void *x, long long x_stride, const int32_t *positions, const float *weight,

@@ -399,3 +399,35 @@ def test_graph_replay_and_stream_argument():
     got = both(stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,rot", [(64, 32), (128, 128)])
+def test_rows_whose_squares_overflow_have_no_direction(d, rot, dtype, layout):
+    """A head whose sum of squares is past fp32's range has xh = 0: the forward gives its rotated beta, the
+    gradient of x is 0 there, whatever the products of x and dy come to, and no sum takes anything of it."""
+    n, H = 9, 3
+    x, al, be, pos = make(n, H, d, dtype, seed=21)
+    dy = torch.randn(n, H, d, generator=torch.Generator().manual_seed(22)).to(dtype)
+    big = [(2, 1, 1.5e38), (5, 0, 3e30), (7, 2, -2e38)]
+    for i, h, v in big:
+        x[i, h] = v
+        dy[i, h] = 64.0  # v dy is past 3.4e38 for two of them
+    x[7, 2, ::2] = 2e38  # products of both signs
+    steps, w = ola.orthros_rotary_steps(frequencies(rot)), weight(d, 4)
+    kw = dict(layout=layout, alpha=al.cuda())
+    y = ola.orthros_norm_rotate(x.cuda(), pos.cuda(), steps.cuda(), w.cuda(), EPS, beta=be.cuda(), **kw)
+    got = ola.orthros_norm_rotate_backward(dy.cuda(), x.cuda(), pos.cuda(), steps.cuda(), w.cuda(), EPS, **kw)
+    zero = x.clone()
+    for i, h, _ in big:
+        zero[i, h] = 0  # rows whose norm is 0 as well
+        assert not bool(got[0][i, h].any())
+    want = ola.orthros_norm_rotate_backward(dy.cuda(), zero.cuda(), pos.cuda(), steps.cuda(), w.cuda(), EPS, **kw)
+    rows = torch.ones(n, H, dtype=torch.bool)
+    for i, h, _ in big:
+        rows[i, h] = False
+    assert torch.equal(got[0][rows.cuda()], want[0][rows.cuda()])
+    assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    assert torch.equal(y, ola.orthros_norm_rotate(zero.cuda(), pos.cuda(), steps.cuda(), w.cuda(), EPS, beta=be.cuda(), **kw))
