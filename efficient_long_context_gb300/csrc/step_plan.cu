@@ -85,7 +85,9 @@ __device__ __forceinline__ bool foreign_page(const StepPlanParams &p, int b, int
     return foreign;
 }
 
+// (aligned: every thread of a warp at once, which a branch of one lane just before does not leave for certain)
 __device__ __forceinline__ void cluster_arrive_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

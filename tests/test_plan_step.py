@@ -555,3 +555,19 @@ def test_plan_reports_pages_that_it_takes_without_a_token_on_them():
             assert got.pop("bits") == PAGE
             want.pop("bits")
             assert all(got[k] == v for k, v in want.items() if v is not None)
+
+
+def test_warps_are_converged_at_aligned_cluster_barriers(lib):
+    """An aligned barrier is undefined for a warp whose lanes come apart, as behind a branch of one lane: a warp
+    barrier stands directly before each. Read in the source, since a run shows its lack by chance at most."""
+    import pathlib
+    import re
+
+    found = 0
+    for path in sorted((pathlib.Path(ola.__file__).parent / "csrc").glob("*.cu*")):
+        text = path.read_text()
+        for m in re.finditer(r'asm volatile\("barrier\.cluster\.arrive[.a-z]*\.aligned', text):
+            found += 1
+            before = text[:m.start()].rstrip()
+            assert before.endswith("__syncwarp();"), f"{path.name}:{text.count(chr(10), 0, m.start()) + 1}"
+    assert found >= 1
