@@ -49,14 +49,17 @@
 // (relative, measured with independent values), beside 0.0017 of o's own rounding.
 //
 // Bound and measured (GQA 32/8, d = 128): decoding by HBM, 32 sequences over 16K-32K
-// keys in 440 us, 7.2 TB/s, above the rate of a copy, which also writes (one warp for
+// keys in 440-446 us, 7.1-7.2 TB/s, above the rate of a copy, which also writes (one warp for
 // keys and values: 480 us; pages of 16 tokens, whose boxes take twice as long to issue as
-// those of 64: 451 instead of 518); chunks by the softmax that has to run beside the products,
-// 2 x 4000 tokens over 24K keys at 1530-1600 TFLOP/s in bursts (80 % of the measured
-// bf16 rate; 1375-1480 once the power limit lowers the clock), 2048 tokens at window 4096 in
+// those of 64: 451-460 instead of 518); chunks by the softmax that has to run beside the products,
+// 2 x 4000 tokens over 24K keys at 1500-1575 TFLOP/s in bursts (77-81 % of the measured
+// bf16 rate; 1330 once the power limit lowers the clock), 2048 tokens at window 4096 in
 // 111 us, 5 of them the merge. Trees: 32 of 9 to 60 tokens over 4K-20K keys in pages of
-// 16 in 274 us (floor 246: HBM, with the softmax of two row tiles close behind), one of
-// 25 tokens over 32K keys in 37 us (floor 20: 7 us of start, 9 of end).
+// 16 in 277 us (floor 246: HBM, with the softmax of two row tiles close behind; 291-297 once
+// the power limit lowers the clock), at d = 64 in 204 (floor 123: that softmax), one of
+// 25 tokens over 32K keys in 37 us (floor 20: 7 us of start, 9 of end). A tree of more than two
+// row tiles is several units, each of which reads all its keys: the 32 at g = 8 in 457 us (floor
+// 249), up to 30 tokens at g = 16 in 450 (267).
 //
 // Keys outside the sequence's length or before every row's window are never
 // read into a result: their copy boxes are skipped (zero fill), their logits
@@ -225,7 +228,8 @@ __device__ __forceinline__ int new_tokens(const ChunkParams &p, int b, int &tok0
 
 // What a key tile of a unit costs in the count that the CTAs share out. A tree's unit of two row
 // tiles takes longer for each than one of a single row tile, which waits for HBM: 32 trees of 9 to
-// 60 tokens over 12000 keys in 264 us instead of 284 with equal shares of tiles (265 at 4 : 5, 269 at 2 : 3).
+// 60 tokens over 12000 keys in 264 us instead of 284 with equal shares of tiles (265 at 4 : 5, 269 at 2 : 3),
+// over 4K-20K keys in 277 instead of 285 (in a long run 295 instead of 302), at d = 64 in 204 instead of 227.
 template <bool kTree> __device__ __forceinline__ int tile_cost(const ChunkParams &p, int cnt) {
     return !kTree ? 1 : cnt > p.tile_tokens ? kPairCost : kSingleCost;
 }

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kMoveThreads) norm_move_kernel(const RotatePar
 // the thread that takes them, partials of a block added in a fixed order) with both sums of
 // a row, of x^2 and of a g x, taken in one exchange. The weight's gradient is the block's sums per
 // head, weighed by alpha, added over its heads. Bound by HBM: 32768 x 32 x 128 bf16 with all
-// gradients 132 us, 6.1 TB/s (91 %), and 6 us of sum (with alpha read in the loop over the heads
+// gradients 134 us, 6.0 TB/s (90 %), and 6 us of sum (with alpha read in the loop over the heads
 // that summed the weight's gradient the kernel took 8 us longer).
 // ---------------------------------------------------------------------------
 constexpr int kDepth = 6;

@@ -6,9 +6,10 @@
 // Plan. With L_b cached and m_b new tokens, sequence b needs ceil((L_b + m_b) / P)
 // pages; what it lacks it takes from the top of the free stack, the sequences in
 // order, so that its share is an exclusive prefix sum of the lacks. Ended
-// sequences (m_b = -1) push theirs before, if all their ids are the pool's. A token's sequence is found by a binary
-// search in the prefix sums of m_b, its page in the table or, if it is a new one,
-// on the stack: no thread waits for another's table entry.
+// sequences (m_b = -1) push theirs before, if all their ids are the pool's. A
+// token's sequence is found by a binary search in the prefix sums of m_b, its page
+// in the table or, if it is a new one, on the stack: no thread waits for another's
+// table entry.
 //
 // One launch of one cluster: every CTA computes all prefix sums in shared memory
 // (a few microseconds of loads whatever the CTAs), then a cluster barrier stands
@@ -284,11 +285,13 @@ template <int kWords> __global__ void __launch_bounds__(kThreads) step_plan_kern
 // layer's keys and values. The path ascends (acc[i] >= i), so a thread that owns 16 bytes of
 // the rows may move them in order, kMoves loads in flight before their stores: what a store
 // overwrites has been read. A block takes a sequence in one layer or a few,
-// its moves laid end to end; blocks past the sequences check all paths and write the status word, as
+// its moves laid end to end; one block past the sequences checks all paths and writes the status word, as
 // the moving blocks of the first layer write the lengths. Bound by latency: lengths, path, pages and
-// rows are four loads that wait for one another. One layer of 32 sequences: 3.1 us; 48 sequences
-// in 32 layers (44 MB read and written): 10.7 us, 61 % of the copy rate, with eight moves in flight
-// instead of four 11.6 (registers: three blocks an SM).
+// rows are four loads that wait for one another. One layer of 32 sequences: 3.4 us; 48 sequences
+// in 32 layers (44 MB read and written): 11 us, 60 % of the copy rate, with eight moves in flight
+// instead of four 0.9 us more (registers: three blocks an SM). With many places to check (sequences
+// times `most`) the status block is the last to end, 256 places a turn: 500 sequences with most = 8
+// take 18 us, with most = 64 110 us.
 // ---------------------------------------------------------------------------
 constexpr int kCommitThreads = 256, kMoves = 4;
 
@@ -410,7 +413,7 @@ cudaError_t launch_step_plan(const StepPlanParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_tree_commit(TreeCommitParams p, cudaStream_t stream) {
-    // eight blocks an SM, five of which run at once (48 sequences x 32 layers: 10.7 us; five an SM 11.8)
+    // eight blocks an SM, five of which run at once (five an SM: 48 sequences x 32 layers 1.1 us longer)
     const int fit = 8 * device_sm_count();
     p.layers_per_block = (int)(((long long)p.layers * p.B + fit - 1) / fit);
     if (p.layers_per_block > p.layers) p.layers_per_block = p.layers;

@@ -586,7 +586,9 @@ ORTHROS_API size_t orthros_chunk_attention_workspace_size(int B, int n, int max_
  *              before)
  * q_indptr     [B+1] int32 DEVICE, 0 .. n, non-decreasing
  * kv_lens      [B] int32 DEVICE: cached tokens, the new ones included
- * max_new      upper bound of the n_b (sizes the workspace; n always serves)
+ * max_new      upper bound of the n_b (sizes the workspace; n always serves). The
+ *              order in which the parts of a row are joined goes by it: the same
+ *              call gives the same bits, one with another bound may round otherwise
  * k_cache, v_cache [num_pages, page_size, Hkv, d], block_table [B, max_pages]
  *              DEVICE int32; any page_size (multiples of 8 are copied by TMA,
  *              others row by row, slower)
@@ -700,6 +702,9 @@ ORTHROS_API orthros_status orthros_norm_rotate_append(
  * block_table  [B, max_pages]: entries of new pages are written, others left
  * n            rows of the token arrays; rows behind the last new token are
  *              padding: token_seq -1, token_pos 0, token_slots -1, no mask bits
+ *              (rows to spare are for orthros_tree_attention; consecutive tokens whose
+ *              number varies, up to 256 a sequence, are trees in which every token's
+ *              parent is the one before it)
  * parents      [n] with max_tree > 0 (at most 256): the new tokens of every
  *              sequence are a drafted tree of at most max_tree tokens, and
  *              parents[i] is the number within its tree (0, 1, ...) of token i's
